@@ -520,6 +520,157 @@ typedef struct zero1_sm_partition {
 int zero1_sm_partition_create(int sms_a, zero1_sm_partition *out);
 int zero1_sm_partition_destroy(zero1_sm_partition *part);
 
+/* ---------------------------------------------------------------- matrices
+ *
+ * A step for the parameters that are matrices, beside AdamW for the others:
+ * the momentum of the averaged gradient, orthogonalised, is the update.
+ *
+ * A matrix of the flat buffers every entry point of this header steps:
+ * entry (r, c) at offset + r*ld + c.  Column slices of one larger matrix
+ * (the query, key and value parts of a fused projection, say) are matrices
+ * of their own with one ld. */
+typedef struct zero1_matrix {
+    uint64_t offset;
+    uint64_t ld;
+    uint32_t rows;
+    uint32_t cols;
+} zero1_matrix;
+
+/* How far a step moves a matrix, as a multiple of its orthogonalised update
+ * (whose singular values are near one):
+ *   RMS:      update_scale * sqrt(max(rows, cols)): entries of a root mean
+ *             square of about update_scale whatever the shape (0.2 is that of
+ *             an AdamW update, so its learning rate carries over);
+ *   SPECTRAL: update_scale * sqrt(max(1, rows/cols)). */
+#define ZERO1_MUON_SCALE_RMS      0
+#define ZERO1_MUON_SCALE_SPECTRAL 1
+
+/* Hyperparameters of the matrix step.
+ *   lr >= 0, momentum in [0, 1), weight_decay >= 0, update_scale >= 0;
+ *   nesterov 1: the update looks one momentum step ahead; scale_rule above;
+ *   eps >= 1e-15 is added to the update's Frobenius norm;
+ *   ns_steps in [1, 32] iterations X <- ns_a X + (ns_b A + ns_c A A) X with
+ *     A = X X^T (of the smaller side).  The coefficients (at most 8 in
+ *     magnitude) must keep every iterate's singular values below 2, as
+ *     (3.4445, -4.7750, 2.0315) does: entries are held in f16 parts scaled
+ *     by 4096, and beyond that range results are infinite or NaN.
+ *   size: sizeof(zero1_muon_hparams) (lets the struct grow). */
+typedef struct zero1_muon_hparams {
+    uint32_t size;
+    int32_t nesterov;
+    int32_t scale_rule;
+    int32_t ns_steps;
+    double lr;
+    double momentum;
+    double weight_decay;
+    double eps;
+    double update_scale;
+    double ns_a;
+    double ns_b;
+    double ns_c;
+} zero1_muon_hparams;
+
+typedef struct zero1_muon_ctx *zero1_muon_handle;
+
+/* Plan the step of `count` matrices (at most 65,536) of flat buffers of n
+ * entries over `world` emulated ranks, and allocate its workspace on the
+ * current device with cudaMalloc: 8 bytes an entry (rows padded to 64
+ * entries) and 8 bytes an entry of the Gram matrices.  `mats` is copied.
+ * Matrices may be given in any order; no two may share an entry, and two
+ * whose extents interleave must have one ld.  Sides are 1 to 2^22.
+ * Errors: ZERO1_EINVAL (before any device call), ZERO1_ENODEV,
+ * ZERO1_ENOMEM, ZERO1_ECUDA.  On error *out is NULL. */
+int zero1_muon_create(uint64_t n, int world, const zero1_matrix *mats, uint64_t count,
+                      const zero1_muon_hparams *hp, zero1_muon_handle *out);
+
+/* Free the handle and its workspace after synchronizing the device.  NULL is
+ * accepted and ignored.  Returns ZERO1_OK, ZERO1_EINVAL or ZERO1_ECUDA. */
+int zero1_muon_destroy(zero1_muon_handle h);
+
+/* One data-parallel step of the matrices, asynchronous and allocation-free.
+ * For each matrix, with G the rank-ordered fp32 sum of the W bf16 gradients
+ * times 1/W and mu the momentum:
+ *     M = mu M + (1-mu) G
+ *     U = mu M + (1-mu) G (nesterov) or M
+ *     X = U / (|U| + eps), iterated (zero1_muon_hparams)
+ *     master = master (1 - lr weight_decay) - lr scale X
+ *     every replica = bf16(master)
+ *   grad_ptrs, param_ptrs: host arrays of W device pointers to bf16 buffers
+ *     of n entries, as zero1_step;
+ *   master, momentum: the caller's fp32 device buffers of n entries, updated
+ *     in place (momentum = 0 before the first step); they are the whole
+ *     state, so a checkpoint is these two.
+ * All buffers 16-byte aligned; entries outside the matrices are neither read
+ * nor written.  The products run as three f16 products with fp32
+ * accumulators (each factor in a high and a low part), as exact as fp32.
+ * A matrix of zeros is moved by its decay alone.  A gradient with an
+ * infinity or a NaN makes its own matrix NaN, and no other.  Deterministic:
+ * the same inputs give the same bits.
+ * Errors: ZERO1_EINVAL, ZERO1_EALIGN, ZERO1_ECUDA. */
+int zero1_muon_step(zero1_muon_handle h, const void *const *grad_ptrs, void *const *param_ptrs, float *master,
+                    float *momentum, void *stream);
+
+/* The orthogonalisation alone: out = the iterated X of every matrix of the
+ * flat buffer `in` (n entries each, ZERO1_DTYPE_BF16 or ZERO1_DTYPE_F32,
+ * 16-byte aligned; out may be in when the types are equal).  Entries of out
+ * outside the matrices keep their values.  Asynchronous, allocation-free.
+ * Errors: ZERO1_EINVAL, ZERO1_EALIGN, ZERO1_ECUDA. */
+int zero1_muon_orthogonalize(zero1_muon_handle h, const void *in, int in_dtype, void *out, int out_dtype,
+                             void *stream);
+
+/* The learning rate of later steps.  Errors: ZERO1_EINVAL. */
+int zero1_muon_set_lr(zero1_muon_handle h, double lr);
+
+/* Wait for `stream` and report whether a kernel wait of this handle ever gave
+ * up (each is bounded to 1 s, so that a fault cannot hang the GPU):
+ * ZERO1_ECUDA then, for the rest of the handle's life; results since are not
+ * valid.  Errors: ZERO1_EINVAL, ZERO1_ECUDA. */
+int zero1_muon_status(zero1_muon_handle h, void *stream);
+
+/* Entries of all matrices, and the bytes of device memory the handle holds.
+ * Either output may be NULL.  Errors: ZERO1_EINVAL. */
+int zero1_muon_layout(zero1_muon_handle h, uint64_t *entries, uint64_t *device_bytes);
+
+/* ------------------------------------------------------------ layer norm
+ *
+ * Layer normalisation of `rows` rows of `cols` entries, whose weight and
+ * bias are vectors of the flat parameter buffers and whose gradients for
+ * them go straight into a flat gradient buffer.  x, y, dy, dx, gamma and
+ * beta are of one type (ZERO1_DTYPE_BF16 or ZERO1_DTYPE_F32); rows start
+ * ldx, ldy, lddy, lddx entries apart (>= cols).  Buffers need the alignment
+ * of their elements only (16-byte aligned rows of whole 16-byte pieces are
+ * faster).  Sums and statistics are fp32.  Sizes: rows < 2^31, cols 1 to
+ * 2^24.  Asynchronous on `stream`; allocates nothing.
+ *
+ * Forward: with mean and var of each row (var over cols, not cols - 1) and
+ * rstd = 1/sqrt(var + eps),
+ *     y = (x - mean) * rstd * gamma + beta.
+ *   beta may be NULL (no bias); mean and rstd (fp32, one a row) are written
+ *   for the backward pass; y may be x.  rows = 0 does nothing.
+ * Errors: ZERO1_EINVAL, ZERO1_EALIGN, ZERO1_ECUDA. */
+int zero1_layernorm_forward(uint64_t rows, uint64_t cols, int dtype, const void *x, uint64_t ldx,
+                            const void *gamma, const void *beta, double eps, void *y, uint64_t ldy, float *mean,
+                            float *rstd, void *stream);
+
+/* Host-only: the bytes of workspace zero1_layernorm_backward needs for this
+ * size (partial column sums of at most 320 blocks).  Errors: ZERO1_EINVAL. */
+int zero1_layernorm_workspace(uint64_t rows, uint64_t cols, uint64_t *bytes);
+
+/* Backward: with h = (x - mean) * rstd and g = dy * gamma,
+ *     dx = rstd * (g - mean(g) - h * mean(g * h)),
+ *     dgamma = sum over rows of dy * h,  dbeta = sum over rows of dy.
+ *   dgamma, dbeta: cols entries of grad_dtype (bf16 or fp32), overwritten;
+ *   dbeta may be NULL; dx may be dy (with lddx == lddy).  The column sums
+ *   are added in a fixed order, so the same inputs give the same bits.
+ *   workspace: device memory of at least zero1_layernorm_workspace bytes,
+ *   16-byte aligned, used by one call at a time; its contents need not be
+ *   kept.  rows = 0 writes zeros to dgamma and dbeta.
+ * Errors: ZERO1_EINVAL, ZERO1_EALIGN, ZERO1_ECUDA. */
+int zero1_layernorm_backward(uint64_t rows, uint64_t cols, int dtype, const void *dy, uint64_t lddy,
+                             const void *x, uint64_t ldx, const void *gamma, const float *mean,
+                             const float *rstd, void *dx, uint64_t lddx, void *dgamma, void *dbeta,
+                             int grad_dtype, void *workspace, uint64_t workspace_bytes, void *stream);
+
 /* Message for the last error on this thread ("" if none). */
 const char *zero1_last_error(void);
 

@@ -25,6 +25,9 @@ __all__ = [
     "zero1_set_lr", "zero1_set_lr_ptr", "zero1_get_grad_norm",
     "zero1_layout", "zero1_bucket_begin", "zero1_bucket_reduce", "zero1_bucket_update", "zero1_bucket_finish", "zero1_profile_start", "zero1_profile_stop", "zero1_profile_read", "zero1_step_launches", "zero1_shard_plan", "zero1_step_scalars", "zero1_step_noalloc", "zero1_allreduce", "zero1_allreduce_sum", "zero1_allgather", "zero1_last_error",
     "SmPartition", "zero1_sm_partition_create", "zero1_sm_partition_destroy",
+    "MuonHparams", "Muon", "zero1_muon_create", "zero1_muon_destroy", "zero1_muon_step", "zero1_muon_orthogonalize",
+    "zero1_muon_set_lr", "zero1_muon_status", "zero1_muon_layout",
+    "zero1_layernorm_forward", "zero1_layernorm_backward", "zero1_layernorm_workspace",
     "library_path", "EXPORTED_SYMBOLS",
 ]
 
@@ -68,6 +71,17 @@ _SIGS = {
     "zero1_allgather": (_I32, [_U64, _I32, _U64, _I32, _P, _P, _P, _P]),
     "zero1_sm_partition_create": (_I32, [_I32, _P]),
     "zero1_sm_partition_destroy": (_I32, [_P]),
+    "zero1_muon_create": (_I32, [_U64, _I32, _P, _U64, _P, _P]),
+    "zero1_muon_destroy": (_I32, [_P]),
+    "zero1_muon_step": (_I32, [_P, _P, _P, _P, _P, _P]),
+    "zero1_muon_orthogonalize": (_I32, [_P, _P, _I32, _P, _I32, _P]),
+    "zero1_muon_set_lr": (_I32, [_P, _F64]),
+    "zero1_muon_status": (_I32, [_P, _P]),
+    "zero1_muon_layout": (_I32, [_P, _P, _P]),
+    "zero1_layernorm_forward": (_I32, [_U64, _U64, _I32, _P, _U64, _P, _P, _F64, _P, _U64, _P, _P, _P]),
+    "zero1_layernorm_workspace": (_I32, [_U64, _U64, _P]),
+    "zero1_layernorm_backward": (_I32, [_U64, _U64, _I32, _P, _U64, _P, _U64, _P, _P, _P, _P, _U64, _P, _P, _I32, _P,
+                                        _U64, _P]),
     "zero1_last_error": (C.c_char_p, []),
 }
 EXPORTED_SYMBOLS = tuple(_SIGS)
@@ -202,6 +216,15 @@ class PtrTable:
 # Element kinds a C entry point expects behind a pointer: torch dtype name
 # and element size in bytes.
 _KINDS = {"bf16": ("torch.bfloat16", 2), "f32": ("torch.float32", 4)}
+_DTYPE_NAMES: dict = {}    # torch dtype -> its name (naming one takes longer than the other checks together)
+
+
+def _dtype_name(x) -> str:
+    d = x.dtype
+    name = _DTYPE_NAMES.get(d)
+    if name is None:
+        name = _DTYPE_NAMES[d] = str(d)
+    return name
 
 
 def _check_buffer(x, count: int, kind: str, on_device: bool | None, what: str) -> None:
@@ -213,7 +236,7 @@ def _check_buffer(x, count: int, kind: str, on_device: bool | None, what: str) -
         return
     want, size = _KINDS[kind]
     if hasattr(x, "data_ptr") and hasattr(x, "numel"):          # torch tensor
-        if str(x.dtype) != want:
+        if _dtype_name(x) != want:
             raise Zero1ArgumentError(f"{what}: expected {want}, got {x.dtype}")
         if on_device is not None and bool(x.is_cuda) != on_device:
             raise Zero1ArgumentError(f"{what}: expected a {'CUDA' if on_device else 'host'} tensor, got {x.device}")
@@ -484,6 +507,229 @@ def zero1_allgather(n: int, world: int, shard_len: int, dtype: int, shard_ptrs, 
                 _check_buffer(x, own, kind, True, f"shards[{r}]")
     _check(_load().zero1_allgather(n, world, shard_len, dtype, shards, _ptrs(out_ptrs, world, n, kind, True, "out"),
                                    _addr(errors), _stream(stream)))
+
+
+# --------------------------------------------------------- matrices
+
+SCALE_RMS, SCALE_SPECTRAL = 0, 1
+
+
+class _CMatrix(C.Structure):
+    _fields_ = [("offset", C.c_uint64), ("ld", C.c_uint64), ("rows", C.c_uint32), ("cols", C.c_uint32)]
+
+
+class _CMuonHparams(C.Structure):
+    _fields_ = [("size", C.c_uint32), ("nesterov", C.c_int32), ("scale_rule", C.c_int32), ("ns_steps", C.c_int32),
+                ("lr", C.c_double), ("momentum", C.c_double), ("weight_decay", C.c_double), ("eps", C.c_double),
+                ("update_scale", C.c_double), ("ns_a", C.c_double), ("ns_b", C.c_double), ("ns_c", C.c_double)]
+
+
+@dataclass
+class MuonHparams:
+    """Hyperparameters of the matrix step (zero1_muon_hparams)."""
+    lr: float = 1e-3
+    momentum: float = 0.95
+    weight_decay: float = 0.1
+    eps: float = 1e-7
+    update_scale: float = 0.2
+    nesterov: bool = True
+    scale_rule: int = SCALE_RMS
+    ns_steps: int = 5
+    ns_a: float = 3.4445
+    ns_b: float = -4.7750
+    ns_c: float = 2.0315
+
+    def _c(self) -> _CMuonHparams:
+        return _CMuonHparams(C.sizeof(_CMuonHparams), int(self.nesterov), self.scale_rule, self.ns_steps, self.lr,
+                             self.momentum, self.weight_decay, self.eps, self.update_scale, self.ns_a, self.ns_b,
+                             self.ns_c)
+
+
+# (n, world) of every matrix handle this binding created.
+_MUON_HANDLES: dict[int, tuple[int, int]] = {}
+
+
+def _muon_info(h) -> tuple[int | None, int | None]:
+    return _MUON_HANDLES.get(h, (None, None))
+
+
+def zero1_muon_create(n: int, world: int, matrices, hp: MuonHparams | None = None) -> int:
+    """Create a matrix handle; `matrices` holds (offset, rows, cols) or
+    (offset, rows, cols, ld) tuples."""
+    mats = [tuple(int(v) for v in m) for m in matrices]
+    for i, m in enumerate(mats):
+        if len(m) not in (3, 4):
+            raise Zero1ArgumentError(f"matrices[{i}]: expected (offset, rows, cols[, ld]), got {m}")
+        if any(v < 0 for v in m) or m[1] >= 1 << 32 or m[2] >= 1 << 32 or any(v >= 1 << 63 for v in m):
+            raise Zero1ArgumentError(f"matrices[{i}]: {m} is out of range")
+    table = (_CMatrix * max(1, len(mats)))(*[_CMatrix(m[0], m[3] if len(m) == 4 else m[2], m[1], m[2]) for m in mats])
+    h = C.c_void_p()
+    c = (hp or MuonHparams())._c()
+    _check(_load().zero1_muon_create(n, world, table, len(mats), C.byref(c), C.byref(h)))
+    _MUON_HANDLES[h.value] = (n, world)
+    return h.value
+
+
+def zero1_muon_destroy(h: int | None) -> None:
+    _check(_load().zero1_muon_destroy(h))
+    _MUON_HANDLES.pop(h, None)
+
+
+def zero1_muon_step(h: int, grad_ptrs, param_ptrs, master, momentum, stream=None) -> None:
+    """One step of the handle's matrices; master and momentum (fp32) are the
+    caller's and are updated in place."""
+    n, world = _muon_info(h)
+    if n is not None:
+        _check_buffer(master, n, "f32", True, "master")
+        _check_buffer(momentum, n, "f32", True, "momentum")
+    _check(_load().zero1_muon_step(h, _ptrs(grad_ptrs, world, n, "bf16", True, "grads"),
+                                   _ptrs(param_ptrs, world, n, "bf16", True, "params"), _addr(master),
+                                   _addr(momentum), _stream(stream)))
+
+
+_KIND_OF = {DTYPE_BF16: "bf16", DTYPE_F32: "f32"}
+
+
+def zero1_muon_orthogonalize(h: int, src, src_dtype: int, dst, dst_dtype: int, stream=None) -> None:
+    """dst = the orthogonalised matrices of the flat buffer src."""
+    n = _muon_info(h)[0]
+    if n is not None:
+        for x, dtype, what in ((src, src_dtype, "src"), (dst, dst_dtype, "dst")):
+            if dtype in _KIND_OF:
+                _check_buffer(x, n, _KIND_OF[dtype], True, what)
+    _check(_load().zero1_muon_orthogonalize(h, _addr(src), src_dtype, _addr(dst), dst_dtype, _stream(stream)))
+
+
+def zero1_muon_set_lr(h: int, lr: float) -> None:
+    _check(_load().zero1_muon_set_lr(h, lr))
+
+
+def zero1_muon_status(h: int, stream=None) -> None:
+    """Wait for the stream; raise if a kernel wait of this handle ever gave up."""
+    _check(_load().zero1_muon_status(h, _stream(stream)))
+
+
+def zero1_muon_layout(h: int) -> tuple[int, int]:
+    """(entries of all matrices, device bytes the handle holds)."""
+    e, b = C.c_uint64(), C.c_uint64()
+    _check(_load().zero1_muon_layout(h, C.byref(e), C.byref(b)))
+    return e.value, b.value
+
+
+def _dtype_of(x, what: str) -> int:
+    code = {"torch.bfloat16": DTYPE_BF16, "torch.float32": DTYPE_F32}.get(_dtype_name(x) if hasattr(x, "dtype") else "")
+    if code is None:
+        raise Zero1ArgumentError(f"{what}: expected a bf16 or fp32 tensor, got {getattr(x, 'dtype', type(x).__name__)}")
+    return code
+
+
+class Muon:
+    """Owning wrapper around a matrix handle (closes on ``close()`` / context exit)."""
+
+    def __init__(self, n: int, world: int, matrices, hp: MuonHparams | None = None):
+        self.handle = None
+        self.n, self.world, self.hp = n, world, hp or MuonHparams()
+        self.handle = zero1_muon_create(n, world, matrices, self.hp)
+
+    def step(self, grads, params, master, momentum, stream=None) -> None:
+        zero1_muon_step(self.handle, grads, params, master, momentum, stream)
+
+    def orthogonalize(self, src, dst, stream=None) -> None:
+        """bf16 or fp32 tensors of n entries; the types may differ."""
+        zero1_muon_orthogonalize(self.handle, src, _dtype_of(src, "src"), dst, _dtype_of(dst, "dst"), stream)
+
+    def set_lr(self, lr: float) -> None:
+        zero1_muon_set_lr(self.handle, lr)
+
+    def status(self, stream=None) -> None:
+        zero1_muon_status(self.handle, stream)
+
+    def layout(self) -> tuple[int, int]:
+        return zero1_muon_layout(self.handle)
+
+    def close(self) -> None:
+        if self.handle is not None:
+            zero1_muon_destroy(self.handle)
+            self.handle = None
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+# --------------------------------------------------------- layer norm
+
+def _check_rows(x, rows: int, cols: int, ld: int, dtype: int, what: str) -> None:
+    """Raise Zero1ArgumentError unless the torch tensor `x` is CUDA memory of
+    the type and, where it describes rows itself, lies as (rows, cols, ld) say
+    and reaches as far as the call reads or writes.  Raw addresses pass."""
+    if x is None or isinstance(x, int) or not hasattr(x, "data_ptr"):
+        return
+    want = _KINDS[_KIND_OF[dtype]][0] if dtype in _KIND_OF else None
+    if want is not None and _dtype_name(x) != want:
+        raise Zero1ArgumentError(f"{what}: expected {want}, got {x.dtype}")
+    if not x.is_cuda:
+        raise Zero1ArgumentError(f"{what}: expected a CUDA tensor, got {x.device}")
+    shape = x.shape
+    if len(shape) == 2 and shape[0] == rows and shape[1] == cols and x.stride() == (ld, 1) or rows == 0:
+        return
+    if len(shape) > 1 and x.stride(-1) != 1 and shape[-1] > 1:
+        raise Zero1ArgumentError(f"{what}: the entries of a row must be adjacent")
+    held = x.untyped_storage().nbytes() // x.element_size() - x.storage_offset()
+    if held < (rows - 1) * ld + cols:
+        raise Zero1ArgumentError(f"{what}: its memory holds {held} elements, the call reads or writes "
+                                 f"{(rows - 1) * ld + cols}")
+
+
+def zero1_layernorm_forward(rows: int, cols: int, dtype: int, x, ldx: int, gamma, beta, eps: float, y, ldy: int,
+                            mean, rstd, stream=None) -> None:
+    """y = layer norm of x; mean and rstd (fp32, one a row) for the backward pass."""
+    _check_rows(x, rows, cols, ldx, dtype, "x")
+    _check_rows(y, rows, cols, ldy, dtype, "y")
+    if dtype in _KIND_OF:
+        _check_buffer(gamma, cols, _KIND_OF[dtype], True, "gamma")
+        _check_buffer(beta, cols, _KIND_OF[dtype], True, "beta")
+    _check_buffer(mean, rows, "f32", True, "mean")
+    _check_buffer(rstd, rows, "f32", True, "rstd")
+    _check(_load().zero1_layernorm_forward(rows, cols, dtype, _addr(x), ldx, _addr(gamma), _addr(beta), eps, _addr(y),
+                                           ldy, _addr(mean), _addr(rstd), _stream(stream)))
+
+
+def zero1_layernorm_workspace(rows: int, cols: int) -> int:
+    """Bytes of workspace the backward pass needs (host only, no device)."""
+    b = C.c_uint64()
+    _check(_load().zero1_layernorm_workspace(rows, cols, C.byref(b)))
+    return b.value
+
+
+def zero1_layernorm_backward(rows: int, cols: int, dtype: int, dy, lddy: int, x, ldx: int, gamma, mean, rstd, dx,
+                             lddx: int, dgamma, dbeta, grad_dtype: int, workspace, stream=None) -> None:
+    """dx, and the weight's and bias's gradients summed over all rows (bf16 or
+    fp32); `workspace` is a CUDA tensor of at least zero1_layernorm_workspace
+    bytes."""
+    for t, ld, what in ((dy, lddy, "dy"), (x, ldx, "x"), (dx, lddx, "dx")):
+        _check_rows(t, rows, cols, ld, dtype, what)
+    if dtype in _KIND_OF:
+        _check_buffer(gamma, cols, _KIND_OF[dtype], True, "gamma")
+    if grad_dtype in _KIND_OF:
+        _check_buffer(dgamma, cols, _KIND_OF[grad_dtype], True, "dgamma")
+        _check_buffer(dbeta, cols, _KIND_OF[grad_dtype], True, "dbeta")
+    _check_buffer(mean, rows, "f32", True, "mean")
+    _check_buffer(rstd, rows, "f32", True, "rstd")
+    if not hasattr(workspace, "numel") or not workspace.is_cuda or not workspace.is_contiguous():
+        raise Zero1ArgumentError("workspace: expected a contiguous CUDA tensor")
+    _check(_load().zero1_layernorm_backward(rows, cols, dtype, _addr(dy), lddy, _addr(x), ldx, _addr(gamma),
+                                            _addr(mean), _addr(rstd), _addr(dx), lddx, _addr(dgamma), _addr(dbeta),
+                                            grad_dtype, _addr(workspace),
+                                            workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
 class _CSmPartition(C.Structure):

@@ -1,6 +1,6 @@
 """Build ``libzero1.so`` in-tree with nvcc for sm_103a.
 
-Two translation units (host ABI, kernels) compile in parallel, then link into
+The translation units of ``SOURCES`` compile in parallel, then link into
 one shared library next to this file.  Rebuilds only when a source or header
 is newer than the library.  ``python -m zero_sharded_adamw_gb300._build``
 builds from the command line; ``-v`` prints ptxas register/spill lines.
@@ -18,8 +18,10 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libzero1.so")
-SOURCES = ["zero1_host.cu", "zero1_kernels.cu", "zero1_noalloc.cu", "zero1_allreduce.cu", "zero1_partition.cu"]
+SOURCES = ["zero1_host.cu", "zero1_kernels.cu", "zero1_noalloc.cu", "zero1_allreduce.cu", "zero1_partition.cu",
+           "zero1_muon.cu", "zero1_muon_kernels.cu", "zero1_layernorm.cu"]
 HEADERS = [os.path.join(CSRC, "zero1_internal.h"), os.path.join(CSRC, "zero1_ptx.cuh"), os.path.join(CSRC, "zero1_policy.h"),
+           os.path.join(CSRC, "zero1_muon.h"), os.path.join(CSRC, "zero1_tc.cuh"),
            os.path.join(INCLUDE, "zero1.h")]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")

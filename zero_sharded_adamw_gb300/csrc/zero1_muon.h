@@ -1,0 +1,77 @@
+// zero1_muon.h -- declarations shared by the matrix optimizer's host code
+// (zero1_muon.cu) and its kernels (zero1_muon_kernels.cu).  Not installed.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>   // CUtensorMap
+#include <cuda_runtime.h>
+
+#include "zero1.h"
+
+namespace zero1 {
+
+// Output tile of the matrix products: 256 rows (128 in each block of a pair)
+// by 128 columns.
+constexpr int kNsTileM = 256;
+constexpr int kNsTileN = 128;
+constexpr int kNsParts = 4;            // arrivals a finished tile makes: two halves in each block
+constexpr int kNsTileK = 64;           // K of one pipeline stage
+constexpr uint32_t kChunk = 16384;     // entries of one elementwise block
+constexpr uint32_t kMaxSide = 1u << 22;
+// Powers of two the f16 operands are scaled by: every iterate has entries
+// below 2 in magnitude and the Gram matrices below 4, so 4096 keeps them
+// under f16's 65,504 and keeps entries down to 1.5e-8 in its normal range.
+constexpr float kNsScale = 4096.0f;
+
+// One matrix of the plan, in device memory.  X (rows x cols) lives in one
+// half of a two-region ping-pong; a region holds either two f16 planes (the
+// high and the low part of S*X) or one fp32 array, each row padded to ldx.
+struct MuonMat {
+    uint64_t offset, ld;       // place in the flat buffers: entry (r, c) at offset + r*ld + c
+    uint32_t rows, cols;
+    uint32_t s;                // the smaller side: the Gram matrix is s x s
+    uint32_t tall;             // rows > cols: Gram matrix X^T X, update X B
+    uint32_t ldx, lds;         // padded row lengths of X and of the Gram matrices
+    unsigned char *region[2];
+    unsigned char *gram, *poly;   // A and B = b A + c A A: two f16 planes each
+    uint64_t xplane, splane;   // entries of one plane
+    uint32_t parts[3];         // arrivals of the three products of one iteration: tiles x kNsParts
+    uint32_t chunk0, chunks;   // elementwise blocks [chunk0, chunk0 + chunks)
+    uint32_t vec;              // rows start and advance in multiples of 8 entries in the flat buffers
+    float scale;               // update_scale times the side factor
+};
+
+// Tensor maps of one matrix: X in region 0 and 1, A, B, and the fp32 result.
+enum { kMapX0 = 0, kMapX1 = 1, kMapA = 2, kMapB = 3, kMapOut = 4, kMapsPerMat = 5 };
+
+// The plan and the workspace of one handle, in device memory.
+struct MuonDev {
+    const MuonMat *mats;
+    const CUtensorMap *maps;
+    const uint2 *work;         // one iteration's tiles: x = matrix | phase << 30, y = row tile | column tile << 16
+    const uint32_t *chunk_mat; // matrix of each elementwise block
+    double *partials;          // one sum of squares a block
+    unsigned *done;            // arrivals of finished tiles, one counter a matrix
+    unsigned *ticket;
+    unsigned *errors;          // sticky: bit 0 = a wait gave up
+    uint32_t count, nchunks, work_per_iter;
+};
+
+struct MuonScalars {
+    float inv_w, momentum, one_minus_momentum, eps;
+    float lr, decay;           // decay = 1 - lr * weight_decay
+    float a, b, c;
+    int nesterov, steps;
+};
+
+cudaError_t launch_muon_momentum(const MuonDev &d, const MuonScalars &sc, const void *const *grads, int world,
+                                 float *momentum, cudaStream_t stream);
+cudaError_t launch_muon_norm(const MuonDev &d, const void *in, bool bf16, cudaStream_t stream);
+// `in` null: the fp32 update that launch_muon_momentum left in region 1.
+cudaError_t launch_muon_split(const MuonDev &d, const MuonScalars &sc, const void *in, bool bf16, cudaStream_t stream);
+cudaError_t launch_muon_iterate(const MuonDev &d, const MuonScalars &sc, int num_sms, cudaStream_t stream);
+cudaError_t launch_muon_apply(const MuonDev &d, const MuonScalars &sc, void *const *params, int world, float *master,
+                              cudaStream_t stream);
+cudaError_t launch_muon_out(const MuonDev &d, const MuonScalars &sc, void *out, bool bf16, cudaStream_t stream);
+
+}  // namespace zero1

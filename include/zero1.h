@@ -551,9 +551,10 @@ typedef struct zero1_matrix {
  *   eps >= 1e-15 is added to the update's Frobenius norm;
  *   ns_steps in [1, 32] iterations X <- ns_a X + (ns_b A + ns_c A A) X with
  *     A = X X^T (of the smaller side).  The coefficients (at most 8 in
- *     magnitude) must keep every iterate's singular values below 2, as
- *     (3.4445, -4.7750, 2.0315) does: entries are held in f16 parts scaled
- *     by 4096, and beyond that range results are infinite or NaN.
+ *     magnitude, ns_c not 0 and |ns_b| <= 8 |ns_c|) must keep every
+ *     iterate's singular values below 2, as (3.4445, -4.7750, 2.0315) does:
+ *     entries are held in f16 parts scaled by 4096, and beyond that range
+ *     results are infinite or NaN.
  *   size: sizeof(zero1_muon_hparams) (lets the struct grow). */
 typedef struct zero1_muon_hparams {
     uint32_t size;

@@ -25,7 +25,9 @@ struct zero1_muon_ctx {
     void *block = nullptr;        // one cudaMalloc holding the plan and the workspace
     uint64_t block_bytes = 0;
     uint64_t entries = 0;         // of all matrices
-    zero1::MuonDev dev{};
+    zero1::MuonDev dev{};         // what the large matrices need: empty plan if there are none
+    zero1::MuonSmall small{};
+    bool any_small = false;
 };
 
 namespace {
@@ -91,6 +93,9 @@ int check_hparams(const zero1_muon_hparams *hp)
     if (!std::isfinite(hp->ns_a) || !std::isfinite(hp->ns_b) || !std::isfinite(hp->ns_c) ||
         std::fabs(hp->ns_a) > 8.0 || std::fabs(hp->ns_b) > 8.0 || std::fabs(hp->ns_c) > 8.0)
         return mfail(ZERO1_EINVAL, "ns_a, ns_b and ns_c must be finite and at most 8 in magnitude");
+    // A (A + (b/c) I) is what the tensor cores form: b/c has to fit beside A in f16
+    if (std::fabs(hp->ns_b) > 8.0 * std::fabs(hp->ns_c) || hp->ns_c == 0.0)
+        return mfail(ZERO1_EINVAL, "ns_c must not be 0, and |ns_b| at most 8 |ns_c|");
     return ZERO1_OK;
 }
 
@@ -155,16 +160,6 @@ EncodeFn encoder()
     return reinterpret_cast<EncodeFn>(f);
 }
 
-// fp32 rows x cols, rows padded to ld: boxes of 32 x 64, 128-byte swizzle.
-bool encode_out(EncodeFn fn, CUtensorMap *map, void *base, uint64_t rows, uint64_t cols, uint64_t ld)
-{
-    const cuuint64_t dims[3] = {cols, rows, 1}, strides[2] = {ld * 4, ld * rows * 4};
-    const cuuint32_t box[3] = {32, 64, 1}, unit[3] = {1, 1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // Two f16 planes of rows x cols, rows padded to ld: boxes of 64 x 64, 128-byte swizzle.
 bool encode(EncodeFn fn, CUtensorMap *map, void *base, uint64_t rows, uint64_t cols, uint64_t ld, uint64_t plane)
 {
@@ -173,6 +168,54 @@ bool encode(EncodeFn fn, CUtensorMap *map, void *base, uint64_t rows, uint64_t c
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, base, dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Tiles of one product: of a Gram-sized matrix from its diagonal blocks on,
+// and of X.
+struct Tiles {
+    uint64_t gram, full;
+};
+
+Tiles tiles_of(const MuonMat &m, uint32_t tile)
+{
+    const uint64_t rb = blocks(m.s, zero1::kNsRows), cb = blocks(m.s, tile), per_row = zero1::kNsRows / tile;
+    return Tiles{rb * cb - per_row * (rb * (rb - 1) / 2), blocks(m.rows, zero1::kNsRows) * blocks(m.cols, tile)};
+}
+
+// Columns of a tile.  256 keeps the tensor cores busiest (a product of 256 x
+// 256 x 16 takes 128 cycles, of 256 x 128 x 16 about 105), 128 spreads few
+// tiles over more block pairs and ends each sooner: taken when even the
+// narrow tiles of the largest product find a pair each.
+uint32_t tile_columns(const std::vector<MuonMat> &plan, const std::vector<uint32_t> &large, int sms)
+{
+    uint64_t gram = 0, full = 0;
+    for (const uint32_t i : large) {
+        const Tiles t = tiles_of(plan[i], 128);
+        gram += t.gram;
+        full += t.full;
+    }
+    return std::max(gram, full) <= (uint64_t)sms / 2 ? 128 : 256;
+}
+
+// log2 of the blocks that step a small matrix in one launch, or -1.  One
+// launch of one to eight blocks takes about 5 us an iteration where the tiled
+// products take 14 and more; it holds no side above 128, nor one above 1,536.
+int small_blocks(const MuonMat &m)
+{
+    if (m.s > 128) return -1;
+    const uint32_t l = std::max(m.rows, m.cols);
+    for (int i = 0; i < zero1::kSmallSizes; ++i)
+        if (l <= (zero1::small_width(1 << i) << i)) return i;
+    return -1;
+}
+
+// SMs of the current device; where there is none, creation fails later on.
+int device_sms()
+{
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 0;
+    return sms;
 }
 
 // Where each part of the one allocation lies.
@@ -205,8 +248,8 @@ int create(uint64_t n, int world, const zero1_matrix *mats, uint64_t count, cons
     // ---- the plan
     std::vector<MuonMat> plan(count);
     std::vector<uint2> work;
-    std::vector<uint32_t> chunk_mat;
-    std::vector<uint64_t> region0(count), region1(count), gram(count), poly(count);
+    std::vector<uint32_t> chunk_mat, large, small[zero1::kSmallSizes];
+    std::vector<uint64_t> region0(count), region1(count), gram(count), poly(count), diag(count);
     uint64_t entries = 0, chunks = 0, tiles = 0;
     for (uint64_t i = 0; i < count; ++i) {
         const zero1_matrix &a = mats[i];
@@ -221,47 +264,59 @@ int create(uint64_t n, int world, const zero1_matrix *mats, uint64_t count, cons
         m.lds = (uint32_t)round_up(m.s, 64);
         m.xplane = (uint64_t)a.rows * m.ldx;
         m.splane = (uint64_t)m.s * m.lds;
-        // A and B: row tile r with the column tiles from its diagonal on (2r)
-        const uint64_t sm = blocks(m.s, zero1::kNsTileM), sn = blocks(m.s, zero1::kNsTileN);
-        const uint64_t sym = sm * sn - sm * (sm - 1);
-        const uint64_t full = blocks(a.rows, zero1::kNsTileM) * blocks(a.cols, zero1::kNsTileN);
         const uint64_t size = (uint64_t)a.rows * a.cols;
-        const uint64_t c = (size + zero1::kChunk - 1) / zero1::kChunk;
-        tiles += 2 * sym + full;
-        chunks += c;
-        entries += size;
-        // tickets and per-matrix counts are 32-bit, over all steps
-        if (tiles * 32 * zero1::kNsParts > 0x7FFFFFFFull || chunks > 0x7FFFFFFFull)
-            return mfail(ZERO1_EINVAL, "the matrices are too large for one handle");
-        m.parts[0] = m.parts[1] = (uint32_t)(sym * zero1::kNsParts);
-        m.parts[2] = (uint32_t)(full * zero1::kNsParts);
-        m.chunk0 = (uint32_t)(chunks - c);
-        m.chunks = (uint32_t)c;
         m.vec = a.offset % 8 == 0 && a.ld % 8 == 0 && a.cols % 8 == 0;
         const double r = a.rows, k = a.cols;
         m.scale = (float)(hp->update_scale *
                           std::sqrt(hp->scale_rule == ZERO1_MUON_SCALE_RMS ? std::max(r, k) : std::max(1.0, r / k)));
+        entries += size;
+        const int blocks_log = small_blocks(m);
+        if (blocks_log >= 0) {
+            small[blocks_log].push_back((uint32_t)i);
+            continue;
+        }
+        large.push_back((uint32_t)i);
+        const uint64_t c = (size + zero1::kChunk - 1) / zero1::kChunk;
+        chunks += c;
+        if (chunks > 0x7FFFFFFFull) return mfail(ZERO1_EINVAL, "the matrices are too large for one handle");
+        m.chunk0 = (uint32_t)(chunks - c);
+        m.chunks = (uint32_t)c;
+    }
+    const int sms_hint = device_sms();
+    const uint32_t tile = tile_columns(plan, large, sms_hint);
+    for (const uint32_t i : large) {
+        MuonMat &m = plan[i];
+        const Tiles t = tiles_of(m, tile);
+        tiles += 2 * t.gram + t.full;
+        // tickets and per-matrix counts are 32-bit, over all steps
+        if (tiles * 32 * zero1::kNsParts > 0x7FFFFFFFull)
+            return mfail(ZERO1_EINVAL, "the matrices are too large for one handle");
+        m.parts[0] = m.parts[1] = (uint32_t)(t.gram * zero1::kNsParts);
+        m.parts[2] = (uint32_t)(t.full * zero1::kNsParts);
     }
     work.reserve(tiles);
     chunk_mat.reserve(chunks);
     const auto push = [&](uint32_t phase, uint64_t i, uint32_t r, uint32_t c) {
         work.push_back(make_uint2((uint32_t)i | phase << 30, r | c << 16));
     };
+    const uint32_t per_row = zero1::kNsRows / tile;   // column tiles of a diagonal block
     for (uint32_t phase = 0; phase < 3; ++phase)
-        for (uint64_t i = 0; i < count; ++i) {
+        for (const uint32_t i : large) {
             const MuonMat &m = plan[i];
+            const uint32_t rb = (uint32_t)blocks(phase < 2 ? m.s : m.rows, zero1::kNsRows);
+            const uint32_t cb = (uint32_t)blocks(phase < 2 ? m.s : m.cols, tile);
             if (phase < 2) {
-                const uint32_t rb = (uint32_t)blocks(m.s, zero1::kNsTileM), cb = (uint32_t)blocks(m.s, zero1::kNsTileN);
                 for (uint32_t r = 0; r < rb; ++r)
-                    for (uint32_t c = 2 * r; c < cb; ++c) push(phase, i, r, c);
+                    for (uint32_t c = per_row * r; c < cb; ++c) push(phase, i, r, c);
             } else {
                 // the Gram-sized factor stays in L2 and X passes once: all of one block of X before the next
-                const uint32_t rb = (uint32_t)blocks(m.rows, zero1::kNsTileM), cb = (uint32_t)blocks(m.cols, zero1::kNsTileN);
                 for (uint32_t j = 0; j < (m.tall ? rb : cb); ++j)
                     for (uint32_t k = 0; k < (m.tall ? cb : rb); ++k) push(phase, i, m.tall ? j : k, m.tall ? k : j);
             }
         }
-    for (uint64_t i = 0; i < count; ++i) chunk_mat.insert(chunk_mat.end(), plan[i].chunks, (uint32_t)i);
+    for (const uint32_t i : large) chunk_mat.insert(chunk_mat.end(), plan[i].chunks, i);
+    std::vector<uint32_t> small_list;
+    for (const auto &v : small) small_list.insert(small_list.end(), v.begin(), v.end());
 
     // ---- the device
     int ndev = 0, dev = 0;
@@ -278,20 +333,22 @@ int create(uint64_t n, int world, const zero1_matrix *mats, uint64_t count, cons
     const EncodeFn fn = encoder();
     if (!fn) return mfail(ZERO1_ECUDA, "the driver has no tensor-map encoder");
 
-    // ---- the workspace: plan | counters | per matrix: two regions, A, B
+    // ---- the workspace: plan | counters | per matrix: two regions, A, P, A's diagonal
     Layout l;
     const uint64_t at_mats = l.take(count * sizeof(MuonMat));
     const uint64_t at_maps = l.take(count * zero1::kMapsPerMat * sizeof(CUtensorMap));
     const uint64_t at_work = l.take(work.size() * sizeof(uint2));
     const uint64_t at_chunk = l.take(chunk_mat.size() * sizeof(uint32_t));
+    const uint64_t at_small = l.take(small_list.size() * sizeof(uint32_t));
     const uint64_t at_part = l.take(chunk_mat.size() * sizeof(double));
     const uint64_t at_done = l.take(count * sizeof(unsigned));
     const uint64_t at_ticket = l.take(sizeof(unsigned)), at_errors = l.take(sizeof(unsigned));
-    for (uint64_t i = 0; i < count; ++i) {
+    for (const uint32_t i : large) {
         region0[i] = l.take(plan[i].xplane * 4);
         region1[i] = l.take(plan[i].xplane * 4);
         gram[i] = l.take(plan[i].splane * 4);
         poly[i] = l.take(plan[i].splane * 4);
+        diag[i] = l.take((uint64_t)plan[i].s * zero1::kNsRows * 4);
     }
     zero1_muon_ctx *h = new zero1_muon_ctx;
     h->n = n;
@@ -308,26 +365,30 @@ int create(uint64_t n, int world, const zero1_matrix *mats, uint64_t count, cons
     unsigned char *base = static_cast<unsigned char *>(h->block);
     std::vector<CUtensorMap> maps(count * zero1::kMapsPerMat);
     bool good = true;
-    for (uint64_t i = 0; i < count && good; ++i) {
+    for (const uint32_t i : large) {
+        if (!good) break;
         MuonMat &m = plan[i];
         m.region[0] = base + region0[i];
         m.region[1] = base + region1[i];
         m.gram = base + gram[i];
         m.poly = base + poly[i];
-        CUtensorMap *t = &maps[i * zero1::kMapsPerMat];
+        m.diag = base + diag[i];
+        CUtensorMap *t = &maps[(uint64_t)i * zero1::kMapsPerMat];
         good = encode(fn, t + zero1::kMapX0, m.region[0], m.rows, m.cols, m.ldx, m.xplane) &&
                encode(fn, t + zero1::kMapX1, m.region[1], m.rows, m.cols, m.ldx, m.xplane) &&
                encode(fn, t + zero1::kMapA, m.gram, m.s, m.s, m.lds, m.splane) &&
-               encode(fn, t + zero1::kMapB, m.poly, m.s, m.s, m.lds, m.splane) &&
-               encode_out(fn, t + zero1::kMapOut, m.region[hp->ns_steps & 1], m.rows, m.cols, m.ldx);
+               encode(fn, t + zero1::kMapP, m.poly, m.s, m.s, m.lds, m.splane) &&
+               encode(fn, t + zero1::kMapD, m.diag, m.s, std::min<uint64_t>(m.s, zero1::kNsRows), zero1::kNsRows,
+                      (uint64_t)m.s * zero1::kNsRows);
     }
     e = good ? cudaMemset(h->block, 0, h->block_bytes) : cudaErrorInvalidValue;
     const auto put = [&](uint64_t at, const void *src, uint64_t bytes) {
-        if (e == cudaSuccess) e = cudaMemcpy(base + at, src, bytes, cudaMemcpyHostToDevice);
+        if (e == cudaSuccess && bytes) e = cudaMemcpy(base + at, src, bytes, cudaMemcpyHostToDevice);
     };
     put(at_mats, plan.data(), count * sizeof(MuonMat));
     put(at_maps, maps.data(), maps.size() * sizeof(CUtensorMap));
     put(at_work, work.data(), work.size() * sizeof(uint2));
+    put(at_small, small_list.data(), small_list.size() * sizeof(uint32_t));
     put(at_chunk, chunk_mat.data(), chunk_mat.size() * sizeof(uint32_t));
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) {
@@ -347,6 +408,14 @@ int create(uint64_t n, int world, const zero1_matrix *mats, uint64_t count, cons
     d.count = (uint32_t)count;
     d.nchunks = (uint32_t)chunk_mat.size();
     d.work_per_iter = (uint32_t)work.size();
+    d.tile = tile;
+    h->small.list = reinterpret_cast<uint32_t *>(base + at_small);
+    for (int i = 0, at = 0; i < zero1::kSmallSizes; ++i) {
+        h->small.first[i] = (uint32_t)at;
+        h->small.count[i] = (uint32_t)small[i].size();
+        at += (int)small[i].size();
+    }
+    h->any_small = !small_list.empty();
     {
         std::lock_guard<std::mutex> lk(g_muon_mu);
         g_muon_live.insert(h);
@@ -417,7 +486,11 @@ int zero1_muon_step(zero1_muon_handle h, const void *const *grad_ptrs, void *con
     MuonDeviceGuard g(h->device);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const zero1::MuonScalars sc = scalars(h);
-    cudaError_t e = zero1::launch_muon_momentum(h->dev, sc, grad_ptrs, h->world, momentum, st);
+    cudaError_t e = cudaSuccess;
+    if (h->any_small)
+        e = zero1::launch_muon_small_step(h->dev, h->small, sc, grad_ptrs, param_ptrs, h->world, master, momentum, st);
+    if (h->dev.nchunks == 0) return e == cudaSuccess ? ZERO1_OK : mcuda(e, "kernel launch");
+    if (e == cudaSuccess) e = zero1::launch_muon_momentum(h->dev, sc, grad_ptrs, h->world, momentum, st);
     if (e == cudaSuccess) e = zero1::launch_muon_split(h->dev, sc, nullptr, false, st);
     if (e == cudaSuccess) e = zero1::launch_muon_iterate(h->dev, sc, h->num_sms, st);
     if (e == cudaSuccess) e = zero1::launch_muon_apply(h->dev, sc, param_ptrs, h->world, master, st);
@@ -436,7 +509,11 @@ int zero1_muon_orthogonalize(zero1_muon_handle h, const void *in, int in_dtype, 
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const zero1::MuonScalars sc = scalars(h);
     const bool bf = in_dtype == ZERO1_DTYPE_BF16;
-    cudaError_t e = zero1::launch_muon_norm(h->dev, in, bf, st);
+    cudaError_t e = cudaSuccess;
+    if (h->any_small)
+        e = zero1::launch_muon_small_orth(h->dev, h->small, sc, in, bf, out, out_dtype == ZERO1_DTYPE_BF16, st);
+    if (h->dev.nchunks == 0) return e == cudaSuccess ? ZERO1_OK : mcuda(e, "kernel launch");
+    if (e == cudaSuccess) e = zero1::launch_muon_norm(h->dev, in, bf, st);
     if (e == cudaSuccess) e = zero1::launch_muon_split(h->dev, sc, in, bf, st);
     if (e == cudaSuccess) e = zero1::launch_muon_iterate(h->dev, sc, h->num_sms, st);
     if (e == cudaSuccess) e = zero1::launch_muon_out(h->dev, sc, out, out_dtype == ZERO1_DTYPE_BF16, st);

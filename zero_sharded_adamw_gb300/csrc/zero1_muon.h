@@ -10,11 +10,10 @@
 
 namespace zero1 {
 
-// Output tile of the matrix products: 256 rows (128 in each block of a pair)
-// by 128 columns.
-constexpr int kNsTileM = 256;
-constexpr int kNsTileN = 128;
-constexpr int kNsParts = 4;            // arrivals a finished tile makes: two halves in each block
+// Output tile of the matrix products: 256 rows, 128 in each block of a pair,
+// by 256 or 128 columns (one choice for a handle, MuonDev::tile).
+constexpr uint32_t kNsRows = 256;
+constexpr int kNsParts = 32;           // arrivals a finished tile makes: one by each warp that writes it
 constexpr int kNsTileK = 64;           // K of one pipeline stage
 constexpr uint32_t kChunk = 16384;     // entries of one elementwise block
 constexpr uint32_t kMaxSide = 1u << 22;
@@ -33,7 +32,8 @@ struct MuonMat {
     uint32_t tall;             // rows > cols: Gram matrix X^T X, update X B
     uint32_t ldx, lds;         // padded row lengths of X and of the Gram matrices
     unsigned char *region[2];
-    unsigned char *gram, *poly;   // A and B = b A + c A A: two f16 planes each
+    unsigned char *gram, *poly;   // A, and the polynomial X is multiplied by: two f16 planes each
+    unsigned char *diag;       // diagonal 256 x 256 blocks of A + (b/c) I, one below the other: two f16 planes
     uint64_t xplane, splane;   // entries of one plane
     uint32_t parts[3];         // arrivals of the three products of one iteration: tiles x kNsParts
     uint32_t chunk0, chunks;   // elementwise blocks [chunk0, chunk0 + chunks)
@@ -41,8 +41,9 @@ struct MuonMat {
     float scale;               // update_scale times the side factor
 };
 
-// Tensor maps of one matrix: X in region 0 and 1, A, B, and the fp32 result.
-enum { kMapX0 = 0, kMapX1 = 1, kMapA = 2, kMapB = 3, kMapOut = 4, kMapsPerMat = 5 };
+// Tensor maps of one matrix: X in region 0 and 1, A, its diagonal blocks with
+// the linear term, and the polynomial.
+enum { kMapX0 = 0, kMapX1 = 1, kMapA = 2, kMapD = 3, kMapP = 4, kMapsPerMat = 5 };
 
 // The plan and the workspace of one handle, in device memory.
 struct MuonDev {
@@ -55,7 +56,21 @@ struct MuonDev {
     unsigned *ticket;
     unsigned *errors;          // sticky: bit 0 = a wait gave up
     uint32_t count, nchunks, work_per_iter;
+    uint32_t tile;             // columns of a tile
 };
+
+// Small matrices, whose whole step is one launch (zero1_muon_small.cu): lists
+// of them by the number of blocks that share one, 1, 2, 4 or 8.
+constexpr int kSmallSizes = 4;
+struct MuonSmall {
+    const uint32_t *list;      // device memory: indices into MuonDev::mats
+    uint32_t first[kSmallSizes], count[kSmallSizes];
+};
+// Columns of the larger side a block holds, at most: X, two f16 parts of 128
+// rows, beside the Gram matrix (64 KB) and, in a cluster, the parts of its
+// sum (64 KB).
+inline uint32_t small_width(int blocks) { return blocks == 1 ? 256 : 192; }
+inline int small_smem(int blocks) { return (int)(2 * 128 * 2 * small_width(blocks)) + (blocks == 1 ? 1 : 2) * 65536 + 1024; }
 
 struct MuonScalars {
     float inv_w, momentum, one_minus_momentum, eps;
@@ -70,6 +85,11 @@ cudaError_t launch_muon_norm(const MuonDev &d, const void *in, bool bf16, cudaSt
 // `in` null: the fp32 update that launch_muon_momentum left in region 1.
 cudaError_t launch_muon_split(const MuonDev &d, const MuonScalars &sc, const void *in, bool bf16, cudaStream_t stream);
 cudaError_t launch_muon_iterate(const MuonDev &d, const MuonScalars &sc, int num_sms, cudaStream_t stream);
+cudaError_t launch_muon_small_step(const MuonDev &d, const MuonSmall &small, const MuonScalars &sc,
+                                   const void *const *grads, void *const *params, int world, float *master,
+                                   float *momentum, cudaStream_t stream);
+cudaError_t launch_muon_small_orth(const MuonDev &d, const MuonSmall &small, const MuonScalars &sc, const void *in,
+                                   bool in_bf16, void *out, bool out_bf16, cudaStream_t stream);
 cudaError_t launch_muon_apply(const MuonDev &d, const MuonScalars &sc, void *const *params, int world, float *master,
                               cudaStream_t stream);
 cudaError_t launch_muon_out(const MuonDev &d, const MuonScalars &sc, void *out, bool bf16, cudaStream_t stream);

@@ -1,19 +1,20 @@
 // zero1_muon_kernels.cu -- kernels of the matrix optimizer: momentum and
 // norm, the Newton-Schulz iteration on the tensor cores, and the update.
 //
-// The iteration (X of sides s <= l, A the s x s Gram matrix):
-//     A = X X^T,  B = b A + c A A,  X <- a X + B X        (rows <= cols)
-//     A = X^T X,  B = b A + c A A,  X <- a X + X B        (rows >  cols)
+// The iteration (X of sides s <= l, A the s x s Gram matrix, P the matrix
+// that X is multiplied by):
+//     A = X X^T,  P = a I + b A + c A A,  X <- P X        (rows <= cols)
+//     A = X^T X,  P = a I + b A + c A A,  X <- X P        (rows >  cols)
 // Singular values far below one grow by a = 3.4 a step, 480-fold over five:
 // an error that a rounding of X leaves there grows with them, and with X in
 // bf16 (2^-9) the result of a matrix with a few strong directions is half
-// noise.  So every operand is kept as two f16 parts, hi + lo = 22 bits, a
-// product is hi*hi + hi*lo + lo*hi into one fp32 accumulator (the dropped
-// lo*lo is 2^-24), and a X is added in fp32 outside the product.  The result
-// is as exact as the iteration in fp32, for three tensor-core products in
-// place of one.
+// noise.  So every operand is kept as two f16 parts, hi + lo = 22 bits, and
+// a product is hi*hi + hi*lo + lo*hi into one fp32 accumulator (the dropped
+// lo*lo is 2^-24).  The result is as exact as the iteration in fp32, for
+// three tensor-core products in place of one.
 #include "zero1_internal.h"
 #include "zero1_muon.h"
+#include "zero1_muon_device.cuh"
 #include "zero1_tc.cuh"
 
 namespace zero1 {
@@ -28,8 +29,8 @@ struct MomentumParams {
     const uint16_t *grads[CAP];
     MuonDev d;
     float *momentum;
-    float inv_w, mu, omm;
-    int world, nesterov;
+    int world;
+    MuonScalars sc;
 };
 
 template <int CAP>
@@ -60,19 +61,6 @@ __device__ __forceinline__ void for_chunk(const MuonMat &m, uint32_t chunk, uint
     }
 }
 
-// A sum of squares in fp32 that moves to fp64 what would leave fp32's range.
-struct SquareSum {
-    float s = 0.f;
-    double big = 0.0;
-    __device__ __forceinline__ void add(float v)
-    {
-        const float q = v * v;
-        if (q > 1e30f) big += (double)v * (double)v;
-        else s += q;
-    }
-    __device__ __forceinline__ double total() const { return big + (double)s; }
-};
-
 // Sum over the block in a fixed order; valid on thread 0.
 __device__ __forceinline__ double block_sum(double v)
 {
@@ -94,46 +82,6 @@ __device__ __forceinline__ void reset_counters(const MuonDev &d)
     if (i == 0) *d.ticket = 0;
 }
 
-__device__ __forceinline__ void load8(float v[8], const float *p)
-{
-    const float4 x = *reinterpret_cast<const float4 *>(p), y = *reinterpret_cast<const float4 *>(p + 4);
-    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
-}
-
-__device__ __forceinline__ void load8(float v[8], const uint16_t *p)
-{
-    ptx::set_widened(v, *reinterpret_cast<const uint4 *>(p));
-}
-
-__device__ __forceinline__ void store8(float *p, const float v[8])
-{
-    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4 *>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-}
-
-__device__ __forceinline__ void store8(uint16_t *p, const float v[8])
-{
-    *reinterpret_cast<uint4 *>(p) = make_uint4(ptx::pack2(v[0], v[1]), ptx::pack2(v[2], v[3]), ptx::pack2(v[4], v[5]),
-                                               ptx::pack2(v[6], v[7]));
-}
-
-__device__ __forceinline__ float load1(const float *p) { return *p; }
-__device__ __forceinline__ float load1(const uint16_t *p) { return __uint_as_float((uint32_t)*p << 16); }
-__device__ __forceinline__ void store1(float *p, float v) { *p = v; }
-__device__ __forceinline__ void store1(uint16_t *p, float v) { *p = __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
-
-// hi + lo = v to 22 bits.
-__device__ __forceinline__ void split(float v, __half &hi, __half &lo)
-{
-    hi = __float2half_rn(v);
-    lo = __float2half_rn(v - __half2float(hi));
-}
-
-__device__ __forceinline__ uint32_t pack(__half a, __half b)
-{
-    return (uint32_t)__half_as_ushort(a) | ((uint32_t)__half_as_ushort(b) << 16);
-}
-
 // Momentum and the update it gives, with the norm's partial sums:
 // m = mu m + (1-mu) g for g the rank-ordered mean of the W gradients, and
 // u = mu m + (1-mu) g (nesterov) or m, left as fp32 in region 1.
@@ -146,9 +94,7 @@ __global__ void __launch_bounds__(kElemThreads) muon_momentum_kernel(const __gri
     float *u = reinterpret_cast<float *>(m.region[1]);
     SquareSum ss;
     const auto one = [&](float sum, float &mom) {
-        const float g = sum * p.inv_w;
-        mom = p.mu * mom + p.omm * g;
-        const float x = p.nesterov ? p.mu * mom + p.omm * g : mom;
+        const float x = look_ahead(p.sc, sum, mom);
         ss.add(x);
         return x;
     };
@@ -224,24 +170,26 @@ __global__ void __launch_bounds__(kElemThreads) muon_split_kernel(MuonDev d, con
     if (threadIdx.x == 0) factor = (float)((double)kNsScale / (sqrt(part[0]) + (double)eps));
     __syncthreads();
     const float k = factor;
-    __half *hi = reinterpret_cast<__half *>(m.region[0]), *lo = hi + m.xplane;
+    uint16_t *hi = reinterpret_cast<uint16_t *>(m.region[0]), *lo = hi + m.xplane;
     const T *src = in ? in : reinterpret_cast<const T *>(m.region[1]);
     if (m.vec) {
         for_chunk(m, blockIdx.x - m.chunk0, 8, [&](uint64_t f, uint64_t x) {
             float v[8];
-            __half h[8], l[8];
+            uint4 h, l;
             load8(v, src + (in ? f : x));
-#pragma unroll
-            for (int i = 0; i < 8; ++i) split(v[i] * k, h[i], l[i]);
-            *reinterpret_cast<uint4 *>(hi + x) = make_uint4(pack(h[0], h[1]), pack(h[2], h[3]), pack(h[4], h[5]), pack(h[6], h[7]));
-            *reinterpret_cast<uint4 *>(lo + x) = make_uint4(pack(l[0], l[1]), pack(l[2], l[3]), pack(l[4], l[5]), pack(l[6], l[7]));
+            split(v[0] * k, v[1] * k, h.x, l.x);
+            split(v[2] * k, v[3] * k, h.y, l.y);
+            split(v[4] * k, v[5] * k, h.z, l.z);
+            split(v[6] * k, v[7] * k, h.w, l.w);
+            *reinterpret_cast<uint4 *>(hi + x) = h;
+            *reinterpret_cast<uint4 *>(lo + x) = l;
         });
     } else {
         for_chunk(m, blockIdx.x - m.chunk0, 1, [&](uint64_t f, uint64_t x) {
-            __half h, l;
-            split(load1(src + (in ? f : x)) * k, h, l);
-            hi[x] = h;
-            lo[x] = l;
+            uint32_t h, l;
+            split(load1(src + (in ? f : x)) * k, 0.f, h, l);
+            hi[x] = (uint16_t)h;
+            lo[x] = (uint16_t)l;
         });
     }
 }
@@ -290,22 +238,38 @@ __global__ void __launch_bounds__(kElemThreads) muon_out_kernel(MuonDev d, T *ou
 
 // ---------------------------------------------------------- the iteration
 
-// Shared memory of one block: three stages of one K step (64) of its 128
-// rows of A and its 64 rows of B, high and low parts, and for each of the
-// two column halves of a tile 32 KB through which it enters and leaves.
-constexpr int kStages = 3;
+// For tiles of TN columns.  Shared memory of one block: stages of one K step
+// (64) of its 128 rows of A and its TN/2 rows of B, high and low parts, and
+// 2 KB an epilogue warp.
 constexpr uint32_t kBox = 8192;                        // 64 x 64 f16
-constexpr uint32_t kStageBytes = 6 * kBox;             // A hi, A lo (two boxes each), B hi, B lo
-constexpr uint32_t kHalfBytes = 4 * kBox;              // 128 rows x 64 columns, hi and lo (or fp32)
-constexpr int kSlots = 4;                              // tiles in flight between the roles
-constexpr int kNsThreads = 384;                        // loads, products, 2 x stores, 2 x 4 epilogue warps
-constexpr uint32_t kTmemCols = 512;                    // two accumulators of hi*hi, two of hi*lo + lo*hi
+constexpr int kSlots = 3;                              // tiles in flight between the roles
+constexpr int kGroups = 4;                             // of 4 epilogue warps, TN/4 columns each
+constexpr int kNsThreads = 64 + kGroups * 128;         // loads, products; epilogue
+constexpr uint32_t kWarpOut = 2048;                    // 32 rows x 64 bytes on an epilogue warp's way out
+template <int TN>
+struct Shape {
+    static constexpr int kBoxesB = TN / 128;           // of one part of B
+    static constexpr uint32_t kStageBytes = (4 + 2 * kBoxesB) * kBox;   // A hi, A lo (two boxes each), B hi, B lo
+    static constexpr int kStages = TN == 256 ? 3 : 4;
+    static constexpr int kAccs = 512 / TN;             // accumulators: all of TMEM
+    static constexpr int kSmem = kStages * kStageBytes + 4 * kGroups * kWarpOut + 1024;
+};
 // K of one accumulator.  The tensor cores cut every addition of 16 products
 // off below the sum's last place, so a sum of positive terms falls short by
-// 8e-8 of itself for each (measured: 4e-6 over K = 1024, 9e-5 over 16384).
-// Longer sums are gathered 256 at a time and added up in rounded fp32.
-constexpr uint32_t kAccK = 256;
-constexpr int kNsSmem = kStages * kStageBytes + 2 * kHalfBytes + 1024;
+// 8e-8 of itself for each (measured with one product: 4e-6 over K = 1024,
+// 9e-5 over 16384).  Longer sums are gathered 128 at a time and added up in
+// rounded fp32.  A wide tile's first two sums are of 256, which keeps the
+// products busy while the tile before is written.
+template <int TN>
+__device__ __forceinline__ bool starts_sum(uint32_t k)
+{
+    return k % (TN == 256 && k < 512 ? 256 : 128) == 0;
+}
+template <int TN>
+__device__ __forceinline__ uint32_t sums_of(uint32_t k)
+{
+    return TN == 128 ? (k + 127) / 128 : k <= 512 ? (k + 255) / 256 : 2 + (k - 512 + 127) / 128;
+}
 
 struct NsParams {
     MuonDev d;
@@ -314,75 +278,104 @@ struct NsParams {
     int steps;
 };
 
-// In the last iterations A is near the identity, and the sums A A and B X
-// are large terms that nearly cancel a X: their errors count several times.
-// There the polynomial is taken about A = alpha I, an identity for any
-// alpha: with A' = A - alpha I,
-//   a + b A + c A A = (a + b alpha + c alpha^2) + ((b + 2 c alpha) A' + c A' A'),
-// whose products are small.  The iterations before keep alpha = 0, since
-// directions still far below one would gain the error of a term that their
-// B X does not have.
-constexpr float kAlpha = 0.85f;
-__device__ __forceinline__ float alpha_of(uint32_t iter, int steps) { return (int)iter + 2 >= steps ? kAlpha : 0.f; }
+// The linear and the square term come from one product, c A' (A' + v I) with
+// v = (b + 2 c alpha)/c; A' + v I differs from A' in its diagonal tiles only.
 
-struct Tile {
-    uint32_t mat, phase, iter, ti, tj;
+// A tile, as it is described to all roles of both blocks of a pair: they meet
+// the plan in shared memory only.
+struct __align__(16) Tile {
+    uint32_t mat, phase;
+    uint32_t map_a, map_b;     // tensor maps of the operands
+    uint32_t k;
+    uint32_t a_turn, b_turn;   // K below which an operand is MN-major in memory
+    uint32_t diag;             // tensor map of B for the 256 of K from b_turn on, or 0
+    uint32_t row, col;         // of the tile in its matrix
+    uint32_t rows, cols;       // of the matrix
+    unsigned char *out;        // first entry of the matrix: f16 parts, or fp32 in the last product
+    uint64_t plane;            // bytes from the high to the low parts
+    unsigned char *also;       // diagonal blocks of A' + v I, or null: a copy with v more on the diagonal
+    uint64_t also_plane;
+    uint32_t pitch;            // bytes of a row
+    uint32_t last;             // results in fp32
+    float factor, on_diagonal; // result = factor * product, plus this on the diagonal
+    float v;
+    uint32_t pad[3];
 };
 constexpr uint32_t kNoMore = 3;                        // phase of the tile that ends the work
+constexpr int kTileWords = sizeof(Tile) / 16;
 
 struct NsShared {
-    uint4 slot[kSlots];
-    uint64_t full[kStages], empty[kStages];            // operand ring
+    Tile slot[kSlots];
+    uint64_t full[4], empty[4];                        // operand ring
     uint64_t slot_full[kSlots], slot_empty[kSlots];    // tile ring
-    uint64_t acc_full[2], acc_empty[2];                // accumulators
-    uint64_t half_full[2], half_done[2];               // a half's memory: free, with the tile's term; written
+    uint64_t slot_go[kSlots];                          // a tile's operands are there to be loaded
+    uint64_t acc_full[4], acc_empty[4];                // accumulators
     uint64_t drain;
     uint32_t tmem;
     int abort;
 };
 
-__device__ __forceinline__ uint4 pack_tile(const Tile &t) { return make_uint4(t.mat, t.phase | t.iter << 2, t.ti, t.tj); }
-__device__ __forceinline__ Tile unpack_tile(uint4 v) { return Tile{v.x, v.y & 3u, v.y >> 2, v.z, v.w}; }
-
-// The operands of a tile's product.  A Gram-sized matrix (A or B) is stored
-// from its 256-row tiles' diagonal on; what lies below is read transposed
-// from above, as an MN-major operand.
-struct Product {
-    const CUtensorMap *a, *b;
-    uint32_t k;
-    uint32_t a_turn, b_turn;   // K below which the operand is MN-major in memory
-
-    __device__ __forceinline__ Product(const MuonDev &d, const Tile &t)
-    {
-        const MuonMat &m = d.mats[t.mat];
-        const CUtensorMap *maps = d.maps + (uint64_t)t.mat * kMapsPerMat;
-        const CUtensorMap *x = maps + (t.iter & 1 ? kMapX1 : kMapX0);
-        constexpr uint32_t kAlways = 0xFFFFFFFFu;
-        const uint32_t row_turn = t.ti * kNsTileM, col_turn = (t.tj >> 1) * kNsTileM;
-        if (t.phase == 0) {          // X X^T, or X^T X
-            a = b = x;
-            k = m.tall ? m.rows : m.cols;
-            a_turn = b_turn = m.tall ? kAlways : 0;
-        } else if (t.phase == 1) {   // A A
-            a = b = maps + kMapA;
-            k = m.s;
-            a_turn = row_turn;
-            b_turn = col_turn;
-        } else if (!m.tall) {        // B X
-            a = maps + kMapB;
-            b = x;
-            k = m.s;
-            a_turn = row_turn;
-            b_turn = kAlways;
-        } else {                     // X B
-            a = x;
-            b = maps + kMapB;
-            k = m.s;
-            a_turn = 0;
-            b_turn = col_turn;
+// The products:
+//   phase 0: A' = X X^T (or X^T X) - alpha I,
+//   phase 1: P = c A' (A' + v I) + (a + b alpha + c alpha^2) I,
+//   phase 2: X <- P X (or X P).
+// A Gram-sized matrix (A' or P) is stored from its diagonal 256 x 256 blocks
+// on; what lies below is read transposed from above, as an MN-major operand.
+__device__ __forceinline__ void describe(const NsParams &p, uint32_t ticket, Tile &t, uint32_t &need)
+{
+    const uint32_t iter = ticket / p.d.work_per_iter;
+    const uint2 w = p.d.work[ticket - iter * p.d.work_per_iter];
+    t.mat = w.x & 0x3FFFFFFFu;
+    t.phase = w.x >> 30;
+    const MuonMat &m = p.d.mats[t.mat];
+    const uint32_t ti = w.y & 0xFFFFu, tj = w.y >> 16;
+    need = iter * (m.parts[0] + m.parts[1] + m.parts[2]) + (t.phase > 0 ? m.parts[0] : 0) + (t.phase > 1 ? m.parts[1] : 0);
+    const uint32_t maps = t.mat * kMapsPerMat, x = maps + (iter & 1 ? kMapX1 : kMapX0);
+    constexpr uint32_t kAlways = 0xFFFFFFFFu;
+    constexpr float inv = 1.0f / kNsScale;
+    t.row = ti * kNsRows;
+    t.col = tj * p.d.tile;
+    const uint32_t block = t.col / kNsRows * kNsRows;   // the diagonal block beside the tile's columns
+    const float alpha = alpha_of(iter, p.steps);
+    t.v = (p.b + 2.f * p.c * alpha) / p.c * kNsScale;
+    t.diag = 0;
+    t.also = nullptr;
+    t.also_plane = (uint64_t)m.s * (kNsRows * 2);
+    t.last = t.phase == 2 && (int)iter + 1 == p.steps;
+    t.factor = t.phase == 1 ? p.c * inv : t.last ? inv * inv : inv;
+    t.on_diagonal = 0.f;
+    if (t.phase < 2) {
+        t.rows = t.cols = m.s;
+        t.pitch = m.lds * 2;
+        t.plane = m.splane * 2;
+        t.out = t.phase == 0 ? m.gram : m.poly;
+        if (t.phase == 0) {
+            t.map_a = t.map_b = x;
+            t.k = m.tall ? m.rows : m.cols;
+            t.a_turn = t.b_turn = m.tall ? kAlways : 0;
+            t.on_diagonal = -alpha * kNsScale;
+            if (t.row == block) t.also = m.diag;
+        } else {
+            t.map_a = t.map_b = maps + kMapA;
+            t.k = m.s;
+            t.a_turn = t.row;
+            t.b_turn = block;
+            t.diag = maps + kMapD;
+            t.on_diagonal = (p.a + alpha * (p.b + alpha * p.c)) * kNsScale;
         }
+    } else {
+        t.rows = m.rows;
+        t.cols = m.cols;
+        t.pitch = m.ldx * (t.last ? 4 : 2);
+        t.plane = m.xplane * 2;
+        t.out = m.region[(iter + 1) & 1];
+        t.k = m.s;
+        t.map_a = m.tall ? x : maps + kMapP;
+        t.map_b = m.tall ? maps + kMapP : x;
+        t.a_turn = m.tall ? 0 : t.row;
+        t.b_turn = m.tall ? block : kAlways;
     }
-};
+}
 
 // Wait until `need` arrivals of the matrix have been made (bounded like the
 // pipeline waits; gives up at once when any block of the grid has).
@@ -406,17 +399,31 @@ __device__ __forceinline__ bool wait_parts(const unsigned *done, unsigned need, 
     }
 }
 
-// w[2i], w[2i+1] += k * (hi + lo) of eight entries.
-__device__ __forceinline__ void add8(float *w, float k, uint4 hi, uint4 lo)
+// A warp's 32 rows of 64 bytes: lane r gives row r, and 4 lanes write each
+// row, 16 bytes at a time.  `mem`: the warp's 2 KB; row r keeps its pieces
+// exchanged by (r >> 1) & 3, free of bank conflicts both ways.
+__device__ __forceinline__ uint32_t turned(uint32_t mem, uint32_t row, uint32_t piece)
 {
-    const uint32_t x[4] = {hi.x, hi.y, hi.z, hi.w}, y[4] = {lo.x, lo.y, lo.z, lo.w};
+    return mem + row * 64 + ((piece ^ ((row >> 1) & 3u)) * 16);
+}
+__device__ __forceinline__ void turn_in(uint32_t mem, const uint32_t x[16])
+{
+    const uint32_t lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&x[i]));
-        const float2 l = __half22float2(*reinterpret_cast<const __half2 *>(&y[i]));
-        w[2 * i] += k * (h.x + l.x);
-        w[2 * i + 1] += k * (h.y + l.y);
+    for (uint32_t j = 0; j < 4; ++j)
+        tc::st_shared(turned(mem, lane, j), make_uint4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]));
+    __syncwarp();
+}
+__device__ __forceinline__ void turn_out(uint32_t mem, unsigned char *dst, uint64_t pitch, uint32_t rows)
+{
+    const uint32_t lane = threadIdx.x & 31;
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i) {
+        const uint32_t row = 8 * i + (lane >> 2);
+        const uint4 v = tc::ld_shared(turned(mem, row, lane & 3));
+        if (row < rows) *reinterpret_cast<uint4 *>(dst + row * pitch + (lane & 3) * 16) = v;
     }
+    __syncwarp();
 }
 
 // The whole iteration over all matrices in one launch, by pairs of blocks.
@@ -424,19 +431,25 @@ __device__ __forceinline__ void add8(float *w, float k, uint4 hi, uint4 lo)
 // depends on (all of the previous product of its matrix), so a pair that
 // waits for a matrix's counter waits only for tiles that running pairs hold:
 // none needs another to be resident, and the grid may be of any size.
-// Within a pair, one thread of each block loads its operands (TMA), one
-// thread of the first block issues the products, and in each block 2 x 4
-// warps take its 128 x 128 half of the tile out of one accumulator while the
-// other fills, 64 columns each four: through shared memory, into which a
-// store thread loaded the term to be added (b A or a X) meanwhile and from
-// which it stores the result and counts the tile as finished.
+// Within a pair, one thread of the second block draws tiles and waits for
+// what they depend on, one thread of each block loads its operands (TMA), one
+// thread of the first block issues the products, and in each block 4 x 4
+// warps take its 128 x 256 half of the tile out of one accumulator while the
+// other fills, write it and count it as finished.  Each warp turns its 32
+// rows in 2 KB of shared memory so that a store covers 8 rows of 64 bytes;
+// straight from the registers, a row a lane, writing took 4.5 us a tile, and
+// through TMA, 64 columns at a time in the 32 KB that the stages leave, 7.4.
+template <int TN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNsThreads, 1)
     muon_iterate_kernel(const __grid_constant__ NsParams p)
 {
+    using S = Shape<TN>;
+    constexpr int kStages = S::kStages, kBoxesB = S::kBoxesB, kAccs = S::kAccs;
+    constexpr uint32_t kStageBytes = S::kStageBytes;
+    constexpr int kCols = TN / kGroups;                // columns of an epilogue warp
     extern __shared__ unsigned char raw[];
     __shared__ NsShared sh;
     const uint32_t ring = (tc::smem_u32(raw) + 1023u) & ~1023u;
-    const uint32_t halves = ring + kStages * kStageBytes;
     const int warp = threadIdx.x >> 5;
     const uint32_t rank = tc::cluster_rank();
     unsigned *errors = p.d.errors;
@@ -444,17 +457,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNsThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) ptx::mbar_init(&sh.full[i], 1), ptx::mbar_init(&sh.empty[i], 1);
-        // a slot is read by the second block's loader, the first's products and, in both, 2 store and 8 epilogue warps
-        for (int i = 0; i < kSlots; ++i) ptx::mbar_init(&sh.slot_full[i], 1), ptx::mbar_init(&sh.slot_empty[i], 22);
-        for (int i = 0; i < 2; ++i) ptx::mbar_init(&sh.acc_full[i], 1), ptx::mbar_init(&sh.acc_empty[i], 16);
-        for (int i = 0; i < 2; ++i) ptx::mbar_init(&sh.half_full[i], 1), ptx::mbar_init(&sh.half_done[i], 4);
+        // a slot is read by both loaders, the first block's products and, in both, 16 epilogue warps
+        for (int i = 0; i < kSlots; ++i) {
+            ptx::mbar_init(&sh.slot_full[i], 1), ptx::mbar_init(&sh.slot_go[i], 1);
+            ptx::mbar_init(&sh.slot_empty[i], 3 + 2 * 4 * kGroups);
+        }
+        for (int i = 0; i < kAccs; ++i) ptx::mbar_init(&sh.acc_full[i], 1), ptx::mbar_init(&sh.acc_empty[i], 2 * 4 * kGroups);
         ptx::mbar_init(&sh.drain, 1);
         sh.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
         __syncwarp();
-        tc::tmem_alloc(&sh.tmem, kTmemCols);
+        tc::tmem_alloc(&sh.tmem, 512);
     }
     tc::fence_before_sync();
     __syncthreads();
@@ -462,60 +477,67 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNsThreads, 1)
     tc::fence_after_sync();
     const uint32_t tmem = sh.tmem;
 
-    if (threadIdx.x == 0) {
-        // ---- tiles (first block) and loads
+    if (threadIdx.x == 32 && rank == 1) {
+        // ---- tiles, a few ahead: drawing and describing one takes 2 us of dependent reads
+        for (uint32_t n = 0;; ++n) {
+            const int slot = n % kSlots;
+            if (n >= kSlots && !tc::pair_wait(&sh.slot_empty[slot], (n / kSlots - 1) & 1u, abort, errors)) break;
+            const uint32_t ticket = atomicAdd(p.d.ticket, 1u);
+            Tile t{};
+            uint32_t need = 0;
+            t.phase = kNoMore;
+            if (ticket < p.total) describe(p, ticket, t, need);
+            const uint32_t there = tc::map_to(tc::smem_u32(&sh.slot[slot]), 0);
+            sh.slot[slot] = t;
+#pragma unroll
+            for (int i = 0; i < kTileWords; ++i) tc::st_cluster(there + 16 * i, reinterpret_cast<const uint4 *>(&t)[i]);
+            tc::arrive_cluster(tc::map_to(tc::smem_u32(&sh.slot_full[slot]), 0));
+            tc::arrive_cluster(tc::map_to(tc::smem_u32(&sh.slot_full[slot]), 1));
+            if (t.phase == kNoMore || !wait_parts(&p.d.done[t.mat], need, abort, errors)) break;
+            tc::arrive_cluster(tc::map_to(tc::smem_u32(&sh.slot_go[slot]), 0));
+            tc::arrive_cluster(tc::map_to(tc::smem_u32(&sh.slot_go[slot]), 1));
+        }
+    } else if (threadIdx.x == 0) {
+        // ---- loads
         uint32_t issued = 0;
         for (uint32_t n = 0;; ++n) {
             const int slot = n % kSlots;
-            Tile t{};
-            if (rank == 0) {
-                if (n >= kSlots && !tc::pair_wait(&sh.slot_empty[slot], (n / kSlots - 1) & 1u, abort, errors)) break;
-                const uint32_t ticket = atomicAdd(p.d.ticket, 1u);
-                t.phase = kNoMore;
-                if (ticket < p.total) {
-                    t.iter = ticket / p.d.work_per_iter;
-                    const uint2 w = p.d.work[ticket - t.iter * p.d.work_per_iter];
-                    t.mat = w.x & 0x3FFFFFFFu;
-                    t.phase = w.x >> 30;
-                    t.ti = w.y & 0xFFFFu;
-                    t.tj = w.y >> 16;
-                    const MuonMat &m = p.d.mats[t.mat];
-                    uint32_t need = t.iter * (m.parts[0] + m.parts[1] + m.parts[2]);
-                    if (t.phase > 0) need += m.parts[0];
-                    if (t.phase > 1) need += m.parts[1];
-                    if (!wait_parts(&p.d.done[t.mat], need, abort, errors)) break;
-                }
-                const uint4 v = pack_tile(t);
-                sh.slot[slot] = v;
-                tc::st_cluster(tc::map_to(tc::smem_u32(&sh.slot[slot]), 1), v);
-                tc::arrive_cluster(tc::map_to(tc::smem_u32(&sh.slot_full[slot]), 1));
-                tc::arrive_cluster(tc::map_to(tc::smem_u32(&sh.slot_full[slot]), 0));
-            } else {
-                if (!tc::pair_wait(&sh.slot_full[slot], (n / kSlots) & 1u, abort, errors)) break;
-                t = unpack_tile(sh.slot[slot]);
-                tc::arrive_cluster(tc::map_to(tc::smem_u32(&sh.slot_empty[slot]), 0));
-            }
+            if (!tc::pair_wait(&sh.slot_full[slot], (n / kSlots) & 1u, abort, errors)) break;
+            const Tile &t = sh.slot[slot];
             if (t.phase == kNoMore) break;
+            tc::prefetch_map(p.d.maps + t.map_a);
+            tc::prefetch_map(p.d.maps + t.map_b);
+            if (!tc::pair_wait(&sh.slot_go[slot], (n / kSlots) & 1u, abort, errors)) break;
             tc::fence_proxy_async_all();   // other blocks' results, before the loads below
-            const Product w(p.d, t);
-            const int row = (int)(t.ti * kNsTileM + rank * 128), col = (int)(t.tj * kNsTileN + rank * 64);
+            const int row = (int)(t.row + rank * 128), col = (int)(t.col + rank * (TN / 2));
+            const uint32_t k_end = t.k, a_turn = t.a_turn, b_turn = t.b_turn, diag = t.diag;
+            const CUtensorMap *map_a = p.d.maps + t.map_a, *map_b = p.d.maps + t.map_b, *map_d = p.d.maps + diag;
+            tc::arrive_cluster(tc::map_to(tc::smem_u32(&sh.slot_empty[slot]), 1));
             bool ok = true;
-            for (uint32_t k0 = 0; k0 < w.k; k0 += kNsTileK) {
+            for (uint32_t k0 = 0; k0 < k_end; k0 += kNsTileK) {
                 const uint32_t stage = issued % kStages;
                 if (issued >= kStages) ok = tc::pair_wait(&sh.empty[stage], (issued / kStages - 1) & 1u, abort, errors);
                 if (!ok) break;
                 if (rank == 0) ptx::mbar_arrive_expect_tx(&sh.full[stage], 2 * kStageBytes);
                 const uint32_t bar = tc::map_to(tc::smem_u32(&sh.full[stage]), 0);
                 const uint32_t dst = ring + stage * kStageBytes;
-                const bool a_mn = k0 < w.a_turn, b_mn = k0 < w.b_turn;
+                const bool a_mn = k0 < a_turn, b_mn = k0 < b_turn;
                 const int k = (int)k0;
+                const bool on_diag = diag != 0 && k0 - b_turn < kNsRows;
+                const CUtensorMap *mb = on_diag ? map_d : map_b;
+                const int kb = on_diag ? (int)(k0 - b_turn) : k;
 #pragma unroll
                 for (int plane = 0; plane < 2; ++plane) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        tc::tma_box_pair(dst + (2 * plane + h) * kBox, w.a, a_mn ? row + 64 * h : k,
-                                         a_mn ? k : row + 64 * h, plane, bar);
-                    tc::tma_box_pair(dst + (4 + plane) * kBox, w.b, b_mn ? col : k, b_mn ? k : col, plane, bar);
+                    for (int i = 0; i < 2; ++i) {
+                        const int r = row + 64 * i;
+                        tc::tma_box_pair(dst + (2 * plane + i) * kBox, map_a, a_mn ? r : k, a_mn ? k : r, plane, bar);
+                    }
+#pragma unroll
+                    for (int i = 0; i < kBoxesB; ++i) {
+                        const int c = col + 64 * i;
+                        tc::tma_box_pair(dst + (4 + kBoxesB * plane + i) * kBox, mb, b_mn ? c : kb, b_mn ? kb : c, plane, bar);
+                    }
                 }
                 ++issued;
             }
@@ -529,37 +551,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNsThreads, 1)
         for (uint32_t n = 0; ok; ++n) {
             const int slot = n % kSlots;
             if (!(ok = tc::pair_wait(&sh.slot_full[slot], (n / kSlots) & 1u, abort, errors))) break;
-            const Tile t = unpack_tile(sh.slot[slot]);
-            tc::arrive_cluster(tc::map_to(tc::smem_u32(&sh.slot_empty[slot]), 0));
-            if (t.phase == kNoMore) break;
-            const Product w(p.d, t);
-            for (uint32_t k0 = 0; k0 < w.k; k0 += kNsTileK) {
-                const uint32_t acc = used & 1u, d = tmem + acc * kNsTileN, e = tmem + (2 + (n & 1u)) * kNsTileN;
-                const bool first = k0 % kAccK == 0;
-                if (first && used >= 2) {
-                    if (!(ok = tc::pair_wait(&sh.acc_empty[acc], (used / 2 - 1) & 1u, abort, errors))) break;
+            const uint32_t phase = sh.slot[slot].phase, k_end = sh.slot[slot].k;
+            const uint32_t a_turn = sh.slot[slot].a_turn, b_turn = sh.slot[slot].b_turn;
+            tc::arrive_cluster(tc::map_to(tc::smem_u32(&sh.slot_empty[slot]), 1));
+            if (phase == kNoMore) break;
+            for (uint32_t k0 = 0; k0 < k_end; k0 += kNsTileK) {
+                const uint32_t acc = used % kAccs, d = tmem + acc * TN;
+                const bool first = starts_sum<TN>(k0);
+                if (first && used >= kAccs) {
+                    if (!(ok = tc::pair_wait(&sh.acc_empty[acc], (used / kAccs - 1) & 1u, abort, errors))) break;
                     tc::fence_after_sync();
                 }
                 const uint32_t stage = taken % kStages;
                 if (!(ok = tc::pair_wait(&sh.full[stage], (taken / kStages) & 1u, abort, errors))) break;
                 tc::fence_after_sync();
-                const bool a_mn = k0 < w.a_turn, b_mn = k0 < w.b_turn;
-                const uint32_t idesc = tc::instr_desc(kNsTileM, kNsTileN, a_mn, b_mn);
+                const bool a_mn = k0 < a_turn, b_mn = k0 < b_turn;
+                const uint32_t idesc = tc::instr_desc(kNsRows, TN, a_mn, b_mn);
                 const uint64_t astep = tc::k16_step(a_mn), bstep = tc::k16_step(b_mn);
                 const uint32_t src = ring + stage * kStageBytes;
                 const uint64_t ah = tc::smem_desc(src, a_mn), al = tc::smem_desc(src + 2 * kBox, a_mn);
-                const uint64_t bh = tc::smem_desc(src + 4 * kBox, b_mn), bl = tc::smem_desc(src + 5 * kBox, b_mn);
-                // hi*hi and the two small products gather apart, which leaves a third as many additions to
-                // the large sum
+                const uint64_t bh = tc::smem_desc(src + 4 * kBox, b_mn), bl = tc::smem_desc(src + (4 + kBoxesB) * kBox, b_mn);
+                // the small products first: what is cut off goes by the size of the sum so far
 #pragma unroll
                 for (int j = 0; j < kNsTileK / 16; ++j) {
-                    tc::mma_f16(d, ah + j * astep, bh + j * bstep, idesc, !first || j > 0);
-                    tc::mma_f16(e, ah + j * astep, bl + j * bstep, idesc, k0 + j > 0);
-                    tc::mma_f16(e, al + j * astep, bh + j * bstep, idesc, true);
+                    tc::mma_f16(d, ah + j * astep, bl + j * bstep, idesc, !first || j > 0);
+                    tc::mma_f16(d, al + j * astep, bh + j * bstep, idesc, true);
                 }
+#pragma unroll
+                for (int j = 0; j < kNsTileK / 16; ++j) tc::mma_f16(d, ah + j * astep, bh + j * bstep, idesc, true);
                 tc::mma_commit(&sh.empty[stage]);
                 ++taken;
-                if (k0 + kNsTileK >= w.k || (k0 + kNsTileK) % kAccK == 0) {
+                if (k0 + kNsTileK >= k_end || starts_sum<TN>(k0 + kNsTileK)) {
                     tc::mma_commit(&sh.acc_full[acc]);
                     ++used;
                 }
@@ -571,135 +593,113 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNsThreads, 1)
             while (!ptx::mbar_test(&sh.drain, 0) && ptx::global_ns() - t0 < ptx::kWaitLimitNs) {
             }
         }
-    } else if ((warp == 2 || warp == 3) && (threadIdx.x & 31) == 0) {
-        // ---- a column half's memory: the term to be added in, the result out
-        const int half = warp - 2;
-        const uint32_t mem = halves + half * kHalfBytes;
-        for (uint32_t n = 0;; ++n) {
-            const int slot = n % kSlots;
-            if (!tc::pair_wait(&sh.slot_full[slot], (n / kSlots) & 1u, abort, errors)) break;
-            const Tile t = unpack_tile(sh.slot[slot]);
-            tc::arrive_cluster(tc::map_to(tc::smem_u32(&sh.slot_empty[slot]), 0));
-            if (t.phase == kNoMore) break;
-            const MuonMat &m = p.d.mats[t.mat];
-            const CUtensorMap *maps = p.d.maps + (uint64_t)t.mat * kMapsPerMat;
-            const int row = (int)(t.ti * kNsTileM + rank * 128), col = (int)(t.tj * kNsTileN + half * 64);
-            if (t.phase > 0) {
-                const CUtensorMap *add = t.phase == 1 ? maps + kMapA : maps + (t.iter & 1 ? kMapX1 : kMapX0);
-                tc::fence_proxy_async_all();
-                ptx::mbar_arrive_expect_tx(&sh.half_full[half], kHalfBytes);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    tc::tma_box(mem + i * kBox, add, col, row + 64 * (i & 1), i >> 1, &sh.half_full[half]);
-            } else {
-                ptx::mbar_arrive(&sh.half_full[half]);
-            }
-            if (!tc::pair_wait(&sh.half_done[half], n & 1u, abort, errors)) break;
-            const bool last = t.phase == 2 && (int)t.iter + 1 == p.steps;
-            const int rows = (int)(t.phase < 2 ? m.s : m.rows), cols = (int)(t.phase < 2 ? m.s : m.cols);
-            const CUtensorMap *out = maps + (t.phase == 0 ? kMapA : t.phase == 1 ? kMapB : last ? kMapOut
-                                             : t.iter & 1 ? kMapX0 : kMapX1);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int y = row + 64 * (i & 1), x = last ? col + 32 * (i >> 1) : col;
-                if (y < rows && x < cols) tc::tma_store_box(out, x, y, last ? 0 : i >> 1, mem + i * kBox);
-            }
-            ptx::tma_commit();
-            ptx::tma_wait_all();
-            tc::fence_proxy_async_all();
-            tc::red_release_add(&p.d.done[t.mat], 1u);
-        }
-    } else if (warp >= 4) {
-        // ---- finished tiles: this block's 128 rows, 64 columns to each half
-        const int half = (warp - 4) >> 2;
+    } else if (warp >= 2) {
+        // ---- finished tiles: this block's 128 rows, kCols columns to each group
+        const int group = (warp - 2) >> 2;
         const uint32_t r = (uint32_t)(warp & 3) * 32 + (threadIdx.x & 31);
-        const uint32_t line = halves + half * kHalfBytes + r * 128, turn = r & 7;   // this thread's row, its swizzle
-        const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+        const uint32_t at = tmem + ((uint32_t)(warp & 3) << 21) + group * kCols;
+        const uint32_t mem = ring + kStages * kStageBytes + (warp - 2) * kWarpOut;
         const bool leader = (threadIdx.x & 31) == 0;
-        uint32_t used = 0;   // accumulators
+        uint32_t used = 0;            // accumulators
+        unsigned *owed = nullptr;     // a tile's counter that this warp has not added to yet
+        // this warp's results, then its arrival: ordered for loads (TMA) by any block
+        const auto settle = [&]() {
+            if (owed) {
+                tc::fence_proxy_async_all();
+                __syncwarp();
+                if (leader) tc::red_release_add(owed, 1u);
+                owed = nullptr;
+            }
+        };
         for (uint32_t n = 0;; ++n) {
             const int slot = n % kSlots;
+            // Waiting for the writes to land may come in the next tile's time if its operands are there already;
+            // else that tile may be waiting for this one.
+            if (!__all_sync(~0u, tc::pair_peek(&sh.slot_go[slot], (n / kSlots) & 1u))) settle();
             if (!__all_sync(~0u, tc::pair_wait(&sh.slot_full[slot], (n / kSlots) & 1u, abort, errors))) break;
-            const Tile t = unpack_tile(sh.slot[slot]);
-            __syncwarp();
-            if (leader) tc::arrive_cluster(tc::map_to(tc::smem_u32(&sh.slot_empty[slot]), 0));
-            if (t.phase == kNoMore) break;
-            const MuonMat &m = p.d.mats[t.mat];
-            const uint32_t sums = ((t.phase == 0 ? (m.tall ? m.rows : m.cols) : m.s) + kAccK - 1) / kAccK;
-            float w[64];
+            const Tile &t = sh.slot[slot];
+            const uint32_t phase = t.phase, sums = sums_of<TN>(t.k);
+            if (phase == kNoMore) break;
+            float w[kCols];
+#pragma unroll
+            for (int q = 0; q < kCols; ++q) w[q] = 0.f;
             bool ok = true;
             for (uint32_t i = 0; i < sums; ++i, ++used) {
-                const uint32_t acc = used & 1u;
-                ok = __all_sync(~0u, tc::pair_wait(&sh.acc_full[acc], (used / 2) & 1u, abort, errors));
+                const uint32_t acc = used % kAccs;
+                ok = __all_sync(~0u, tc::pair_wait(&sh.acc_full[acc], (used / kAccs) & 1u, abort, errors));
                 if (!ok) break;
                 tc::fence_after_sync();
-const uint32_t at = tmem + lanes + half * 64;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
+                for (int q = 0; q < kCols / 16; ++q) {
                     float x[16];
-                    tc::tmem_load16(x, at + acc * kNsTileN + q * 16);
+                    tc::tmem_load16(x, at + acc * TN + q * 16);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) w[16 * q + j] = i == 0 ? x[j] : w[16 * q + j] + x[j];
-                }
-                if (i + 1 == sums) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        float x[16];
-                        tc::tmem_load16(x, at + (2 + (n & 1u)) * kNsTileN + q * 16);
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) w[16 * q + j] += x[j];
-                    }
+                    for (int j = 0; j < 16; ++j) w[16 * q + j] += x[j];
                 }
                 tc::fence_before_sync();
                 __syncwarp();
-                if (leader) tc::arrive_cluster(tc::map_to(tc::smem_u32(&sh.acc_empty[acc]), 0));
+                if (leader) tc::arrive_cluster_relaxed(tc::map_to(tc::smem_u32(&sh.acc_empty[acc]), 0));
+                if (i == 1 || sums == 1) settle();
             }
-            if (!ok || !__all_sync(~0u, tc::pair_wait(&sh.half_full[half], n & 1u, abort, errors))) break;
-            constexpr float inv = 1.0f / kNsScale;
-            const float alpha = alpha_of(t.iter, p.steps);
-            const float f = t.phase == 1 ? p.c * inv : inv;
-            const float k = t.phase == 1 ? p.b + 2.f * p.c * alpha : p.a + alpha * (p.b + alpha * p.c);
-#pragma unroll
-            for (int q = 0; q < 64; ++q) w[q] *= f;
-            if (t.phase > 0) {
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const uint32_t piece = (q ^ turn) * 16;
-                    add8(w + 8 * q, k, tc::ld_shared(line + piece), tc::ld_shared(line + 2 * kBox + piece));
-                }
-            } else if (alpha != 0.f) {   // A' = A - alpha I
-                const uint32_t diagonal = t.ti * kNsTileM + rank * 128 + r - (t.tj * kNsTileN + half * 64);
-#pragma unroll
-                for (uint32_t q = 0; q < 64; ++q)
-                    if (q == diagonal) w[q] -= alpha * kNsScale;
-            }
-            const bool last = t.phase == 2 && (int)t.iter + 1 == p.steps;
-            if (!last) {
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    __half h[8], l[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) split(w[8 * q + i], h[i], l[i]);
-                    const uint32_t piece = (q ^ turn) * 16;
-                    tc::st_shared(line + piece, make_uint4(pack(h[0], h[1]), pack(h[2], h[3]), pack(h[4], h[5]), pack(h[6], h[7])));
-                    tc::st_shared(line + 2 * kBox + piece,
-                                  make_uint4(pack(l[0], l[1]), pack(l[2], l[3]), pack(l[4], l[5]), pack(l[6], l[7])));
-                }
-            } else {   // the result, fp32 and unscaled: 32 columns where the high parts were, 32 where the low parts were
-#pragma unroll
-                for (int q = 0; q < 16; ++q) {
-                    const float *v = w + 4 * q;
-                    tc::st_shared(line + (q >> 3) * 2 * kBox + ((q & 7) ^ turn) * 16,
-                                  make_uint4(__float_as_uint(v[0] * inv), __float_as_uint(v[1] * inv),
-                                             __float_as_uint(v[2] * inv), __float_as_uint(v[3] * inv)));
-                }
-            }
-            ptx::fence_proxy_async_smem();
+            if (!ok) break;
+            const uint32_t col = t.col + group * kCols, row = t.row + rank * 128 + r, row0 = row - (r & 31);
+            const uint32_t here = t.rows - row0;   // this warp's rows, 32 or the last of the matrix
+            const uint32_t pitch = t.pitch, diagonal = row - col;
+            const bool any = col < t.cols && row0 < t.rows, last = t.last;
+            const bool meets = phase < 2 && t.row == t.col / kNsRows * kNsRows;
+            unsigned char *out = t.out + (uint64_t)row0 * pitch + col * (last ? 4 : 2);
+            unsigned char *also = t.also ? t.also + (uint64_t)row0 * (kNsRows * 2) + (col - t.row) * 2 : nullptr;
+            const uint64_t plane = t.plane, also_plane = t.also_plane;
+            const float f = t.factor, more = t.on_diagonal, v = t.v;
+            owed = &p.d.done[t.mat];
             __syncwarp();
-            if (leader) ptx::mbar_arrive(&sh.half_done[half]);
+            // before the writes: the arrival would wait for them
+            if (leader) tc::arrive_cluster(tc::map_to(tc::smem_u32(&sh.slot_empty[slot]), 1));
+            if (any) {
+#pragma unroll
+                for (uint32_t q = 0; q < kCols; ++q) w[q] *= f;
+                float own = 0.f;   // where this row meets the diagonal
+                if (meets) {
+#pragma unroll
+                    for (uint32_t q = 0; q < kCols; ++q) {
+                        w[q] += q == diagonal ? more : 0.f;
+                        own = q == diagonal ? w[q] : own;
+                    }
+                }
+                if (last) {
+#pragma unroll
+                    for (int q = 0; q < kCols / 16; ++q) {
+                        turn_in(mem, reinterpret_cast<const uint32_t *>(w + 16 * q));
+                        turn_out(mem, out + 64 * q, pitch, here);
+                    }
+                } else {
+#pragma unroll
+                    for (int q = 0; q < kCols / 32; ++q) {
+                        uint32_t hi[16], lo[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) split(w[32 * q + 2 * i], w[32 * q + 2 * i + 1], hi[i], lo[i]);
+#pragma unroll
+                        for (int part = 0; part < 2; ++part) {
+                            turn_in(mem, part ? lo : hi);
+                            turn_out(mem, out + part * plane + 64 * q, pitch, here);
+                            if (also) {
+                                if ((diagonal >> 5) == (uint32_t)q) {
+                                    uint32_t own_hi, own_lo;
+                                    split(own + v, 0.f, own_hi, own_lo);
+                                    tc::st_shared16(turned(mem, r & 31, (diagonal & 31) >> 3) + (diagonal & 7) * 2,
+                                                    (uint16_t)(part ? own_lo : own_hi));
+                                }
+                                __syncwarp();
+                                turn_out(mem, also + part * also_plane + 64 * q, kNsRows * 2, here);
+                            }
+                        }
+                    }
+                }
+            }
         }
+        if (!*abort) settle();
     }
-    if (*abort) {   // give copies that nothing above waits for (the second block's loads, a half's term) 1 ms to land
+    if (*abort) {   // give copies that nothing above waits for (the second block's loads) 1 ms to land
         const unsigned long long t0 = ptx::global_ns();
         while (ptx::global_ns() - t0 < 1000000ull) {
         }
@@ -711,7 +711,7 @@ const uint32_t at = tmem + lanes + half * 64;
     __syncthreads();
     ptx::cluster_sync();
     tc::fence_after_sync();
-    if (warp == 1) tc::tmem_free(tmem, kTmemCols);
+    if (warp == 1) tc::tmem_free(tmem, 512);
 }
 
 template <int CAP>
@@ -722,11 +722,8 @@ cudaError_t momentum_t(const MuonDev &d, const MuonScalars &sc, const void *cons
     for (int r = 0; r < world; ++r) p.grads[r] = static_cast<const uint16_t *>(grads[r]);
     p.d = d;
     p.momentum = momentum;
-    p.inv_w = sc.inv_w;
-    p.mu = sc.momentum;
-    p.omm = sc.one_minus_momentum;
     p.world = world;
-    p.nesterov = sc.nesterov;
+    p.sc = sc;
     muon_momentum_kernel<CAP><<<grid, kElemThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }
@@ -783,10 +780,17 @@ cudaError_t launch_muon_split(const MuonDev &d, const MuonScalars &sc, const voi
     return cudaGetLastError();
 }
 
+template <int TN>
+static cudaError_t iterate_t(const NsParams &p, uint32_t grid, cudaStream_t stream)
+{
+    const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(muon_iterate_kernel<TN>), Shape<TN>::kSmem);
+    if (e != cudaSuccess) return e;
+    muon_iterate_kernel<TN><<<grid, kNsThreads, Shape<TN>::kSmem, stream>>>(p);
+    return cudaGetLastError();
+}
+
 cudaError_t launch_muon_iterate(const MuonDev &d, const MuonScalars &sc, int num_sms, cudaStream_t stream)
 {
-    const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(muon_iterate_kernel), kNsSmem);
-    if (e != cudaSuccess) return e;
     NsParams p{};
     p.d = d;
     p.a = sc.a;
@@ -796,8 +800,7 @@ cudaError_t launch_muon_iterate(const MuonDev &d, const MuonScalars &sc, int num
     p.total = d.work_per_iter * (uint32_t)sc.steps;
     const uint32_t pairs = (uint32_t)num_sms / 2;
     const uint32_t grid = 2 * (p.total < pairs ? p.total : pairs);
-    muon_iterate_kernel<<<grid, kNsThreads, kNsSmem, stream>>>(p);
-    return cudaGetLastError();
+    return d.tile == 256 ? iterate_t<256>(p, grid, stream) : iterate_t<128>(p, grid, stream);
 }
 
 cudaError_t launch_muon_apply(const MuonDev &d, const MuonScalars &sc, void *const *params, int world, float *master,

@@ -16,20 +16,9 @@ using ptx::smem_u32;
 
 // ------------------------------------------------------------ tiled TMA
 
-// Box of a 3-D tensor map (x fastest) into shared memory; completion bytes
-// are counted on `bar` of this block.  x times the element size is a
-// multiple of 16 bytes.
-__device__ __forceinline__ void tma_box(uint32_t smem_dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
-        "[%5];" ::"r"(smem_dst),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-        : "memory");
-}
-
-// The same for a block of a pair: the bytes are counted on a barrier of
-// either block, given by its cluster address.
+// Box of a 3-D tensor map (x fastest) into shared memory of this block of a
+// pair; its bytes are counted on a barrier of either block, given by its
+// cluster address.  x times the element size is a multiple of 16 bytes.
 __device__ __forceinline__ void tma_box_pair(uint32_t smem_dst, const CUtensorMap *map, int x, int y, int z,
                                              uint32_t cluster_bar)
 {
@@ -40,13 +29,9 @@ __device__ __forceinline__ void tma_box_pair(uint32_t smem_dst, const CUtensorMa
         : "memory");
 }
 
-// Box from shared memory to a 3-D tensor map, in this thread's bulk group;
-// what lies outside the tensor is not written.
-__device__ __forceinline__ void tma_store_box(const CUtensorMap *map, int x, int y, int z, uint32_t smem_src)
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
 {
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
-                 "r"(x), "r"(y), "r"(z), "r"(smem_src)
-                 : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
 // Order generic-proxy accesses of global memory before later async-proxy
@@ -89,6 +74,13 @@ __device__ __forceinline__ void arrive_cluster(uint32_t cluster_bar)
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
+// The same without ordering this thread's writes before it (which would wait
+// for its stores to global memory).
+__device__ __forceinline__ void arrive_cluster_relaxed(uint32_t cluster_bar)
+{
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
 __device__ __forceinline__ void st_cluster(uint32_t cluster_addr, uint4 v)
 {
     asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "r"(v.x), "r"(v.y), "r"(v.z),
@@ -103,6 +95,19 @@ __device__ __forceinline__ bool pair_test(uint64_t *bar, uint32_t parity)
     uint32_t ok;
     asm volatile(
         "{ .reg .pred q; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 q, [%1], %2; selp.u32 %0, 1, 0, q; }"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// The same without waiting at all (try_wait above may suspend the thread for
+// some microseconds before it answers no).
+__device__ __forceinline__ bool pair_peek(uint64_t *bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{ .reg .pred q; mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 q, [%1], %2; selp.u32 %0, 1, 0, q; }"
         : "=r"(ok)
         : "r"(smem_u32(bar)), "r"(parity)
         : "memory");
@@ -191,7 +196,10 @@ __device__ __forceinline__ void tmem_load16(float v[16], uint32_t addr)
 __device__ __forceinline__ uint4 ld_shared(uint32_t addr)
 {
     uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
     return v;
 }
 
@@ -201,16 +209,47 @@ __device__ __forceinline__ void st_shared(uint32_t addr, uint4 v)
                  : "memory");
 }
 
+__device__ __forceinline__ void st_shared16(uint32_t addr, uint16_t v)
+{
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
+}
+
+// The same for one block by itself (cta_group::1).
+__device__ __forceinline__ void tmem_alloc1(uint32_t *smem_slot, uint32_t cols)
+{
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(smem_slot)),
+                 "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free1(uint32_t addr, uint32_t cols)
+{
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void mma1_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate)
+{
+    asm volatile(
+        "{ .reg .pred p; setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma1_commit(uint64_t *bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+
 // Shared-memory operand descriptor, 128-byte swizzle, tiles made of boxes of
-// 64 f16 (128 bytes) by 64 rows, each 8 KB:
+// 64 f16 (128 bytes) by 64 or 128 rows, `box` bytes each:
 //   K-major:  the box's rows are M (or N) and its columns K; 8-row groups
 //             follow at 1024 bytes (SBO), K within one box (LBO unused);
 //   MN-major: the box's rows are K and its columns M (or N); 8-row groups of
 //             K follow at 1024 bytes (SBO), the next 64 of M (or N) one box
-//             further at 8192 bytes (LBO).
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, bool mn_major)
+//             further (LBO).
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, bool mn_major, uint32_t box = 8192)
 {
-    const uint64_t lbo = mn_major ? (8192u >> 4) : 1u;
+    const uint64_t lbo = mn_major ? (box >> 4) : 1u;
     return (uint64_t)((addr & 0x3FFFFu) >> 4) | (lbo << 16) | ((uint64_t)(1024u >> 4) << 32) | (1ull << 46) |
            (2ull << 61);
 }

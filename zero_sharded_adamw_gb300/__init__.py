@@ -217,6 +217,7 @@ class PtrTable:
 # and element size in bytes.
 _KINDS = {"bf16": ("torch.bfloat16", 2), "f32": ("torch.float32", 4)}
 _DTYPE_NAMES: dict = {}    # torch dtype -> its name (naming one takes longer than the other checks together)
+_TORCH_DTYPES: dict = {}   # element kind -> torch dtype, as they are met
 
 
 def _dtype_name(x) -> str:
@@ -224,7 +225,20 @@ def _dtype_name(x) -> str:
     name = _DTYPE_NAMES.get(d)
     if name is None:
         name = _DTYPE_NAMES[d] = str(d)
+        _TORCH_DTYPES.update({kind: d for kind, (want, _) in _KINDS.items() if want == name})
     return name
+
+
+def _take(x, count: int, kind: str, what: str) -> int | None:
+    """Address of device buffer `x` after _check_buffer, whose tests an
+    ordinary CUDA tensor passes here in one line."""
+    try:
+        if x.dtype is _TORCH_DTYPES[kind] and x.is_cuda and x.is_contiguous() and x.numel() >= count:
+            return x.data_ptr()
+    except (AttributeError, KeyError):
+        pass
+    _check_buffer(x, count, kind, True, what)
+    return _addr(x)
 
 
 def _check_buffer(x, count: int, kind: str, on_device: bool | None, what: str) -> None:
@@ -272,6 +286,8 @@ def _ptrs(xs, world: int | None = None, count: int | None = None, kind: str | No
                 xs._checked.add(key)
         return xs.array
     if count is not None and kind is not None:
+        if on_device:
+            return (C.c_void_p * n)(*[_take(x, count, kind, what) for x in xs])
         for r, x in enumerate(xs):
             _check_buffer(x, count, kind, on_device, f"{what}[{r}]")
     return (C.c_void_p * n)(*[_addr(x) for x in xs])
@@ -579,12 +595,11 @@ def zero1_muon_step(h: int, grad_ptrs, param_ptrs, master, momentum, stream=None
     """One step of the handle's matrices; master and momentum (fp32) are the
     caller's and are updated in place."""
     n, world = _muon_info(h)
-    if n is not None:
-        _check_buffer(master, n, "f32", True, "master")
-        _check_buffer(momentum, n, "f32", True, "momentum")
+    master = _addr(master) if n is None else _take(master, n, "f32", "master")
+    momentum = _addr(momentum) if n is None else _take(momentum, n, "f32", "momentum")
     _check(_load().zero1_muon_step(h, _ptrs(grad_ptrs, world, n, "bf16", True, "grads"),
-                                   _ptrs(param_ptrs, world, n, "bf16", True, "params"), _addr(master),
-                                   _addr(momentum), _stream(stream)))
+                                   _ptrs(param_ptrs, world, n, "bf16", True, "params"), master, momentum,
+                                   _stream(stream)))
 
 
 _KIND_OF = {DTYPE_BF16: "bf16", DTYPE_F32: "f32"}
@@ -593,11 +608,9 @@ _KIND_OF = {DTYPE_BF16: "bf16", DTYPE_F32: "f32"}
 def zero1_muon_orthogonalize(h: int, src, src_dtype: int, dst, dst_dtype: int, stream=None) -> None:
     """dst = the orthogonalised matrices of the flat buffer src."""
     n = _muon_info(h)[0]
-    if n is not None:
-        for x, dtype, what in ((src, src_dtype, "src"), (dst, dst_dtype, "dst")):
-            if dtype in _KIND_OF:
-                _check_buffer(x, n, _KIND_OF[dtype], True, what)
-    _check(_load().zero1_muon_orthogonalize(h, _addr(src), src_dtype, _addr(dst), dst_dtype, _stream(stream)))
+    a, b = (_addr(x) if n is None or dtype not in _KIND_OF else _take(x, n, _KIND_OF[dtype], what)
+            for x, dtype, what in ((src, src_dtype, "src"), (dst, dst_dtype, "dst")))
+    _check(_load().zero1_muon_orthogonalize(h, a, src_dtype, b, dst_dtype, _stream(stream)))
 
 
 def zero1_muon_set_lr(h: int, lr: float) -> None:
@@ -667,40 +680,43 @@ class Muon:
 
 # --------------------------------------------------------- layer norm
 
-def _check_rows(x, rows: int, cols: int, ld: int, dtype: int, what: str) -> None:
-    """Raise Zero1ArgumentError unless the torch tensor `x` is CUDA memory of
-    the type and, where it describes rows itself, lies as (rows, cols, ld) say
-    and reaches as far as the call reads or writes.  Raw addresses pass."""
-    if x is None or isinstance(x, int) or not hasattr(x, "data_ptr"):
-        return
-    want = _KINDS[_KIND_OF[dtype]][0] if dtype in _KIND_OF else None
-    if want is not None and _dtype_name(x) != want:
-        raise Zero1ArgumentError(f"{what}: expected {want}, got {x.dtype}")
-    if not x.is_cuda:
-        raise Zero1ArgumentError(f"{what}: expected a CUDA tensor, got {x.device}")
-    shape = x.shape
-    if len(shape) == 2 and shape[0] == rows and shape[1] == cols and x.stride() == (ld, 1) or rows == 0:
-        return
-    if len(shape) > 1 and x.stride(-1) != 1 and shape[-1] > 1:
-        raise Zero1ArgumentError(f"{what}: the entries of a row must be adjacent")
-    held = x.untyped_storage().nbytes() // x.element_size() - x.storage_offset()
-    if held < (rows - 1) * ld + cols:
-        raise Zero1ArgumentError(f"{what}: its memory holds {held} elements, the call reads or writes "
-                                 f"{(rows - 1) * ld + cols}")
+def _take_rows(x, rows: int, cols: int, ld: int, kind: str | None, what: str) -> int | None:
+    """Address of `x`, after refusing a torch tensor that is not CUDA memory of
+    the type or does not reach as far as rows `ld` apart do.  Raw addresses
+    pass."""
+    try:
+        if x.dtype is _TORCH_DTYPES[kind] and x.is_cuda and x.shape == (rows, cols) and x.stride() == (ld, 1):
+            return x.data_ptr()
+    except (AttributeError, KeyError):
+        pass
+    if x is not None and hasattr(x, "data_ptr"):
+        want = _KINDS[kind][0] if kind is not None else None
+        if want is not None and _dtype_name(x) != want:
+            raise Zero1ArgumentError(f"{what}: expected {want}, got {x.dtype}")
+        if not x.is_cuda:
+            raise Zero1ArgumentError(f"{what}: expected a CUDA tensor, got {x.device}")
+        if rows:
+            if x.dim() > 1 and x.stride(-1) != 1 and x.shape[-1] > 1:
+                raise Zero1ArgumentError(f"{what}: the entries of a row must be adjacent")
+            held = x.untyped_storage().nbytes() // x.element_size() - x.storage_offset()
+            if held < (rows - 1) * ld + cols:
+                raise Zero1ArgumentError(f"{what}: its memory holds {held} elements, the call reads or writes "
+                                         f"{(rows - 1) * ld + cols}")
+    return _addr(x)
+
+
+def _take_vector(x, count: int, kind: str | None, what: str) -> int | None:
+    return _addr(x) if kind is None else _take(x, count, kind, what)
 
 
 def zero1_layernorm_forward(rows: int, cols: int, dtype: int, x, ldx: int, gamma, beta, eps: float, y, ldy: int,
                             mean, rstd, stream=None) -> None:
     """y = layer norm of x; mean and rstd (fp32, one a row) for the backward pass."""
-    _check_rows(x, rows, cols, ldx, dtype, "x")
-    _check_rows(y, rows, cols, ldy, dtype, "y")
-    if dtype in _KIND_OF:
-        _check_buffer(gamma, cols, _KIND_OF[dtype], True, "gamma")
-        _check_buffer(beta, cols, _KIND_OF[dtype], True, "beta")
-    _check_buffer(mean, rows, "f32", True, "mean")
-    _check_buffer(rstd, rows, "f32", True, "rstd")
-    _check(_load().zero1_layernorm_forward(rows, cols, dtype, _addr(x), ldx, _addr(gamma), _addr(beta), eps, _addr(y),
-                                           ldy, _addr(mean), _addr(rstd), _stream(stream)))
+    kind = _KIND_OF.get(dtype)
+    _check(_load().zero1_layernorm_forward(
+        rows, cols, dtype, _take_rows(x, rows, cols, ldx, kind, "x"), ldx, _take_vector(gamma, cols, kind, "gamma"),
+        _take_vector(beta, cols, kind, "beta"), eps, _take_rows(y, rows, cols, ldy, kind, "y"), ldy,
+        _take(mean, rows, "f32", "mean"), _take(rstd, rows, "f32", "rstd"), _stream(stream)))
 
 
 def zero1_layernorm_workspace(rows: int, cols: int) -> int:
@@ -715,21 +731,16 @@ def zero1_layernorm_backward(rows: int, cols: int, dtype: int, dy, lddy: int, x,
     """dx, and the weight's and bias's gradients summed over all rows (bf16 or
     fp32); `workspace` is a CUDA tensor of at least zero1_layernorm_workspace
     bytes."""
-    for t, ld, what in ((dy, lddy, "dy"), (x, ldx, "x"), (dx, lddx, "dx")):
-        _check_rows(t, rows, cols, ld, dtype, what)
-    if dtype in _KIND_OF:
-        _check_buffer(gamma, cols, _KIND_OF[dtype], True, "gamma")
-    if grad_dtype in _KIND_OF:
-        _check_buffer(dgamma, cols, _KIND_OF[grad_dtype], True, "dgamma")
-        _check_buffer(dbeta, cols, _KIND_OF[grad_dtype], True, "dbeta")
-    _check_buffer(mean, rows, "f32", True, "mean")
-    _check_buffer(rstd, rows, "f32", True, "rstd")
+    kind, grad_kind = _KIND_OF.get(dtype), _KIND_OF.get(grad_dtype)
     if not hasattr(workspace, "numel") or not workspace.is_cuda or not workspace.is_contiguous():
         raise Zero1ArgumentError("workspace: expected a contiguous CUDA tensor")
-    _check(_load().zero1_layernorm_backward(rows, cols, dtype, _addr(dy), lddy, _addr(x), ldx, _addr(gamma),
-                                            _addr(mean), _addr(rstd), _addr(dx), lddx, _addr(dgamma), _addr(dbeta),
-                                            grad_dtype, _addr(workspace),
-                                            workspace.numel() * workspace.element_size(), _stream(stream)))
+    _check(_load().zero1_layernorm_backward(
+        rows, cols, dtype, _take_rows(dy, rows, cols, lddy, kind, "dy"), lddy,
+        _take_rows(x, rows, cols, ldx, kind, "x"), ldx, _take_vector(gamma, cols, kind, "gamma"),
+        _take(mean, rows, "f32", "mean"), _take(rstd, rows, "f32", "rstd"),
+        _take_rows(dx, rows, cols, lddx, kind, "dx"), lddx, _take_vector(dgamma, cols, grad_kind, "dgamma"),
+        _take_vector(dbeta, cols, grad_kind, "dbeta"), grad_dtype, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
 class _CSmPartition(C.Structure):

@@ -73,11 +73,13 @@ __device__ __forceinline__ void row_sum(float &a, float &b, float2 (*shared)[THR
         a += __shfl_xor_sync(~0u, a, o);
         b += __shfl_xor_sync(~0u, b, o);
     }
-    if (TPR > 32) {   // two buffers in turn: one barrier a call
+    if (TPR > 32) {   // two buffers in turn: one barrier a call, of the warps that share the row
+        const uint32_t group = threadIdx.x / TPR;
         float2 *s = shared[turn];
         turn ^= 1;
         if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = make_float2(a, b);
-        __syncthreads();
+        asm volatile("barrier.cta.sync.aligned %0, %1;" ::"r"(1 + group), "n"(TPR) : "memory");
+        s += group * (TPR / 32);
         a = b = 0.f;
 #pragma unroll
         for (int i = 0; i < TPR / 32; ++i) {
@@ -208,8 +210,10 @@ struct BwdParams {
     float inv_n;
 };
 
-template <typename T, int V, int TPR, int NV, int THREADS>
-__global__ void __launch_bounds__(THREADS) zero1_layernorm_bwd_kernel(const __grid_constant__ BwdParams<T> p)
+// AHEAD: the next row's pieces are fetched while this one's are used, where
+// 128 registers hold both and the column sums (blocks of 256, two an SM).
+template <typename T, int V, int TPR, int NV, int THREADS, bool AHEAD>
+__global__ void __launch_bounds__(THREADS, 512 / THREADS) zero1_layernorm_bwd_kernel(const __grid_constant__ BwdParams<T> p)
 {
     constexpr int kRows = THREADS / TPR;      // rows at a time
     __shared__ float2 shared[2][THREADS / 32];
@@ -220,7 +224,6 @@ __global__ void __launch_bounds__(THREADS) zero1_layernorm_bwd_kernel(const __gr
     float ag[NV * V], ab[NV * V];
 #pragma unroll
     for (int i = 0; i < NV * V; ++i) ag[i] = ab[i] = 0.f;
-    // the next row's pieces are fetched while this one's are used
     Piece<T, V> xs[NV], ds[NV];
     float mean = 0.f, rstd = 0.f;
     const uint64_t step = (uint64_t)gridDim.x * kRows;
@@ -237,13 +240,14 @@ __global__ void __launch_bounds__(THREADS) zero1_layernorm_bwd_kernel(const __gr
         mean = p.mean[r];
         rstd = p.rstd[r];
     };
-    if (row < p.rows) load(row);
+    if (AHEAD && row < p.rows) load(row);
     for (; row < p.rows; row += step) {
+        if (!AHEAD) load(row);
         Piece<T, V> xc[NV], dc[NV];
         const float mc = mean, rc = rstd;
 #pragma unroll
         for (int j = 0; j < NV; ++j) xc[j] = xs[j], dc[j] = ds[j];
-        if (row + step < p.rows) load(row + step);
+        if (AHEAD && row + step < p.rows) load(row + step);
         float sg = 0.f, sh = 0.f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -365,26 +369,36 @@ __global__ void __launch_bounds__(kLnThreads) zero1_layernorm_cols_wide_kernel(c
     }
 }
 
-// dgamma and dbeta: the partial rows added in order, 8 groups of them at once.
+// dgamma and dbeta: the partial rows added in order, 32 groups of them at
+// once so that a thread's few reads are all in flight together.
 template <typename G>
-__global__ void __launch_bounds__(256) zero1_layernorm_cols_kernel(const float *partials, int count, uint32_t cols,
-                                                                   G *dgamma, G *dbeta)
+__global__ void __launch_bounds__(1024) zero1_layernorm_cols_kernel(const float *partials, int count, uint32_t cols,
+                                                                    G *dgamma, G *dbeta)
 {
-    __shared__ float s[8][33];
+    __shared__ float s[32][33];
     ptx::grid_dependency_wait();
     const uint32_t lane = threadIdx.x & 31, group = threadIdx.x >> 5;
     const uint64_t c = (uint64_t)blockIdx.x * 32 + lane;   // over dgamma's columns, then dbeta's
     const uint64_t width = 2ull * cols;
     float v = 0.f;
-    if (c < width)
-        for (int i = (int)group; i < count; i += 8) v += partials[(uint64_t)i * width + c];
+    if (c < width) {
+        float x[kMaxPartials / 32];
+#pragma unroll
+        for (int i = 0; i < kMaxPartials / 32; ++i) {
+            const int at = (int)group + 32 * i;
+            x[i] = at < count ? partials[(uint64_t)at * width + c] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < kMaxPartials / 32; ++i) v += x[i];
+    }
     s[group][lane] = v;
     __syncthreads();
-    if (group == 0 && c < width) {
-        v = 0.f;
+    v = s[lane][group];        // warp `group` adds up column `group`
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v += s[i][lane];
-        G *out = c < cols ? dgamma + c : dbeta ? dbeta + (c - cols) : nullptr;
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+    const uint64_t column = (uint64_t)blockIdx.x * 32 + group;
+    if (lane == 0 && column < width) {
+        G *out = column < cols ? dgamma + column : dbeta ? dbeta + (column - cols) : nullptr;
         if (out) {
             Piece<G, 1> w;
             w.set(&v);
@@ -420,15 +434,16 @@ bool fwd_pick(const FwdParams<T> &p, cudaStream_t st)
     const uint32_t n = (p.cols + V - 1) / V;
     if (n <= 32) return fwd<T, V, 32, 1, 256>(p, st);
     if (n <= 64) return fwd<T, V, 32, 2, 256>(p, st);
+    if (n <= 96) return fwd<T, V, 32, 3, 256>(p, st);
     if (n <= 128) return fwd<T, V, 32, 4, 256>(p, st);
     if (n <= 256) return fwd<T, V, 32, 8, 256>(p, st);
     if constexpr (V == 1)
         if (n <= 1024) return fwd<T, V, 32, 32, 256>(p, st);
-    if (n <= 512) return fwd<T, V, 256, 2, 256>(p, st);
+    if (n <= 512) return fwd<T, V, 128, 4, 256>(p, st);
     if (n <= 1024) return fwd<T, V, 256, 4, 256>(p, st);
     if (n <= 2048) return fwd<T, V, 256, 8, 256>(p, st);
     if constexpr (V == 1)
-        if (n <= 8192) return fwd<T, V, 256, 32, 256>(p, st);
+        if (n <= 8192) return fwd<T, V, 512, 16, 512>(p, st);
     return false;
 }
 
@@ -440,37 +455,41 @@ uint64_t partial_rows(uint64_t rows, uint64_t at_once)
     return n < 1 ? 1 : n < (uint64_t)kMaxPartials ? n : kMaxPartials;
 }
 
-template <typename T, int V, int TPR, int NV, int THREADS>
+template <typename T, int V, int TPR, int NV, int THREADS = (TPR > 256 ? TPR : 256), bool AHEAD = true>
 cudaError_t bwd(const BwdParams<T> &p, int *blocks, cudaStream_t st)
 {
     const size_t fold = TPR < THREADS ? (size_t)(THREADS / TPR) * p.cols * sizeof(float) : 0;   // at most 32 KB
     const int n = (int)partial_rows(p.rows, THREADS / TPR);
     *blocks = n < *blocks ? n : *blocks;
-    zero1_layernorm_bwd_kernel<T, V, TPR, NV, THREADS><<<*blocks, THREADS, fold, st>>>(p);
+    zero1_layernorm_bwd_kernel<T, V, TPR, NV, THREADS, AHEAD><<<*blocks, THREADS, fold, st>>>(p);
     return cudaGetLastError();
 }
 
-// The variants by pieces of a row: a warp while a lane holds at most 32
-// entries, then a block, of 512 threads where 256 would need over 100
-// registers each (two rows' pieces and two sums an entry).
+// The variants by pieces of a row: a warp a row while its lanes hold the
+// column sums (a row shared by more warps costs each of them the same
+// shuffles: rows of 768 by three warps took twice the time of one), then
+// blocks.  Single entries of unaligned rows: 8 a lane.
 template <typename T, int V>
 cudaError_t bwd_pick(const BwdParams<T> &p, int *blocks, cudaStream_t st)
 {
     const uint32_t n = (p.cols + V - 1) / V;
-    if (n <= 32) return bwd<T, V, 32, 1, 256>(p, blocks, st);
-    if (n <= 64) return bwd<T, V, 32, 2, 256>(p, blocks, st);
-    if (n <= 128) return bwd<T, V, 32, 4, 256>(p, blocks, st);
-    if constexpr (V < 8) {
-        if (n <= 256) return bwd<T, V, 32, 8, 256>(p, blocks, st);
+    if (n <= 32) return bwd<T, V, 32, 1>(p, blocks, st);
+    if (n <= 64) return bwd<T, V, 32, 2>(p, blocks, st);
+    if (n <= 96) return bwd<T, V, 32, 3>(p, blocks, st);
+    if (n <= 128) return bwd<T, V, 32, 4, 256, V < 8>(p, blocks, st);
+    if constexpr (V == 1) {
+        if (n <= 256) return bwd<T, V, 32, 8>(p, blocks, st);
+        if (n <= 1024) return bwd<T, V, 128, 8>(p, blocks, st);
+        if (n <= 2048) return bwd<T, V, 256, 8>(p, blocks, st);
+        if (n <= 8192) return bwd<T, V, 512, 16, 512, false>(p, blocks, st);
+        return cudaErrorNotSupported;
     } else {
-        if (n <= 256) return bwd<T, V, 256, 1, 256>(p, blocks, st);
+        if (n <= 256) return bwd<T, V, 256, 1>(p, blocks, st);
+        if (n <= 512) return bwd<T, V, 256, 2>(p, blocks, st);
+        if (n <= 1024) return bwd<T, V, 512, 2>(p, blocks, st);
+        if (n <= 2048) return bwd<T, V, 512, 4, 512, false>(p, blocks, st);
+        return cudaErrorNotSupported;
     }
-    if (n <= 512) return bwd<T, V, 256, 2, 256>(p, blocks, st);
-    if (n <= 1024) return bwd<T, V, 512, 2, 512>(p, blocks, st);
-    if (n <= 2048) return bwd<T, V, 512, 4, 512>(p, blocks, st);
-    if constexpr (V == 1)
-        if (n <= 8192) return bwd<T, V, 512, 16, 512>(p, blocks, st);
-    return cudaErrorNotSupported;
 }
 
 template <typename T, int V>
@@ -540,7 +559,7 @@ int backward(uint64_t rows, uint64_t cols, const void *dy, uint64_t lddy, const 
     if (e == cudaSuccess) {
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3((unsigned)((2 * cols + 31) / 32));
-        cfg.blockDim = dim3(256);
+        cfg.blockDim = dim3(1024);
         cfg.stream = st;
         cudaLaunchAttribute attr{};
         attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

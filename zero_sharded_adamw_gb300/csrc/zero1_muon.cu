@@ -182,19 +182,26 @@ Tiles tiles_of(const MuonMat &m, uint32_t tile)
     return Tiles{rb * cb - per_row * (rb * (rb - 1) / 2), blocks(m.rows, zero1::kNsRows) * blocks(m.cols, tile)};
 }
 
-// Columns of a tile.  256 keeps the tensor cores busiest (a product of 256 x
-// 256 x 16 takes 128 cycles, of 256 x 128 x 16 about 105), 128 spreads few
-// tiles over more block pairs and ends each sooner: taken when even the
-// narrow tiles of the largest product find a pair each.
+// Columns of a tile: whichever of 256 and 128 ends one iteration sooner by
+// measured times.  A step of 64 of K takes 0.85 us for a tile of 256 and
+// 0.69 us for one of 128 (its operand reads bind it), and each of the three
+// products costs 7 or 5 us beside its steps.  An iteration ends no sooner
+// than its longest chain of products and than all steps over all block pairs.
 uint32_t tile_columns(const std::vector<MuonMat> &plan, const std::vector<uint32_t> &large, int sms)
 {
-    uint64_t gram = 0, full = 0;
-    for (const uint32_t i : large) {
-        const Tiles t = tiles_of(plan[i], 128);
-        gram += t.gram;
-        full += t.full;
-    }
-    return std::max(gram, full) <= (uint64_t)sms / 2 ? 128 : 256;
+    const double pairs = std::max(1, sms / 2);
+    const auto time = [&](uint32_t tile, double step, double each) {
+        double all = 0.0, chain = 0.0;
+        for (const uint32_t i : large) {
+            const MuonMat &m = plan[i];
+            const Tiles t = tiles_of(m, tile);
+            const double gram = (double)blocks(std::max(m.rows, m.cols), 64), rest = (double)blocks(m.s, 64);
+            all += t.gram * (gram + rest) + t.full * rest;
+            chain = std::max(chain, (gram + 2 * rest) * step + 3 * each);
+        }
+        return std::max(all * step / pairs, chain);
+    };
+    return time(128, 0.69, 5.0) <= time(256, 0.85, 7.0) ? 128 : 256;
 }
 
 // log2 of the blocks that step a small matrix in one launch, or -1.  One

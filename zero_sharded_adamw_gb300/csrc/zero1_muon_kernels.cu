@@ -88,6 +88,7 @@ __device__ __forceinline__ void reset_counters(const MuonDev &d)
 template <int CAP>
 __global__ void __launch_bounds__(kElemThreads) muon_momentum_kernel(const __grid_constant__ MomentumParams<CAP> p)
 {
+    ptx::launch_dependents();
     reset_counters(p.d);
     if (blockIdx.x >= p.d.nchunks) return;
     const MuonMat &m = p.d.mats[p.d.chunk_mat[blockIdx.x]];
@@ -131,6 +132,7 @@ __global__ void __launch_bounds__(kElemThreads) muon_momentum_kernel(const __gri
 template <typename T>
 __global__ void __launch_bounds__(kElemThreads) muon_norm_kernel(MuonDev d, const T *in)
 {
+    ptx::launch_dependents();
     reset_counters(d);
     if (blockIdx.x >= d.nchunks) return;
     const MuonMat &m = d.mats[d.chunk_mat[blockIdx.x]];
@@ -155,6 +157,8 @@ __global__ void __launch_bounds__(kElemThreads) muon_norm_kernel(MuonDev d, cons
 template <typename T>
 __global__ void __launch_bounds__(kElemThreads) muon_split_kernel(MuonDev d, const T *in, float eps)
 {
+    ptx::launch_dependents();
+    ptx::grid_dependency_wait();
     const MuonMat &m = d.mats[d.chunk_mat[blockIdx.x]];
     __shared__ float factor;
     // the blocks' sums in a fixed order
@@ -198,6 +202,7 @@ __global__ void __launch_bounds__(kElemThreads) muon_split_kernel(MuonDev d, con
 template <int CAP>
 __global__ void __launch_bounds__(kElemThreads) muon_apply_kernel(const __grid_constant__ ApplyParams<CAP> p)
 {
+    ptx::grid_dependency_wait();
     const MuonMat &m = p.d.mats[p.d.chunk_mat[blockIdx.x]];
     const float *x = reinterpret_cast<const float *>(m.region[p.region]);
     const float step = p.lr * m.scale;
@@ -223,6 +228,7 @@ __global__ void __launch_bounds__(kElemThreads) muon_apply_kernel(const __grid_c
 template <typename T>
 __global__ void __launch_bounds__(kElemThreads) muon_out_kernel(MuonDev d, T *out, int region)
 {
+    ptx::grid_dependency_wait();
     const MuonMat &m = d.mats[d.chunk_mat[blockIdx.x]];
     const float *x = reinterpret_cast<const float *>(m.region[region]);
     if (m.vec) {
@@ -476,6 +482,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNsThreads, 1)
     ptx::cluster_sync();
     tc::fence_after_sync();
     const uint32_t tmem = sh.tmem;
+    ptx::launch_dependents();
+    ptx::grid_dependency_wait();
 
     if (threadIdx.x == 32 && rank == 1) {
         // ---- tiles, a few ahead: drawing and describing one takes 2 us of dependent reads
@@ -740,8 +748,25 @@ cudaError_t apply_t(const MuonDev &d, const MuonScalars &sc, void *const *params
     p.decay = sc.decay;
     p.world = world;
     p.region = sc.steps & 1;
-    muon_apply_kernel<CAP><<<d.nchunks, kElemThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_early(muon_apply_kernel<CAP>, d.nchunks, kElemThreads, 0, stream, p);
+}
+
+// A launch that may begin while the one before it on the stream still runs:
+// the kernel waits for its end (griddepcontrol.wait) before it reads anything.
+template <typename K, typename... Args>
+cudaError_t launch_early(K kernel, uint32_t grid, uint32_t threads, int smem, cudaStream_t stream, Args... args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // The first kernel of a call also clears one counter a matrix.
@@ -774,10 +799,8 @@ cudaError_t launch_muon_norm(const MuonDev &d, const void *in, bool bf16, cudaSt
 cudaError_t launch_muon_split(const MuonDev &d, const MuonScalars &sc, const void *in, bool bf16, cudaStream_t stream)
 {
     if (in && bf16)
-        muon_split_kernel<<<d.nchunks, kElemThreads, 0, stream>>>(d, static_cast<const uint16_t *>(in), sc.eps);
-    else
-        muon_split_kernel<<<d.nchunks, kElemThreads, 0, stream>>>(d, static_cast<const float *>(in), sc.eps);
-    return cudaGetLastError();
+        return launch_early(muon_split_kernel<uint16_t>, d.nchunks, kElemThreads, 0, stream, d, static_cast<const uint16_t *>(in), sc.eps);
+    return launch_early(muon_split_kernel<float>, d.nchunks, kElemThreads, 0, stream, d, static_cast<const float *>(in), sc.eps);
 }
 
 template <int TN>
@@ -785,8 +808,7 @@ static cudaError_t iterate_t(const NsParams &p, uint32_t grid, cudaStream_t stre
 {
     const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(muon_iterate_kernel<TN>), Shape<TN>::kSmem);
     if (e != cudaSuccess) return e;
-    muon_iterate_kernel<TN><<<grid, kNsThreads, Shape<TN>::kSmem, stream>>>(p);
-    return cudaGetLastError();
+    return launch_early(muon_iterate_kernel<TN>, grid, kNsThreads, Shape<TN>::kSmem, stream, p);
 }
 
 cudaError_t launch_muon_iterate(const MuonDev &d, const MuonScalars &sc, int num_sms, cudaStream_t stream)
@@ -814,10 +836,8 @@ cudaError_t launch_muon_apply(const MuonDev &d, const MuonScalars &sc, void *con
 cudaError_t launch_muon_out(const MuonDev &d, const MuonScalars &sc, void *out, bool bf16, cudaStream_t stream)
 {
     if (bf16)
-        muon_out_kernel<<<d.nchunks, kElemThreads, 0, stream>>>(d, static_cast<uint16_t *>(out), sc.steps & 1);
-    else
-        muon_out_kernel<<<d.nchunks, kElemThreads, 0, stream>>>(d, static_cast<float *>(out), sc.steps & 1);
-    return cudaGetLastError();
+        return launch_early(muon_out_kernel<uint16_t>, d.nchunks, kElemThreads, 0, stream, d, static_cast<uint16_t *>(out), sc.steps & 1);
+    return launch_early(muon_out_kernel<float>, d.nchunks, kElemThreads, 0, stream, d, static_cast<float *>(out), sc.steps & 1);
 }
 
 }  // namespace zero1

@@ -230,11 +230,14 @@ __global__ void __launch_bounds__(kThreads, 1) muon_small_kernel(const __grid_co
         }
     }
 
-    // This thread's row of a product, and its share of the columns: 64 of
-    // the Gram-sized ones, every other 16 of X's.
+    // This thread's row of a product, and its share of the columns: every
+    // other 16.  Rows and columns past those that are computed (n) are left
+    // as they are: they only ever reach each other.
     const uint32_t r = (warp & 3) * 32 + lane, half = warp >> 2;
     const uint32_t lanes = (warp & 3) << 21;
     const uint32_t n = (s + 15) & ~15u;        // rows of X the products take
+    const bool active = (warp & 3) * 32 < n;   // this warp's rows
+    const auto unit = [&](int q) { return (2 * q + half) * 16; };   // its q-th 16 columns
     constexpr float inv = 1.0f / kNsScale;
     uint32_t waits = 0;
     // Shared memory written by this block's threads is ready for the products.
@@ -265,12 +268,14 @@ __global__ void __launch_bounds__(kThreads, 1) muon_small_kernel(const __grid_co
         finished();
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            tc::tmem_load16(w + 16 * q, tmem + kSumTmem + lanes + half * 64 + 16 * q);
-            if (width > 128) {
-                float v[16];
-                tc::tmem_load16(v, tmem + kSumTmem + 128 + lanes + half * 64 + 16 * q);
+            if (active && unit(q) < n) {
+                tc::tmem_load16(w + 16 * q, tmem + kSumTmem + lanes + unit(q));
+                if (width > 128) {
+                    float v[16];
+                    tc::tmem_load16(v, tmem + kSumTmem + 128 + lanes + unit(q));
 #pragma unroll
-                for (int e = 0; e < 16; ++e) w[16 * q + e] += v[e];
+                    for (int e = 0; e < 16; ++e) w[16 * q + e] += v[e];
+                }
             }
         }
         if (blocks > 1) {
@@ -278,13 +283,19 @@ __global__ void __launch_bounds__(kThreads, 1) muon_small_kernel(const __grid_co
             const uint32_t strip = 128 / blocks, owner = r / strip, row = r % strip;
             const uint32_t there = tc::map_to(parts, owner);
 #pragma unroll
-            for (uint32_t q = 0; q < 16; ++q)
-                tc::st_cluster(f32_piece(there, rank * strip + row, half * 16 + q, 32),
-                               as_u4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]));
+            for (int q = 0; q < 4; ++q)
+                if (active && unit(q) < n)
+#pragma unroll
+                    for (uint32_t e = 0; e < 4; ++e) {
+                        const float *t = w + 16 * q + 4 * e;
+                        tc::st_cluster(f32_piece(there, rank * strip + row, unit(q) / 4 + e, 32), as_u4(t[0], t[1], t[2], t[3]));
+                    }
             ptx::cluster_sync();
             // and the sums to all blocks, in the place of the Gram matrix
-            for (uint32_t id = tid; id < strip * 32; id += kThreads) {
-                const uint32_t row = id >> 5, quad = id & 31;
+            const uint32_t quads_n = n >> 2;
+            for (uint32_t id = tid; id < strip * quads_n; id += kThreads) {
+                const uint32_t row = id / quads_n, quad = id % quads_n;
+                if (rank * strip + row >= n) continue;
                 float4 t = ld_f4(f32_piece(parts, row, quad, 32));
                 for (uint32_t b = 1; b < blocks; ++b) {
                     const float4 v = ld_f4(f32_piece(parts, b * strip + row, quad, 32));
@@ -295,55 +306,57 @@ __global__ void __launch_bounds__(kThreads, 1) muon_small_kernel(const __grid_co
             }
             ptx::cluster_sync();
 #pragma unroll
-            for (uint32_t q = 0; q < 16; ++q) {
-                const float4 t = ld_f4(f32_piece(gram, r, half * 16 + q, 32));
-                w[4 * q] = t.x, w[4 * q + 1] = t.y, w[4 * q + 2] = t.z, w[4 * q + 3] = t.w;
-            }
+            for (int q = 0; q < 4; ++q)
+                if (active && unit(q) < n)
+#pragma unroll
+                    for (uint32_t e = 0; e < 4; ++e) {
+                        const float4 t = ld_f4(f32_piece(gram, r, unit(q) / 4 + e, 32));
+                        w[16 * q + 4 * e] = t.x, w[16 * q + 4 * e + 1] = t.y, w[16 * q + 4 * e + 2] = t.z, w[16 * q + 4 * e + 3] = t.w;
+                    }
             __syncthreads();
         }
-        // columns past n were not computed: zeros, as the rows past s of X would give
+        const auto put_gram = [&](int q) {
 #pragma unroll
-        for (uint32_t q = 0; q < 64; ++q) {
-            const uint32_t c = half * 64 + q;
-            w[q] = c < n ? w[q] * inv : 0.f;
-            if (c == r) w[q] -= alpha * kNsScale;
-        }
-        const auto put_gram = [&](const float *v) {
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
+            for (int e = 0; e < 2; ++e) {
+                const float *v = w + 16 * q + 8 * e;
                 uint4 h, lo;
-                split(v[8 * q], v[8 * q + 1], h.x, lo.x);
-                split(v[8 * q + 2], v[8 * q + 3], h.y, lo.y);
-                split(v[8 * q + 4], v[8 * q + 5], h.z, lo.z);
-                split(v[8 * q + 6], v[8 * q + 7], h.w, lo.w);
-                tc::st_shared(f16_piece(gram, r, half * 8 + q), h);
-                tc::st_shared(f16_piece(gram + 2 * kBox, r, half * 8 + q), lo);
+                split(v[0], v[1], h.x, lo.x);
+                split(v[2], v[3], h.y, lo.y);
+                split(v[4], v[5], h.z, lo.z);
+                split(v[6], v[7], h.w, lo.w);
+                tc::st_shared(f16_piece(gram, r, unit(q) / 8 + e), h);
+                tc::st_shared(f16_piece(gram + 2 * kBox, r, unit(q) / 8 + e), lo);
             }
         };
-        put_gram(w);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (active && unit(q) < n) {
+#pragma unroll
+                for (uint32_t e = 0; e < 16; ++e) w[16 * q + e] = w[16 * q + e] * inv - (unit(q) + e == r ? alpha * kNsScale : 0.f);
+                put_gram(q);
+            }
 
         // P = c A' A' + (b + 2 c alpha) A' + (a + b alpha + c alpha^2) I, about A' = A - alpha I
         ready();
         if (tid == 0) product(tmem + kGramTmem, gram, 2 * kBox, gram, 2 * kBox, false, 0, n, n);
         finished();
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            float v[16];
-            tc::tmem_load16(v, tmem + kGramTmem + lanes + half * 64 + 16 * q);
+        for (int q = 0; q < 4; ++q)
+            if (active && unit(q) < n) {
+                float v[16];
+                tc::tmem_load16(v, tmem + kGramTmem + lanes + unit(q));
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const uint32_t c = half * 64 + 16 * q + e;
-                w[16 * q + e] = (c < n ? p.sc.c * inv * v[e] : 0.f) + linear * w[16 * q + e] + (c == r ? constant * kNsScale : 0.f);
+                for (uint32_t e = 0; e < 16; ++e)
+                    w[16 * q + e] = p.sc.c * inv * v[e] + linear * w[16 * q + e] + (unit(q) + e == r ? constant * kNsScale : 0.f);
+                put_gram(q);
             }
-        }
-        put_gram(w);
 
         // X <- P X, or on the last iteration the result in fp32
         ready();
         if (tid == 0) product(tmem + kSumTmem, gram, 2 * kBox, x, x_plane, true, 0, n, width);
         finished();
         const bool last = iter + 1 == p.sc.steps;
-        for (uint32_t c = half * 16; c < width; c += 32) {
+        for (uint32_t c = half * 16; active && c < width; c += 32) {
             float v[16];
             tc::tmem_load16(v, tmem + kSumTmem + lanes + c);
             if (last) {

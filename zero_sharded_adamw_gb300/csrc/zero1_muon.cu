@@ -257,7 +257,7 @@ int create(uint64_t n, int world, const zero1_matrix *mats, uint64_t count, cons
     std::vector<uint2> work;
     std::vector<uint32_t> chunk_mat, large, small[zero1::kSmallSizes];
     std::vector<uint64_t> region0(count), region1(count), gram(count), poly(count), diag(count);
-    uint64_t entries = 0, chunks = 0, tiles = 0;
+    uint64_t entries = 0, large_entries = 0, chunks = 0, tiles = 0;
     for (uint64_t i = 0; i < count; ++i) {
         const zero1_matrix &a = mats[i];
         MuonMat &m = plan[i];
@@ -283,7 +283,15 @@ int create(uint64_t n, int world, const zero1_matrix *mats, uint64_t count, cons
             continue;
         }
         large.push_back((uint32_t)i);
-        const uint64_t c = (size + zero1::kChunk - 1) / zero1::kChunk;
+        large_entries += size;
+    }
+    // Blocks of 16,384 entries, or of 2,048 and more so that small lists spread over the SMs too (each block of
+    // the second kernel adds up all partial sums of its matrix: 4,096 at 67 million entries).
+    uint32_t chunk = 2048;
+    while (chunk < 16384 && large_entries / chunk > 2048) chunk *= 2;
+    for (const uint32_t i : large) {
+        MuonMat &m = plan[i];
+        const uint64_t c = blocks((uint64_t)m.rows * m.cols, chunk);
         chunks += c;
         if (chunks > 0x7FFFFFFFull) return mfail(ZERO1_EINVAL, "the matrices are too large for one handle");
         m.chunk0 = (uint32_t)(chunks - c);
@@ -416,6 +424,7 @@ int create(uint64_t n, int world, const zero1_matrix *mats, uint64_t count, cons
     d.nchunks = (uint32_t)chunk_mat.size();
     d.work_per_iter = (uint32_t)work.size();
     d.tile = tile;
+    d.chunk = chunk;
     h->small.list = reinterpret_cast<uint32_t *>(base + at_small);
     for (int i = 0, at = 0; i < zero1::kSmallSizes; ++i) {
         h->small.first[i] = (uint32_t)at;

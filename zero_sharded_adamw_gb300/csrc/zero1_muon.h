@@ -15,7 +15,6 @@ namespace zero1 {
 constexpr uint32_t kNsRows = 256;
 constexpr int kNsParts = 32;           // arrivals a finished tile makes: one by each warp that writes it
 constexpr int kNsTileK = 64;           // K of one pipeline stage
-constexpr uint32_t kChunk = 16384;     // entries of one elementwise block
 constexpr uint32_t kMaxSide = 1u << 22;
 // Powers of two the f16 operands are scaled by: every iterate has entries
 // below 2 in magnitude and the Gram matrices below 4, so 4096 keeps them
@@ -57,6 +56,7 @@ struct MuonDev {
     unsigned *errors;          // sticky: bit 0 = a wait gave up
     uint32_t count, nchunks, work_per_iter;
     uint32_t tile;             // columns of a tile
+    uint32_t chunk;            // entries of one elementwise block
 };
 
 // Small matrices, whose whole step is one launch (zero1_muon_small.cu): lists

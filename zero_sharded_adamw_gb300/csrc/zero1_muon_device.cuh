@@ -14,11 +14,18 @@ namespace zero1 {
 struct SquareSum {
     float s = 0.f;
     double big = 0.0;
-    __device__ __forceinline__ void add(float v)
+    template <int N>
+    __device__ __forceinline__ void add(const float (&v)[N])
     {
-        const float q = v * v;
-        if (q > 1e30f) big += (double)v * (double)v;
+        float q = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) q += v[i] * v[i];
+        if (q > 1e30f) outsized(v, N);
         else s += q;
+    }
+    __device__ __noinline__ void outsized(const float *v, int n)
+    {
+        for (int i = 0; i < n; ++i) big += (double)v[i] * (double)v[i];
     }
     __device__ __forceinline__ double total() const { return big + (double)s; }
 };

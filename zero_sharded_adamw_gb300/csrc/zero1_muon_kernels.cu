@@ -46,11 +46,11 @@ struct ApplyParams {
 // visited by f(flat index, padded index) in steps of `step` entries that
 // share a row.
 template <typename F>
-__device__ __forceinline__ void for_chunk(const MuonMat &m, uint32_t chunk, uint32_t step, F f)
+__device__ __forceinline__ void for_chunk(const MuonMat &m, uint32_t chunk, uint32_t size_of, uint32_t step, F f)
 {
-    const uint64_t begin = (uint64_t)chunk * kChunk;
+    const uint64_t begin = (uint64_t)chunk * size_of;
     const uint64_t size = (uint64_t)m.rows * m.cols;
-    const uint32_t n = (uint32_t)min((uint64_t)kChunk, size - begin);
+    const uint32_t n = (uint32_t)min((uint64_t)size_of, size - begin);
     const uint64_t r0 = begin / m.cols;
     const uint32_t c0 = (uint32_t)(begin - r0 * m.cols);
     for (uint32_t o = threadIdx.x * step; o < n; o += kElemThreads * step) {
@@ -94,13 +94,8 @@ __global__ void __launch_bounds__(kElemThreads) muon_momentum_kernel(const __gri
     const MuonMat &m = p.d.mats[p.d.chunk_mat[blockIdx.x]];
     float *u = reinterpret_cast<float *>(m.region[1]);
     SquareSum ss;
-    const auto one = [&](float sum, float &mom) {
-        const float x = look_ahead(p.sc, sum, mom);
-        ss.add(x);
-        return x;
-    };
     if (m.vec) {
-        for_chunk(m, blockIdx.x - m.chunk0, 8, [&](uint64_t f, uint64_t x) {
+        for_chunk(m, blockIdx.x - m.chunk0, p.d.chunk, 8, [&](uint64_t f, uint64_t x) {
             float s[8], mom[8];
             load8(mom, p.momentum + f);
             load8(s, p.grads[0] + f);
@@ -112,15 +107,17 @@ __global__ void __launch_bounds__(kElemThreads) muon_momentum_kernel(const __gri
                 for (int k = 0; k < 8; ++k) s[k] += g[k];
             }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) s[k] = one(s[k], mom[k]);
+            for (int k = 0; k < 8; ++k) s[k] = look_ahead(p.sc, s[k], mom[k]);
+            ss.add(s);
             store8(p.momentum + f, mom);
             store8(u + x, s);
         });
     } else {
-        for_chunk(m, blockIdx.x - m.chunk0, 1, [&](uint64_t f, uint64_t x) {
-            float s = load1(p.grads[0] + f), mom = p.momentum[f];
-            for (int r = 1; r < p.world; ++r) s += load1(p.grads[r] + f);
-            u[x] = one(s, mom);
+        for_chunk(m, blockIdx.x - m.chunk0, p.d.chunk, 1, [&](uint64_t f, uint64_t x) {
+            float s[1] = {load1(p.grads[0] + f)}, mom = p.momentum[f];
+            for (int r = 1; r < p.world; ++r) s[0] += load1(p.grads[r] + f);
+            u[x] = s[0] = look_ahead(p.sc, s[0], mom);
+            ss.add(s);
             p.momentum[f] = mom;
         });
     }
@@ -138,15 +135,15 @@ __global__ void __launch_bounds__(kElemThreads) muon_norm_kernel(MuonDev d, cons
     const MuonMat &m = d.mats[d.chunk_mat[blockIdx.x]];
     SquareSum ss;
     if (m.vec) {
-        for_chunk(m, blockIdx.x - m.chunk0, 8, [&](uint64_t f, uint64_t) {
+        for_chunk(m, blockIdx.x - m.chunk0, d.chunk, 8, [&](uint64_t f, uint64_t) {
             float v[8];
             load8(v, in + f);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) ss.add(v[k]);
+            ss.add(v);
         });
     } else {
-        for_chunk(m, blockIdx.x - m.chunk0, 1, [&](uint64_t f, uint64_t) {
-            ss.add(load1(in + f));
+        for_chunk(m, blockIdx.x - m.chunk0, d.chunk, 1, [&](uint64_t f, uint64_t) {
+            const float v[1] = {load1(in + f)};
+            ss.add(v);
         });
     }
     const double sum = block_sum(ss.total());
@@ -162,22 +159,22 @@ __global__ void __launch_bounds__(kElemThreads) muon_split_kernel(MuonDev d, con
     const MuonMat &m = d.mats[d.chunk_mat[blockIdx.x]];
     __shared__ float factor;
     // the blocks' sums in a fixed order
-    __shared__ double part[kElemThreads];
+    __shared__ double part[kElemThreads / 32];
     double t = 0.0;
     for (uint32_t i = threadIdx.x; i < m.chunks; i += kElemThreads) t += d.partials[m.chunk0 + i];
-    part[threadIdx.x] = t;
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(~0u, t, o);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = t;
     __syncthreads();
-    for (int o = kElemThreads / 2; o > 0; o >>= 1) {
-        if (threadIdx.x < o) part[threadIdx.x] += part[threadIdx.x + o];
-        __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int i = 1; i < kElemThreads / 32; ++i) t += part[i];
+        factor = (float)((double)kNsScale / (sqrt(t) + (double)eps));
     }
-    if (threadIdx.x == 0) factor = (float)((double)kNsScale / (sqrt(part[0]) + (double)eps));
     __syncthreads();
     const float k = factor;
     uint16_t *hi = reinterpret_cast<uint16_t *>(m.region[0]), *lo = hi + m.xplane;
     const T *src = in ? in : reinterpret_cast<const T *>(m.region[1]);
     if (m.vec) {
-        for_chunk(m, blockIdx.x - m.chunk0, 8, [&](uint64_t f, uint64_t x) {
+        for_chunk(m, blockIdx.x - m.chunk0, d.chunk, 8, [&](uint64_t f, uint64_t x) {
             float v[8];
             uint4 h, l;
             load8(v, src + (in ? f : x));
@@ -189,7 +186,7 @@ __global__ void __launch_bounds__(kElemThreads) muon_split_kernel(MuonDev d, con
             *reinterpret_cast<uint4 *>(lo + x) = l;
         });
     } else {
-        for_chunk(m, blockIdx.x - m.chunk0, 1, [&](uint64_t f, uint64_t x) {
+        for_chunk(m, blockIdx.x - m.chunk0, d.chunk, 1, [&](uint64_t f, uint64_t x) {
             uint32_t h, l;
             split(load1(src + (in ? f : x)) * k, 0.f, h, l);
             hi[x] = (uint16_t)h;
@@ -207,7 +204,7 @@ __global__ void __launch_bounds__(kElemThreads) muon_apply_kernel(const __grid_c
     const float *x = reinterpret_cast<const float *>(m.region[p.region]);
     const float step = p.lr * m.scale;
     if (m.vec) {
-        for_chunk(m, blockIdx.x - m.chunk0, 8, [&](uint64_t f, uint64_t i) {
+        for_chunk(m, blockIdx.x - m.chunk0, p.d.chunk, 8, [&](uint64_t f, uint64_t i) {
             float o[8], w[8];
             load8(o, x + i);
             load8(w, p.master + f);
@@ -217,7 +214,7 @@ __global__ void __launch_bounds__(kElemThreads) muon_apply_kernel(const __grid_c
             for (int r = 0; r < p.world; ++r) store8(p.params[r] + f, w);
         });
     } else {
-        for_chunk(m, blockIdx.x - m.chunk0, 1, [&](uint64_t f, uint64_t i) {
+        for_chunk(m, blockIdx.x - m.chunk0, p.d.chunk, 1, [&](uint64_t f, uint64_t i) {
             const float w = p.master[f] * p.decay - step * x[i];
             p.master[f] = w;
             for (int r = 0; r < p.world; ++r) store1(p.params[r] + f, w);
@@ -232,13 +229,13 @@ __global__ void __launch_bounds__(kElemThreads) muon_out_kernel(MuonDev d, T *ou
     const MuonMat &m = d.mats[d.chunk_mat[blockIdx.x]];
     const float *x = reinterpret_cast<const float *>(m.region[region]);
     if (m.vec) {
-        for_chunk(m, blockIdx.x - m.chunk0, 8, [&](uint64_t f, uint64_t i) {
+        for_chunk(m, blockIdx.x - m.chunk0, d.chunk, 8, [&](uint64_t f, uint64_t i) {
             float v[8];
             load8(v, x + i);
             store8(out + f, v);
         });
     } else {
-        for_chunk(m, blockIdx.x - m.chunk0, 1, [&](uint64_t f, uint64_t i) { store1(out + f, x[i]); });
+        for_chunk(m, blockIdx.x - m.chunk0, d.chunk, 1, [&](uint64_t f, uint64_t i) { store1(out + f, x[i]); });
     }
 }
 
@@ -248,7 +245,7 @@ __global__ void __launch_bounds__(kElemThreads) muon_out_kernel(MuonDev d, T *ou
 // (64) of its 128 rows of A and its TN/2 rows of B, high and low parts, and
 // 2 KB an epilogue warp.
 constexpr uint32_t kBox = 8192;                        // 64 x 64 f16
-constexpr int kSlots = 3;                              // tiles in flight between the roles
+constexpr int kSlots = 2;                              // tiles known to a pair: this one and the next
 constexpr int kGroups = 4;                             // of 4 epilogue warps, TN/4 columns each
 constexpr int kNsThreads = 64 + kGroups * 128;         // loads, products; epilogue
 constexpr uint32_t kWarpOut = 2048;                    // 32 rows x 64 bytes on an epilogue warp's way out
@@ -486,7 +483,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNsThreads, 1)
     ptx::grid_dependency_wait();
 
     if (threadIdx.x == 32 && rank == 1) {
-        // ---- tiles, a few ahead: drawing and describing one takes 2 us of dependent reads
+        // ---- tiles, one ahead: drawing and describing one takes 2 us of dependent reads
         for (uint32_t n = 0;; ++n) {
             const int slot = n % kSlots;
             if (n >= kSlots && !tc::pair_wait(&sh.slot_empty[slot], (n / kSlots - 1) & 1u, abort, errors)) break;

@@ -176,8 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1) muon_small_kernel(const __grid_co
                         u[e] = p.in_bf16 ? load1(static_cast<const uint16_t *>(p.in) + f + e * next)
                                          : static_cast<const float *>(p.in)[f + e * next];
             }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) ss.add(u[e]);
+            ss.add(u);
         }
         tc::st_shared(f32_piece(x, i, j >> 2, quads), as_u4(u[0], u[1], u[2], u[3]));
         tc::st_shared(f32_piece(x, i, (j >> 2) + 1, quads), as_u4(u[4], u[5], u[6], u[7]));

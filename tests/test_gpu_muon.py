@@ -73,6 +73,25 @@ def test_orthogonalize_random(rows, cols, dtype):
     assert rel(run_orth(u), ref_orth(u)) <= PLAIN
 
 
+@pytest.mark.parametrize("shapes", [[(150, 4000)], [(4000, 150)], [(257, 3001)], [(513, 2050), (2050, 140)],
+                                    [(200, 9000), (300, 300), (1030, 129), (40, 50), (17, 2000)]])
+def test_long_sums_and_mixed_lists(shapes):
+    """Gram matrices formed in slices of K, beside matrices that are not, and
+    beside small ones; the same bits twice."""
+    mats, at = [], 0
+    for r, c in shapes:
+        mats.append((at, r, c))
+        at += r * c
+    u = torch.randn(at, generator=torch.Generator(device="cuda").manual_seed(at), device="cuda")
+    out, again = torch.empty_like(u), torch.empty_like(u)
+    with z.Muon(at, 1, mats) as opt:
+        opt.orthogonalize(u, out)
+        opt.orthogonalize(u, again)
+        opt.status()
+    assert torch.equal(out, again)
+    assert max(rel(view(out, *m), ref_orth(view(u, *m))) for m in mats) <= PLAIN
+
+
 @pytest.mark.parametrize("rows,cols", [(64, 64), (256, 256), (300, 1100), (900, 130)])
 @pytest.mark.parametrize("kind", ["decay", "strong", "rank1"])
 def test_orthogonalize_uneven_spectra(rows, cols, kind):

@@ -184,8 +184,8 @@ Tiles tiles_of(const MuonMat &m, uint32_t tile)
 
 // Columns of a tile: whichever of 256 and 128 ends one iteration sooner by
 // measured times.  A step of 64 of K takes 0.85 us for a tile of 256 and
-// 0.69 us for one of 128 (its operand reads bind it), and each of the three
-// products costs 7 or 5 us beside its steps.  An iteration ends no sooner
+// 0.57 us for one of 128 (two wide products where the other has three), and
+// each of the three phases costs 7 or 5 us beside its steps.  An iteration ends no sooner
 // than its longest chain of products and than all steps over all block pairs.
 uint32_t tile_columns(const std::vector<MuonMat> &plan, const std::vector<uint32_t> &large, int sms)
 {
@@ -201,7 +201,7 @@ uint32_t tile_columns(const std::vector<MuonMat> &plan, const std::vector<uint32
         }
         return std::max(all * step / pairs, chain);
     };
-    return time(128, 0.69, 5.0) <= time(256, 0.85, 7.0) ? 128 : 256;
+    return time(128, 0.57, 5.0) <= time(256, 0.85, 7.0) ? 128 : 256;
 }
 
 // log2 of the blocks that step a small matrix in one launch, or -1.  One

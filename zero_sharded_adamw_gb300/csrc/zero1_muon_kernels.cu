@@ -254,7 +254,12 @@ struct Shape {
     static constexpr int kBoxesB = TN / 128;           // of one part of B
     static constexpr uint32_t kStageBytes = (4 + 2 * kBoxesB) * kBox;   // A hi, A lo (two boxes each), B hi, B lo
     static constexpr int kStages = TN == 256 ? 3 : 4;
-    static constexpr int kAccs = 512 / TN;             // accumulators: all of TMEM
+    // Two accumulators of 256 columns, all of TMEM.  A narrow tile's hold each
+    // block's 64 columns of hi*hi + lo*hi and then of hi*lo + lo*lo: its B
+    // parts lie one after the other, so one product takes both, at the rate
+    // of a wide one (256 x 256 x 16 in 128 cycles, 256 x 128 x 16 in 105).
+    static constexpr int kAccs = 2;
+    static constexpr uint32_t kAccCols = 256;
     static constexpr int kSmem = kStages * kStageBytes + 4 * kGroups * kWarpOut + 1024;
 };
 // K of one accumulator.  The tensor cores cut every addition of 16 products
@@ -312,7 +317,7 @@ struct NsShared {
     uint64_t full[4], empty[4];                        // operand ring
     uint64_t slot_full[kSlots], slot_empty[kSlots];    // tile ring
     uint64_t slot_go[kSlots];                          // a tile's operands are there to be loaded
-    uint64_t acc_full[4], acc_empty[4];                // accumulators
+    uint64_t acc_full[2], acc_empty[2];                // accumulators
     uint64_t drain;
     uint32_t tmem;
     int abort;
@@ -561,7 +566,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNsThreads, 1)
             tc::arrive_cluster(tc::map_to(tc::smem_u32(&sh.slot_empty[slot]), 1));
             if (phase == kNoMore) break;
             for (uint32_t k0 = 0; k0 < k_end; k0 += kNsTileK) {
-                const uint32_t acc = used % kAccs, d = tmem + acc * TN;
+                const uint32_t acc = used % kAccs, d = tmem + acc * S::kAccCols;
                 const bool first = starts_sum<TN>(k0);
                 if (first && used >= kAccs) {
                     if (!(ok = tc::pair_wait(&sh.acc_empty[acc], (used / kAccs - 1) & 1u, abort, errors))) break;
@@ -571,7 +576,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNsThreads, 1)
                 if (!(ok = tc::pair_wait(&sh.full[stage], (taken / kStages) & 1u, abort, errors))) break;
                 tc::fence_after_sync();
                 const bool a_mn = k0 < a_turn, b_mn = k0 < b_turn;
-                const uint32_t idesc = tc::instr_desc(kNsRows, TN, a_mn, b_mn);
+                const uint32_t idesc = tc::instr_desc(kNsRows, 256, a_mn, b_mn);
                 const uint64_t astep = tc::k16_step(a_mn), bstep = tc::k16_step(b_mn);
                 const uint32_t src = ring + stage * kStageBytes;
                 const uint64_t ah = tc::smem_desc(src, a_mn), al = tc::smem_desc(src + 2 * kBox, a_mn);
@@ -579,8 +584,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNsThreads, 1)
                 // the small products first: what is cut off goes by the size of the sum so far
 #pragma unroll
                 for (int j = 0; j < kNsTileK / 16; ++j) {
-                    tc::mma_f16(d, ah + j * astep, bl + j * bstep, idesc, !first || j > 0);
-                    tc::mma_f16(d, al + j * astep, bh + j * bstep, idesc, true);
+                    if (TN == 256) tc::mma_f16(d, ah + j * astep, bl + j * bstep, idesc, !first || j > 0);
+                    tc::mma_f16(d, al + j * astep, bh + j * bstep, idesc, TN == 256 || !first || j > 0);
                 }
 #pragma unroll
                 for (int j = 0; j < kNsTileK / 16; ++j) tc::mma_f16(d, ah + j * astep, bh + j * bstep, idesc, true);
@@ -602,7 +607,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNsThreads, 1)
         // ---- finished tiles: this block's 128 rows, kCols columns to each group
         const int group = (warp - 2) >> 2;
         const uint32_t r = (uint32_t)(warp & 3) * 32 + (threadIdx.x & 31);
-        const uint32_t at = tmem + ((uint32_t)(warp & 3) << 21) + group * kCols;
+        const uint32_t at = tmem + ((uint32_t)(warp & 3) << 21) + group * kCols + (TN == 128 && group >= 2 ? 64 : 0);
         const uint32_t mem = ring + kStages * kStageBytes + (warp - 2) * kWarpOut;
         const bool leader = (threadIdx.x & 31) == 0;
         uint32_t used = 0;            // accumulators
@@ -637,9 +642,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNsThreads, 1)
 #pragma unroll
                 for (int q = 0; q < kCols / 16; ++q) {
                     float x[16];
-                    tc::tmem_load16(x, at + acc * TN + q * 16);
+                    tc::tmem_load16(x, at + acc * S::kAccCols + q * 16);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) w[16 * q + j] += x[j];
+                    if (TN == 128) {
+                        tc::tmem_load16(x, at + acc * S::kAccCols + 64 + q * 16);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) w[16 * q + j] += x[j];
+                    }
                 }
                 tc::fence_before_sync();
                 __syncwarp();

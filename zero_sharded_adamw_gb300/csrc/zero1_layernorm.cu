@@ -240,6 +240,23 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) zero1_layernorm_bwd_ke
         mean = p.mean[r];
         rstd = p.rstd[r];
     };
+    // h and dy gamma of a row stay as they are computed while registers hold them, with the weights; else a row's
+    // pieces stay and both are computed again.
+    constexpr bool kKeep = AHEAD && NV * V <= (V == 8 ? 16 : 8);   // unpacked pieces take a register an entry
+    constexpr int kKept = kKeep ? NV * V : 1;
+    float gamma[kKept];
+    if constexpr (kKeep) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const uint32_t c = (j * TPR + t) * V;
+            if (c < p.cols) {
+                float g[V];
+                fetch<T, V>(p.gamma + c).get(g);
+#pragma unroll
+                for (int i = 0; i < V; ++i) gamma[j * V + i] = g[i];
+            }
+        }
+    }
     if (AHEAD && row < p.rows) load(row);
     for (; row < p.rows; row += step) {
         if (!AHEAD) load(row);
@@ -248,7 +265,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) zero1_layernorm_bwd_ke
 #pragma unroll
         for (int j = 0; j < NV; ++j) xc[j] = xs[j], dc[j] = ds[j];
         if (AHEAD && row + step < p.rows) load(row + step);
-        float sg = 0.f, sh = 0.f;
+        float sg = 0.f, sh = 0.f, hs[kKept], ws[kKept];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const uint32_t c = (j * TPR + t) * V;
@@ -256,14 +273,15 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) zero1_layernorm_bwd_ke
                 float x[V], d[V], g[V];
                 xc[j].get(x);
                 dc[j].get(d);
-                fetch<T, V>(p.gamma + c).get(g);
+                if constexpr (!kKeep) fetch<T, V>(p.gamma + c).get(g);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    const float h = (x[i] - mc) * rc, w = d[i] * g[i];
+                    const float h = (x[i] - mc) * rc, w = d[i] * (kKeep ? gamma[(j * V + i) % kKept] : g[i]);
                     ag[j * V + i] += d[i] * h;
                     ab[j * V + i] += d[i];
                     sg += w;
                     sh += w * h;
+                    if (kKeep) hs[(j * V + i) % kKept] = h, ws[(j * V + i) % kKept] = w;
                 }
             }
         }
@@ -276,13 +294,15 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) zero1_layernorm_bwd_ke
             const uint32_t c = (j * TPR + t) * V;
             if (c < p.cols) {
                 float x[V], d[V], g[V];
-                xc[j].get(x);
-                dc[j].get(d);
-                fetch<T, V>(p.gamma + c).get(g);
+                if constexpr (kKeep) {
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float h = (x[i] - mc) * rc;
-                    d[i] = rc * (d[i] * g[i] - sg - h * sh);
+                    for (int i = 0; i < V; ++i) d[i] = rc * (ws[(j * V + i) % kKept] - sg - hs[(j * V + i) % kKept] * sh);
+                } else {
+                    xc[j].get(x);
+                    dc[j].get(d);
+                    fetch<T, V>(p.gamma + c).get(g);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) d[i] = rc * (d[i] * g[i] - sg - (x[i] - mc) * rc * sh);
                 }
                 Piece<T, V> out;
                 out.set(d);

@@ -555,6 +555,11 @@ typedef struct zero1_matrix {
  *     iterate's singular values below 2, as (3.4445, -4.7750, 2.0315) does:
  *     entries are held in f16 parts scaled by 4096, and beyond that range
  *     results are infinite or NaN.
+ *   inject_wait_timeout: failure testing only.  1 = the tiled iteration (a
+ *     side above 128) is given no tiles, so that its waits run out after
+ *     their 1 s limit; the call returns, its results mean nothing, and
+ *     zero1_muon_status then reports ZERO1_ECUDA.
+ *   reserved: 0.
  *   size: sizeof(zero1_muon_hparams) (lets the struct grow). */
 typedef struct zero1_muon_hparams {
     uint32_t size;
@@ -569,6 +574,8 @@ typedef struct zero1_muon_hparams {
     double ns_a;
     double ns_b;
     double ns_c;
+    int32_t inject_wait_timeout;
+    int32_t reserved;
 } zero1_muon_hparams;
 
 typedef struct zero1_muon_ctx *zero1_muon_handle;

@@ -374,3 +374,22 @@ def test_refusals():
         opt.status()
     with pytest.raises(z.Zero1Error):
         z.zero1_muon_step(opt.handle or 0xDEAD0000, [h, h], [h, h], x, x)
+
+
+def test_a_wait_that_runs_out_is_reported():
+    """No tile is ever drawn: every wait of the iteration gives up after its
+    limit, the call ends, the status says so for this handle and no other,
+    and the device goes on."""
+    u = torch.randn(300 * 200, device="cuda")
+    out = torch.empty_like(u)
+    with z.Muon(u.numel(), 1, [(0, 300, 200)], z.MuonHparams(inject_wait_timeout=True)) as bad, \
+            z.Muon(u.numel(), 1, [(0, 300, 200)]) as good:
+        bad.orthogonalize(u, out)
+        with pytest.raises(z.Zero1Error) as e:
+            bad.status()
+        assert e.value.code == -4 and "gave up" in str(e.value)
+        good.orthogonalize(u, out)
+        good.status()
+        assert rel(view(out, 0, 300, 200), ref_orth(view(u, 0, 300, 200))) <= PLAIN
+        with pytest.raises(z.Zero1Error):
+            bad.status()

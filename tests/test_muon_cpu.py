@@ -41,7 +41,7 @@ def accepted(n, mats):
 @pytest.mark.parametrize("hp", [dict(lr=-1.0), dict(lr=float("nan")), dict(momentum=1.0), dict(momentum=-0.1),
                                 dict(weight_decay=float("inf")), dict(eps=0.0), dict(eps=1e-16), dict(update_scale=-1.0),
                                 dict(nesterov=2), dict(scale_rule=5), dict(ns_steps=0), dict(ns_steps=33),
-                                dict(ns_a=float("nan")), dict(ns_b=9.0), dict(ns_c=0.0), dict(ns_b=-4.0, ns_c=0.4)])
+                                dict(ns_a=float("nan")), dict(ns_b=9.0), dict(ns_c=0.0), dict(ns_b=-4.0, ns_c=0.4), dict(inject_wait_timeout=2)])
 def test_hyperparameters(hp):
     assert refused(64, 1, [(0, 8, 8)], z.MuonHparams(**hp))[0] == -1
 

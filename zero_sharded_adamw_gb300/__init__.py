@@ -537,7 +537,8 @@ class _CMatrix(C.Structure):
 class _CMuonHparams(C.Structure):
     _fields_ = [("size", C.c_uint32), ("nesterov", C.c_int32), ("scale_rule", C.c_int32), ("ns_steps", C.c_int32),
                 ("lr", C.c_double), ("momentum", C.c_double), ("weight_decay", C.c_double), ("eps", C.c_double),
-                ("update_scale", C.c_double), ("ns_a", C.c_double), ("ns_b", C.c_double), ("ns_c", C.c_double)]
+                ("update_scale", C.c_double), ("ns_a", C.c_double), ("ns_b", C.c_double), ("ns_c", C.c_double),
+                ("inject_wait_timeout", C.c_int32), ("reserved", C.c_int32)]
 
 
 @dataclass
@@ -554,11 +555,12 @@ class MuonHparams:
     ns_a: float = 3.4445
     ns_b: float = -4.7750
     ns_c: float = 2.0315
+    inject_wait_timeout: bool = False    # failure testing: the tiled iteration's waits run out
 
     def _c(self) -> _CMuonHparams:
         return _CMuonHparams(C.sizeof(_CMuonHparams), int(self.nesterov), self.scale_rule, self.ns_steps, self.lr,
                              self.momentum, self.weight_decay, self.eps, self.update_scale, self.ns_a, self.ns_b,
-                             self.ns_c)
+                             self.ns_c, int(self.inject_wait_timeout), 0)
 
 
 # (n, world) of every matrix handle this binding created.

@@ -86,6 +86,9 @@ int check_hparams(const zero1_muon_hparams *hp)
     // below 1e-15 an update whose fp32 squares vanish would leave f16's range
     if (!(std::isfinite(hp->eps) && hp->eps >= 1e-15)) return mfail(ZERO1_EINVAL, "eps must be finite and >= 1e-15");
     if (!finite_nonneg(hp->update_scale)) return mfail(ZERO1_EINVAL, "update_scale must be finite and >= 0");
+    if (hp->inject_wait_timeout != 0 && hp->inject_wait_timeout != 1)
+        return mfail(ZERO1_EINVAL, "inject_wait_timeout must be 0 or 1");
+    if (hp->reserved != 0) return mfail(ZERO1_EINVAL, "reserved must be 0");
     if (hp->nesterov != 0 && hp->nesterov != 1) return mfail(ZERO1_EINVAL, "nesterov must be 0 or 1");
     if (hp->scale_rule != ZERO1_MUON_SCALE_RMS && hp->scale_rule != ZERO1_MUON_SCALE_SPECTRAL)
         return mfail(ZERO1_EINVAL, "unknown scale_rule %d", (int)hp->scale_rule);
@@ -454,6 +457,7 @@ zero1::MuonScalars scalars(const zero1_muon_ctx *h)
     s.c = (float)h->hp.ns_c;
     s.nesterov = h->hp.nesterov;
     s.steps = h->hp.ns_steps;
+    s.stall = h->hp.inject_wait_timeout;
     return s;
 }
 

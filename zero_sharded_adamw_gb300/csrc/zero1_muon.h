@@ -77,6 +77,7 @@ struct MuonScalars {
     float lr, decay;           // decay = 1 - lr * weight_decay
     float a, b, c;
     int nesterov, steps;
+    int stall;                 // failure test: no tiles are drawn
 };
 
 cudaError_t launch_muon_momentum(const MuonDev &d, const MuonScalars &sc, const void *const *grads, int world,

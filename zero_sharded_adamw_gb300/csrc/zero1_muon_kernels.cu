@@ -283,7 +283,7 @@ struct NsParams {
     MuonDev d;
     float a, b, c;
     uint32_t total;
-    int steps;
+    int steps, stall;
 };
 
 // The linear and the square term come from one product, c A' (A' + v I) with
@@ -489,7 +489,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNsThreads, 1)
 
     if (threadIdx.x == 32 && rank == 1) {
         // ---- tiles, one ahead: drawing and describing one takes 2 us of dependent reads
-        for (uint32_t n = 0;; ++n) {
+        for (uint32_t n = 0; !p.stall; ++n) {
             const int slot = n % kSlots;
             if (n >= kSlots && !tc::pair_wait(&sh.slot_empty[slot], (n / kSlots - 1) & 1u, abort, errors)) break;
             const uint32_t ticket = atomicAdd(p.d.ticket, 1u);
@@ -826,6 +826,7 @@ cudaError_t launch_muon_iterate(const MuonDev &d, const MuonScalars &sc, int num
     p.b = sc.b;
     p.c = sc.c;
     p.steps = sc.steps;
+    p.stall = sc.stall;
     p.total = d.work_per_iter * (uint32_t)sc.steps;
     const uint32_t pairs = (uint32_t)num_sms / 2;
     const uint32_t grid = 2 * (p.total < pairs ? p.total : pairs);

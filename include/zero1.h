@@ -582,12 +582,14 @@ typedef struct zero1_muon_ctx *zero1_muon_handle;
 
 /* Plan the step of `count` matrices (at most 65,536) of flat buffers of n
  * entries over `world` emulated ranks, and allocate its workspace on the
- * current device with cudaMalloc: 8 bytes an entry (rows padded to 64
- * entries) and 8 bytes an entry of the Gram matrices.  `mats` is copied.
+ * current device with cudaMalloc.  Small matrices (a side of at most 128 and
+ * the other at most 1,536) need none; a larger one of sides s <= l takes
+ * 8 bytes an entry (rows padded to 64 entries), 8 bytes an entry of the
+ * s x s Gram matrix and 1 KB for each of its rows.  `mats` is copied.
  * Matrices may be given in any order; no two may share an entry, and two
  * whose extents interleave must have one ld.  Sides are 1 to 2^22.
- * Errors: ZERO1_EINVAL (before any device call), ZERO1_ENODEV,
- * ZERO1_ENOMEM, ZERO1_ECUDA.  On error *out is NULL. */
+ * Errors: ZERO1_EINVAL (before any device call but that for the number of
+ * SMs), ZERO1_ENODEV, ZERO1_ENOMEM, ZERO1_ECUDA.  On error *out is NULL. */
 int zero1_muon_create(uint64_t n, int world, const zero1_matrix *mats, uint64_t count,
                       const zero1_muon_hparams *hp, zero1_muon_handle *out);
 

@@ -220,3 +220,30 @@ def test_gradients_into_a_flat_buffer_at_an_odd_offset():
     _, rdg, rdb, _, _ = ref_bwd(dy, x, gamma, mean, rstd)
     assert rel(flat.t[301:301 + cols], rdg) <= 2.0 ** -8 and rel(flat.t[301 + cols:301 + 2 * cols], rdb) <= 2.0 ** -8
     assert (flat.t[:301].float() == 9).all() and (flat.t[301 + 2 * cols:].float() == 9).all() and flat.intact()
+
+
+@pytest.mark.parametrize("cols", [96, 1001])
+def test_rows_past_32_bits(cols):
+    """Rows so far apart that the last begins beyond 2^32 entries; forward and
+    backward in place."""
+    rows, ld = 3, (1 << 31) + 8
+    full = torch.zeros((rows - 1) * ld + cols, dtype=torch.bfloat16, device="cuda")
+    x = torch.as_strided(full, (rows, cols), (ld, 1))
+    keep = torch.randn(rows, cols, device="cuda").to(torch.bfloat16)
+    x.copy_(keep)
+    gamma = torch.randn(cols, device="cuda").to(torch.bfloat16)
+    mean, rstd = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    z.zero1_layernorm_forward(rows, cols, z.DTYPE_BF16, x, ld, gamma, None, EPS, x, ld, mean, rstd)
+    ry, rm, rr = ref_fwd(keep, gamma, None)
+    assert rel(x, ry) <= TOL[torch.bfloat16] and rel(rstd, rr) <= 1e-5
+    dy = torch.randn(rows, cols, device="cuda").to(torch.bfloat16)
+    x.copy_(dy)                                   # dy, and dx in its place
+    dg, db = torch.empty(cols, device="cuda"), torch.empty(cols, device="cuda")
+    work = torch.empty(z.zero1_layernorm_workspace(rows, cols), dtype=torch.uint8, device="cuda")
+    z.zero1_layernorm_backward(rows, cols, z.DTYPE_BF16, x, ld, keep, cols, gamma, mean, rstd, x, ld, dg, db,
+                               z.DTYPE_F32, work)
+    rdx, rdg, rdb, sg, sb = ref_bwd(dy, keep, gamma, mean, rstd)
+    assert rel(x, rdx) <= TOL[torch.bfloat16]
+    assert (dg.double() - rdg).norm().item() <= 1e-5 * sg and (db.double() - rdb).norm().item() <= 1e-5 * sb
+    del full, x
+    torch.cuda.empty_cache()

@@ -393,3 +393,22 @@ def test_a_wait_that_runs_out_is_reported():
         assert rel(view(out, 0, 300, 200), ref_orth(view(u, 0, 300, 200))) <= PLAIN
         with pytest.raises(z.Zero1Error):
             bad.status()
+
+
+def test_offsets_past_32_bits():
+    """A large and a small matrix that lie beyond 2^32 entries of their buffer."""
+    at = (1 << 32) + 24
+    mats = [(at, 200, 150), (at + 200 * 150, 40, 64)]
+    n = at + 200 * 150 + 40 * 64
+    flat = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    u = torch.randn(n - at, device="cuda", generator=torch.Generator(device="cuda").manual_seed(5)).to(torch.bfloat16)
+    flat[at:] = u
+    with z.Muon(n, 1, mats) as opt:
+        opt.orthogonalize(flat, flat)
+        opt.status()
+    for off, r, c in mats:
+        got, want = view(flat, off, r, c), ref_orth(view(u, off - at, r, c))
+        assert rel(got, want) <= PLAIN + 2.0 ** -8
+    assert not flat[:4096].any() and not flat[at - 4096:at].any()
+    del flat
+    torch.cuda.empty_cache()

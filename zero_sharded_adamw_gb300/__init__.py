@@ -698,7 +698,7 @@ def _take_rows(x, rows: int, cols: int, ld: int, kind: str | None, what: str) ->
         if not x.is_cuda:
             raise Zero1ArgumentError(f"{what}: expected a CUDA tensor, got {x.device}")
         if rows:
-            if x.dim() > 1 and x.stride(-1) != 1 and x.shape[-1] > 1:
+            if x.dim() > 0 and x.stride(-1) != 1 and x.shape[-1] > 1:
                 raise Zero1ArgumentError(f"{what}: the entries of a row must be adjacent")
             held = x.untyped_storage().nbytes() // x.element_size() - x.storage_offset()
             if held < (rows - 1) * ld + cols:

@@ -613,6 +613,9 @@ int check_sizes(uint64_t rows, uint64_t cols, int dtype)
     return ZERO1_OK;
 }
 
+// Strides whose last row is past 2^50 entries name no memory (and, multiplied, could leave 64 bits).
+bool stride_ok(uint64_t rows, uint64_t cols, uint64_t ld) { return ld >= cols && ld <= ((uint64_t)1 << 50) / (rows ? rows : 1); }
+
 }  // namespace
 }  // namespace zero1
 
@@ -625,7 +628,9 @@ int zero1_layernorm_forward(uint64_t rows, uint64_t cols, int dtype, const void 
     const int rc = check_sizes(rows, cols, dtype);
     if (rc) return rc;
     if (!(eps >= 0.0 && eps < 1e30)) return lfail(ZERO1_EINVAL, "eps must be finite and >= 0");
-    if (ldx < cols || ldy < cols) return lfail(ZERO1_EINVAL, "row strides must be at least cols");
+    if (!stride_ok(rows, cols, ldx) || !stride_ok(rows, cols, ldy))
+        return lfail(ZERO1_EINVAL, "row strides must be at least cols, and rows times one at most 2^50");
+    if (x && x == y && ldx != ldy && rows > 1) return lfail(ZERO1_EINVAL, "y may be x with the same row stride only");
     if (rows == 0) return ZERO1_OK;
     if (!x || !gamma || !y || !mean || !rstd) return lfail(ZERO1_EINVAL, "NULL pointer argument");
     const size_t e = dtype == ZERO1_DTYPE_BF16 ? 2 : 4;
@@ -655,7 +660,9 @@ int zero1_layernorm_backward(uint64_t rows, uint64_t cols, int dtype, const void
     int rc = check_sizes(rows, cols, dtype);
     if (rc) return rc;
     if (grad_dtype != ZERO1_DTYPE_BF16 && grad_dtype != ZERO1_DTYPE_F32) return lfail(ZERO1_EINVAL, "bad grad_dtype");
-    if (lddy < cols || ldx < cols || lddx < cols) return lfail(ZERO1_EINVAL, "row strides must be at least cols");
+    if (!stride_ok(rows, cols, lddy) || !stride_ok(rows, cols, ldx) || !stride_ok(rows, cols, lddx))
+        return lfail(ZERO1_EINVAL, "row strides must be at least cols, and rows times one at most 2^50");
+    if (dx && dx == dy && lddx != lddy && rows > 1) return lfail(ZERO1_EINVAL, "dx may be dy with the same row stride only");
     if (!gamma || !dgamma || !workspace || (rows > 0 && (!dy || !x || !mean || !rstd || !dx)))
         return lfail(ZERO1_EINVAL, "NULL pointer argument");
     uint64_t need = 0;

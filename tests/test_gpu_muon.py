@@ -412,3 +412,18 @@ def test_offsets_past_32_bits():
     assert not flat[:4096].any() and not flat[at - 4096:at].any()
     del flat
     torch.cuda.empty_cache()
+
+
+def test_a_refused_allocation_leaves_no_error_behind():
+    """Eight matrices of 65,536 x 65,536 need half a terabyte: creation says so,
+    and the calls after it on the same thread are judged by their own launches."""
+    side = 65536
+    with pytest.raises(z.Zero1Error) as e:
+        z.Muon(8 * side * side, 1, [(i * side * side, side, side) for i in range(8)])
+    assert e.value.code == -3, e.value
+    x = torch.randn(16, 300, device="cuda")
+    y, mean, rstd, gamma = torch.empty_like(x), torch.empty(16, device="cuda"), torch.empty(16, device="cuda"), torch.ones(300, device="cuda")
+    z.zero1_layernorm_forward(16, 300, z.DTYPE_F32, x, 300, gamma, None, 1e-5, y, 300, mean, rstd)
+    assert rel(y, torch.nn.functional.layer_norm(x.double(), (300,), eps=1e-5)) < 1e-6
+    u = torch.randn(130, 140, device="cuda")
+    assert rel(run_orth(u), ref_orth(u)) < PLAIN

@@ -23,6 +23,7 @@ SOURCES = ["zero1_host.cu", "zero1_kernels.cu", "zero1_noalloc.cu", "zero1_allre
            "zero1_layernorm.cu"]
 HEADERS = [os.path.join(CSRC, "zero1_internal.h"), os.path.join(CSRC, "zero1_ptx.cuh"), os.path.join(CSRC, "zero1_policy.h"),
            os.path.join(CSRC, "zero1_muon.h"), os.path.join(CSRC, "zero1_muon_device.cuh"), os.path.join(CSRC, "zero1_tc.cuh"),
+           os.path.join(CSRC, "zero1_launch.h"),
            os.path.join(INCLUDE, "zero1.h")]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")

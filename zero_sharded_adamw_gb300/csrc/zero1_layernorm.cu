@@ -25,6 +25,7 @@
 
 #include "zero1.h"
 #include "zero1_internal.h"
+#include "zero1_launch.h"
 #include "zero1_ptx.cuh"
 
 namespace zero1 {
@@ -444,18 +445,23 @@ int lfail(int code, const char *fmt, ...)
     return code;
 }
 
+int lcuda(cudaError_t e, const char *what)
+{
+    cudaGetLastError();   // reported here, and not again by the caller's next launch
+    return lfail(ZERO1_ECUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
 template <typename T, int V, int TPR, int NV, int THREADS>
-bool fwd(const FwdParams<T> &p, cudaStream_t st)
+cudaError_t fwd(const FwdParams<T> &p, cudaStream_t st)
 {
     constexpr uint64_t per = THREADS / TPR;
-    zero1_layernorm_fwd_kernel<T, V, TPR, NV, THREADS><<<(unsigned)((p.rows + per - 1) / per), THREADS, 0, st>>>(p);
-    return true;
+    return launch(zero1_layernorm_fwd_kernel<T, V, TPR, NV, THREADS>, (unsigned)((p.rows + per - 1) / per), THREADS, 0, st, p);
 }
 
 // The variants by pieces of a row: a warp while a lane holds at most 8 (32
 // single entries), then a block of 256 threads.
 template <typename T, int V>
-bool fwd_pick(const FwdParams<T> &p, cudaStream_t st)
+cudaError_t fwd_pick(const FwdParams<T> &p, cudaStream_t st)
 {
     const uint32_t n = (p.cols + V - 1) / V;
     if (n <= 32) return fwd<T, V, 32, 1, 256>(p, st);
@@ -470,7 +476,7 @@ bool fwd_pick(const FwdParams<T> &p, cudaStream_t st)
     if (n <= 2048) return fwd<T, V, 256, 8, 256>(p, st);
     if constexpr (V == 1)
         if (n <= 8192) return fwd<T, V, 512, 16, 512>(p, st);
-    return false;
+    return cudaErrorNotSupported;
 }
 
 // Blocks of the backward pass (each leaves one partial row) where a block
@@ -487,8 +493,7 @@ cudaError_t bwd(const BwdParams<T> &p, int *blocks, cudaStream_t st)
     const size_t fold = TPR < THREADS ? (size_t)(THREADS / TPR) * p.cols * sizeof(float) : 0;   // at most 32 KB
     const int n = (int)partial_rows(p.rows, THREADS / TPR);
     *blocks = n < *blocks ? n : *blocks;
-    zero1_layernorm_bwd_kernel<T, V, TPR, NV, THREADS, AHEAD><<<*blocks, THREADS, fold, st>>>(p);
-    return cudaGetLastError();
+    return launch(zero1_layernorm_bwd_kernel<T, V, TPR, NV, THREADS, AHEAD>, *blocks, THREADS, fold, st, p);
 }
 
 // The variants by pieces of a row: a warp a row while its lanes hold the
@@ -543,10 +548,10 @@ int forward(uint64_t rows, uint64_t cols, const void *x, uint64_t ldx, const voi
     p.inv_n = (float)(1.0 / (double)cols);
     const bool vec = cols % V == 0 && aligned_for<T, V>(p.x, ldx) && aligned_for<T, V>(p.y, ldy) &&
                      aligned_for<T, V>(p.gamma, 0) && aligned_for<T, V>(p.beta, 0);
-    if (!(vec ? fwd_pick<T, V>(p, st) : fwd_pick<T, 1>(p, st)))
-        zero1_layernorm_fwd_wide_kernel<T><<<(unsigned)rows, 1024, 0, st>>>(p);
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? ZERO1_OK : lfail(ZERO1_ECUDA, "kernel launch: %s", cudaGetErrorString(e));
+    cudaError_t e = vec ? fwd_pick<T, V>(p, st) : fwd_pick<T, 1>(p, st);
+    if (e == cudaErrorNotSupported)   // wider than any
+        e = launch(zero1_layernorm_fwd_wide_kernel<T>, (unsigned)rows, 1024, 0, st, p);
+    return e == cudaSuccess ? ZERO1_OK : lcuda(e, "kernel launch");
 }
 
 template <typename T, int V>
@@ -575,32 +580,20 @@ int backward(uint64_t rows, uint64_t cols, const void *dy, uint64_t lddy, const 
     cudaError_t e = vec ? bwd_pick<T, V>(p, &blocks, st) : bwd_pick<T, 1>(p, &blocks, st);
     if (e == cudaErrorNotSupported) {   // wider than any
         const dim3 grid(blocks, (unsigned)((cols + kWideTile - 1) / kWideTile));
-        zero1_layernorm_cols_wide_kernel<T><<<grid, kLnThreads, 0, st>>>(p);
-        e = cudaGetLastError();
-        if (e == cudaSuccess && rows > 0) {
-            zero1_layernorm_bwd_wide_kernel<T><<<(unsigned)rows, 1024, 0, st>>>(p);
-            e = cudaGetLastError();
-        }
+        e = launch(zero1_layernorm_cols_wide_kernel<T>, grid, kLnThreads, 0, st, p);
+        if (e == cudaSuccess && rows > 0) e = launch(zero1_layernorm_bwd_wide_kernel<T>, (unsigned)rows, 1024, 0, st, p);
     }
     if (e == cudaSuccess) {
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3((unsigned)((2 * cols + 31) / 32));
-        cfg.blockDim = dim3(1024);
-        cfg.stream = st;
-        cudaLaunchAttribute attr{};
-        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr.val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
+        const unsigned grid = (unsigned)((2 * cols + 31) / 32);
         const float *src = partials;
         if (grad_bf16)
-            e = cudaLaunchKernelEx(&cfg, zero1_layernorm_cols_kernel<uint16_t>, src, blocks, p.cols,
-                                   static_cast<uint16_t *>(dgamma), static_cast<uint16_t *>(dbeta));
+            e = launch_early(zero1_layernorm_cols_kernel<uint16_t>, grid, 1024, 0, st, src, blocks, p.cols,
+                             static_cast<uint16_t *>(dgamma), static_cast<uint16_t *>(dbeta));
         else
-            e = cudaLaunchKernelEx(&cfg, zero1_layernorm_cols_kernel<float>, src, blocks, p.cols,
-                                   static_cast<float *>(dgamma), static_cast<float *>(dbeta));
+            e = launch_early(zero1_layernorm_cols_kernel<float>, grid, 1024, 0, st, src, blocks, p.cols,
+                             static_cast<float *>(dgamma), static_cast<float *>(dbeta));
     }
-    return e == cudaSuccess ? ZERO1_OK : lfail(ZERO1_ECUDA, "kernel launch: %s", cudaGetErrorString(e));
+    return e == cudaSuccess ? ZERO1_OK : lcuda(e, "kernel launch");
 }
 
 bool on(const void *p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
@@ -677,7 +670,7 @@ int zero1_layernorm_backward(uint64_t rows, uint64_t cols, int dtype, const void
     int dev = 0, sms = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (err != cudaSuccess) return lfail(ZERO1_ECUDA, "device query: %s", cudaGetErrorString(err));
+    if (err != cudaSuccess) return lcuda(err, "device query");
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     float *w = static_cast<float *>(workspace);
     const bool gb = grad_dtype == ZERO1_DTYPE_BF16;

@@ -7,6 +7,8 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <exception>
+#include <memory>
 #include <mutex>
 #include <new>
 #include <unordered_set>
@@ -50,6 +52,7 @@ int mfail(int code, const char *fmt, ...)
 
 int mcuda(cudaError_t e, const char *what)
 {
+    cudaGetLastError();   // reported here, and not again by the caller's next launch
     return mfail(e == cudaErrorMemoryAllocation ? ZERO1_ENOMEM : ZERO1_ECUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
@@ -228,6 +231,15 @@ int device_sms()
     return sms;
 }
 
+// A handle under construction: its memory goes with it.
+struct FreeHandle {
+    void operator()(zero1_muon_ctx *h) const
+    {
+        if (h->block) cudaFree(h->block);
+        delete h;
+    }
+};
+
 // Where each part of the one allocation lies.
 struct Layout {
     uint64_t at = 0;
@@ -368,7 +380,7 @@ int create(uint64_t n, int world, const zero1_matrix *mats, uint64_t count, cons
         poly[i] = l.take(plan[i].splane * 4);
         diag[i] = l.take((uint64_t)plan[i].s * zero1::kNsRows * 4);
     }
-    zero1_muon_ctx *h = new zero1_muon_ctx;
+    std::unique_ptr<zero1_muon_ctx, FreeHandle> h(new zero1_muon_ctx);
     h->n = n;
     h->world = world;
     h->hp = *hp;
@@ -377,7 +389,7 @@ int create(uint64_t n, int world, const zero1_matrix *mats, uint64_t count, cons
     h->entries = entries;
     h->block_bytes = l.at;
     if ((e = cudaMalloc(&h->block, h->block_bytes)) != cudaSuccess) {
-        delete h;
+        h->block = nullptr;
         return mcuda(e, "cudaMalloc of the matrix optimizer's workspace");
     }
     unsigned char *base = static_cast<unsigned char *>(h->block);
@@ -409,11 +421,8 @@ int create(uint64_t n, int world, const zero1_matrix *mats, uint64_t count, cons
     put(at_small, small_list.data(), small_list.size() * sizeof(uint32_t));
     put(at_chunk, chunk_mat.data(), chunk_mat.size() * sizeof(uint32_t));
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
-    if (e != cudaSuccess) {
-        cudaFree(h->block);
-        delete h;
+    if (e != cudaSuccess)
         return good ? mcuda(e, "filling the workspace") : mfail(ZERO1_ECUDA, "encoding a tensor map failed");
-    }
     zero1::MuonDev &d = h->dev;
     d.mats = reinterpret_cast<MuonMat *>(base + at_mats);
     d.maps = reinterpret_cast<CUtensorMap *>(base + at_maps);
@@ -437,9 +446,9 @@ int create(uint64_t n, int world, const zero1_matrix *mats, uint64_t count, cons
     h->any_small = !small_list.empty();
     {
         std::lock_guard<std::mutex> lk(g_muon_mu);
-        g_muon_live.insert(h);
+        g_muon_live.insert(h.get());
     }
-    *out = h;
+    *out = h.release();
     return ZERO1_OK;
 }
 
@@ -472,6 +481,8 @@ int zero1_muon_create(uint64_t n, int world, const zero1_matrix *mats, uint64_t 
         return create(n, world, mats, count, hp, out);
     } catch (const std::bad_alloc &) {
         return mfail(ZERO1_ENOMEM, "host allocation failed");
+    } catch (const std::exception &x) {
+        return mfail(ZERO1_EINVAL, "%s", x.what());
     }
 }
 

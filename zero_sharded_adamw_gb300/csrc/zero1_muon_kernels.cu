@@ -19,8 +19,9 @@
 // active, DRAM 10%), of 4096 x 16384 7.17 ms, 1.9 PFLOP/s; all 48 matrices of
 // the GPT-2-small blocks 2.19 ms, 1.6 PFLOP/s.  Bound by latency where they
 // are few: three 768 x 768 take 0.23 ms, 15.5 us for each of fifteen
-// products one after another, of which 7 us are products.
+// products one after another, of which 8 us are products.
 #include "zero1_internal.h"
+#include "zero1_launch.h"
 #include "zero1_muon.h"
 #include "zero1_muon_device.cuh"
 #include "zero1_tc.cuh"
@@ -754,8 +755,7 @@ cudaError_t momentum_t(const MuonDev &d, const MuonScalars &sc, const void *cons
     p.momentum = momentum;
     p.world = world;
     p.sc = sc;
-    muon_momentum_kernel<CAP><<<grid, kElemThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch(muon_momentum_kernel<CAP>, grid, kElemThreads, 0, stream, p);
 }
 
 template <int CAP>
@@ -771,24 +771,6 @@ cudaError_t apply_t(const MuonDev &d, const MuonScalars &sc, void *const *params
     p.world = world;
     p.region = sc.steps & 1;
     return launch_early(muon_apply_kernel<CAP>, d.nchunks, kElemThreads, 0, stream, p);
-}
-
-// A launch that may begin while the one before it on the stream still runs:
-// the kernel waits for its end (griddepcontrol.wait) before it reads anything.
-template <typename K, typename... Args>
-cudaError_t launch_early(K kernel, uint32_t grid, uint32_t threads, int smem, cudaStream_t stream, Args... args)
-{
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = (size_t)smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // The first kernel of a call also clears one counter a matrix.
@@ -812,10 +794,8 @@ cudaError_t launch_muon_momentum(const MuonDev &d, const MuonScalars &sc, const 
 cudaError_t launch_muon_norm(const MuonDev &d, const void *in, bool bf16, cudaStream_t stream)
 {
     if (bf16)
-        muon_norm_kernel<<<first_grid(d), kElemThreads, 0, stream>>>(d, static_cast<const uint16_t *>(in));
-    else
-        muon_norm_kernel<<<first_grid(d), kElemThreads, 0, stream>>>(d, static_cast<const float *>(in));
-    return cudaGetLastError();
+        return launch(muon_norm_kernel<uint16_t>, first_grid(d), kElemThreads, 0, stream, d, static_cast<const uint16_t *>(in));
+    return launch(muon_norm_kernel<float>, first_grid(d), kElemThreads, 0, stream, d, static_cast<const float *>(in));
 }
 
 cudaError_t launch_muon_split(const MuonDev &d, const MuonScalars &sc, const void *in, bool bf16, cudaStream_t stream)

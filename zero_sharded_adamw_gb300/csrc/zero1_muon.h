@@ -69,8 +69,15 @@ struct MuonSmall {
 // Columns of the larger side a block holds, at most: X, two f16 parts of 128
 // rows, beside the Gram matrix (64 KB) and, in a cluster, the parts of its
 // sum (64 KB).
-inline uint32_t small_width(int blocks) { return blocks == 1 ? 256 : 192; }
-inline int small_smem(int blocks) { return (int)(2 * 128 * 2 * small_width(blocks)) + (blocks == 1 ? 1 : 2) * 65536 + 1024; }
+constexpr uint32_t small_width(int blocks) { return blocks == 1 ? 256 : 192; }
+constexpr int small_smem(int blocks) { return (int)(2 * 128 * 2 * small_width(blocks)) + (blocks == 1 ? 1 : 2) * 65536 + 1024; }
+
+// Blocks of a cluster that take tensor memory have their SMs to themselves:
+// with two such clusters on the same two SMs, each could hold the columns
+// that the other's second block waits for.  Shared memory keeps them apart
+// (228 KB an SM): 200 KB leave no room for another such block.
+constexpr int kAloneSmem = 200 * 1024;
+static_assert(small_smem(2) >= kAloneSmem, "two clusters could wait for each other's tensor memory");
 
 struct MuonScalars {
     float inv_w, momentum, one_minus_momentum, eps;

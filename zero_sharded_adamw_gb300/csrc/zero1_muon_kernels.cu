@@ -277,6 +277,7 @@ struct Shape {
     static constexpr int kAccs = 2;
     static constexpr uint32_t kAccCols = 256;
     static constexpr int kSmem = kStages * kStageBytes + 4 * kGroups * kWarpOut + 1024;
+    static_assert(kSmem >= kAloneSmem, "two pairs could wait for each other's tensor memory");
 };
 // K of one accumulator.  The tensor cores cut every addition of 16 products
 // off below the sum's last place, so a sum of positive terms falls short by

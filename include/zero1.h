@@ -616,6 +616,11 @@ int zero1_muon_destroy(zero1_muon_handle h);
  * A matrix of zeros is moved by its decay alone.  A gradient with an
  * infinity or a NaN makes its own matrix NaN, and no other.  Deterministic:
  * the same inputs give the same bits.
+ * On a stream of an SM partition: a small matrix (zero1_muon_create) of a
+ * larger side above 256 runs as a cluster of 2, 4 (above 384) or 8 (above
+ * 768) blocks that needs as many SMs of one processing cluster, and the rest
+ * of a partition may have too few of them; the call is then refused
+ * (ZERO1_EINVAL) before anything runs.
  * Errors: ZERO1_EINVAL, ZERO1_EALIGN, ZERO1_ECUDA. */
 int zero1_muon_step(zero1_muon_handle h, const void *const *grad_ptrs, void *const *param_ptrs, float *master,
                     float *momentum, void *stream);

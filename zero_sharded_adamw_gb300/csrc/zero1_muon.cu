@@ -470,6 +470,18 @@ zero1::MuonScalars scalars(const zero1_muon_ctx *h)
     return s;
 }
 
+// Before anything of a call runs: a cluster that the stream's SMs cannot hold would never start.
+int check_clusters(const zero1_muon_ctx *h, cudaStream_t st)
+{
+    if (!h->any_small) return ZERO1_OK;
+    int blocks = 0;
+    const cudaError_t e = zero1::muon_small_misfit(h->small, st, &blocks);
+    if (e != cudaSuccess) return mcuda(e, "cluster query");
+    if (blocks)
+        return mfail(ZERO1_EINVAL, "the stream's SMs hold no cluster of %d blocks, which a matrix of this handle needs", blocks);
+    return ZERO1_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -516,6 +528,7 @@ int zero1_muon_step(zero1_muon_handle h, const void *const *grad_ptrs, void *con
         return mfail(ZERO1_EALIGN, "master and momentum must be 16-byte aligned");
     MuonDeviceGuard g(h->device);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (const int rc = check_clusters(h, st)) return rc;
     const zero1::MuonScalars sc = scalars(h);
     cudaError_t e = cudaSuccess;
     if (h->any_small)
@@ -538,6 +551,7 @@ int zero1_muon_orthogonalize(zero1_muon_handle h, const void *in, int in_dtype, 
     if (!aligned16(in) || !aligned16(out)) return mfail(ZERO1_EALIGN, "buffers must be 16-byte aligned");
     MuonDeviceGuard g(h->device);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (const int rc = check_clusters(h, st)) return rc;
     const zero1::MuonScalars sc = scalars(h);
     const bool bf = in_dtype == ZERO1_DTYPE_BF16;
     cudaError_t e = cudaSuccess;

@@ -93,6 +93,10 @@ cudaError_t launch_muon_norm(const MuonDev &d, const void *in, bool bf16, cudaSt
 // `in` null: the fp32 update that launch_muon_momentum left in region 1.
 cudaError_t launch_muon_split(const MuonDev &d, const MuonScalars &sc, const void *in, bool bf16, cudaStream_t stream);
 cudaError_t launch_muon_iterate(const MuonDev &d, const MuonScalars &sc, int num_sms, cudaStream_t stream);
+// The blocks of the smallest cluster in use that does not fit the stream's SMs
+// (all blocks of a cluster run at once, on SMs of one processing cluster, and
+// a stream of an SM partition may have too few of them), or 0 if all fit.
+cudaError_t muon_small_misfit(const MuonSmall &small, cudaStream_t stream, int *blocks);
 cudaError_t launch_muon_small_step(const MuonDev &d, const MuonSmall &small, const MuonScalars &sc,
                                    const void *const *grads, void *const *params, int world, float *master,
                                    float *momentum, cudaStream_t stream);

@@ -428,27 +428,40 @@ __global__ void __launch_bounds__(kThreads, 1) muon_small_kernel(const __grid_co
     ptx::cluster_sync();
 }
 
+// How the matrices of clusters of 2^i blocks are launched; `attr` has to outlive the configuration.
+cudaLaunchConfig_t small_config(const MuonSmall &small, int i, cudaStream_t stream, cudaLaunchAttribute *attr)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(small.count[i] << i);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = (size_t)small_smem(1 << i);
+    cfg.stream = stream;
+    attr->id = cudaLaunchAttributeClusterDimension;
+    attr->val.clusterDim.x = 1u << i;
+    attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
+template <int CAP>
+cudaError_t allow_small_smem()
+{
+    return allow_dynamic_smem(reinterpret_cast<const void *>(muon_small_kernel<CAP>),
+                              small_smem(1) > small_smem(2) ? small_smem(1) : small_smem(2));
+}
+
 template <int CAP>
 cudaError_t launch_small(const SmallParams<CAP> &base, const MuonSmall &small, cudaStream_t stream)
 {
-    const auto kernel = muon_small_kernel<CAP>;
-    cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), small_smem(1) > small_smem(2) ? small_smem(1) : small_smem(2));
+    cudaError_t e = allow_small_smem<CAP>();
     for (int i = 0; i < kSmallSizes && e == cudaSuccess; ++i) {
         if (small.count[i] == 0) continue;
         SmallParams<CAP> p = base;
         p.list = small.list + small.first[i];
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3(small.count[i] << i);
-        cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = (size_t)small_smem(1 << i);
-        cfg.stream = stream;
         cudaLaunchAttribute attr{};
-        attr.id = cudaLaunchAttributeClusterDimension;
-        attr.val.clusterDim.x = 1u << i;
-        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, kernel, p);
+        const cudaLaunchConfig_t cfg = small_config(small, i, stream, &attr);
+        e = cudaLaunchKernelEx(&cfg, muon_small_kernel<CAP>, p);
     }
     return e;
 }
@@ -471,6 +484,22 @@ cudaError_t step_t(const MuonDev &d, const MuonSmall &small, const MuonScalars &
 }
 
 }  // namespace
+
+// 1 us a cluster size in use.  Shared memory decides, the same for every CAP.
+cudaError_t muon_small_misfit(const MuonSmall &small, cudaStream_t stream, int *blocks)
+{
+    *blocks = 0;
+    cudaError_t e = allow_small_smem<8>();
+    for (int i = 1; i < kSmallSizes && e == cudaSuccess && *blocks == 0; ++i) {
+        if (small.count[i] == 0) continue;
+        cudaLaunchAttribute attr{};
+        const cudaLaunchConfig_t cfg = small_config(small, i, stream, &attr);
+        int fit = 0;
+        e = cudaOccupancyMaxActiveClusters(&fit, muon_small_kernel<8>, &cfg);
+        if (e == cudaSuccess && fit < 1) *blocks = 1 << i;
+    }
+    return e;
+}
 
 cudaError_t launch_muon_small_step(const MuonDev &d, const MuonSmall &small, const MuonScalars &sc,
                                    const void *const *grads, void *const *params, int world, float *master,

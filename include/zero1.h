@@ -627,8 +627,9 @@ int zero1_muon_step(zero1_muon_handle h, const void *const *grad_ptrs, void *con
 
 /* The orthogonalisation alone: out = the iterated X of every matrix of the
  * flat buffer `in` (n entries each, ZERO1_DTYPE_BF16 or ZERO1_DTYPE_F32,
- * 16-byte aligned; out may be in when the types are equal).  Entries of out
- * outside the matrices keep their values.  Asynchronous, allocation-free.
+ * 16-byte aligned; out may be in when the types are equal, and is refused
+ * when they are not).  Entries of out outside the matrices keep their values.
+ * Asynchronous, allocation-free.
  * Errors: ZERO1_EINVAL, ZERO1_EALIGN, ZERO1_ECUDA. */
 int zero1_muon_orthogonalize(zero1_muon_handle h, const void *in, int in_dtype, void *out, int out_dtype,
                              void *stream);

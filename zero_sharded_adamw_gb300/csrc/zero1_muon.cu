@@ -548,6 +548,8 @@ int zero1_muon_orthogonalize(zero1_muon_handle h, const void *in, int in_dtype, 
     if ((in_dtype != ZERO1_DTYPE_BF16 && in_dtype != ZERO1_DTYPE_F32) ||
         (out_dtype != ZERO1_DTYPE_BF16 && out_dtype != ZERO1_DTYPE_F32))
         return mfail(ZERO1_EINVAL, "bad dtype");
+    // a block may write its matrix where another has yet to read its own
+    if (in == out && in_dtype != out_dtype) return mfail(ZERO1_EINVAL, "out may be in only when their types are equal");
     if (!aligned16(in) || !aligned16(out)) return mfail(ZERO1_EALIGN, "buffers must be 16-byte aligned");
     MuonDeviceGuard g(h->device);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -229,15 +229,15 @@ def _dtype_name(x) -> str:
     return name
 
 
-def _take(x, count: int, kind: str, what: str) -> int | None:
-    """Address of device buffer `x` after _check_buffer, whose tests an
-    ordinary CUDA tensor passes here in one line."""
+def _take(x, count: int, kind: str, what: str, rank: int | None = None) -> int | None:
+    """Address of device buffer `x` (of that rank) after _check_buffer, whose
+    tests an ordinary CUDA tensor passes here in one line."""
     try:
         if x.dtype is _TORCH_DTYPES[kind] and x.is_cuda and x.is_contiguous() and x.numel() >= count:
             return x.data_ptr()
     except (AttributeError, KeyError):
         pass
-    _check_buffer(x, count, kind, True, what)
+    _check_buffer(x, count, kind, True, what if rank is None else f"{what}[{rank}]")
     return _addr(x)
 
 
@@ -287,7 +287,7 @@ def _ptrs(xs, world: int | None = None, count: int | None = None, kind: str | No
         return xs.array
     if count is not None and kind is not None:
         if on_device:
-            return (C.c_void_p * n)(*[_take(x, count, kind, what) for x in xs])
+            return (C.c_void_p * n)(*[_take(x, count, kind, what, r) for r, x in enumerate(xs)])
         for r, x in enumerate(xs):
             _check_buffer(x, count, kind, on_device, f"{what}[{r}]")
     return (C.c_void_p * n)(*[_addr(x) for x in xs])

@@ -684,8 +684,8 @@ class Muon:
 
 def _take_rows(x, rows: int, cols: int, ld: int, kind: str | None, what: str) -> int | None:
     """Address of `x`, after refusing a torch tensor that is not CUDA memory of
-    the type or does not reach as far as rows `ld` apart do.  Raw addresses
-    pass."""
+    the type, has these rows at another stride than `ld`, or does not reach as
+    far as rows `ld` apart do.  Raw addresses pass."""
     try:
         if x.dtype is _TORCH_DTYPES[kind] and x.is_cuda and x.shape == (rows, cols) and x.stride() == (ld, 1):
             return x.data_ptr()
@@ -700,6 +700,8 @@ def _take_rows(x, rows: int, cols: int, ld: int, kind: str | None, what: str) ->
         if rows:
             if x.dim() > 0 and x.stride(-1) != 1 and x.shape[-1] > 1:
                 raise Zero1ArgumentError(f"{what}: the entries of a row must be adjacent")
+            if rows > 1 and x.shape == (rows, cols) and x.stride(0) != ld:
+                raise Zero1ArgumentError(f"{what}: its row stride is {x.stride(0)}, the call was given {ld}")
             held = x.untyped_storage().nbytes() // x.element_size() - x.storage_offset()
             if held < (rows - 1) * ld + cols:
                 raise Zero1ArgumentError(f"{what}: its memory holds {held} elements, the call reads or writes "

@@ -12,8 +12,8 @@
 // fits (forward up to 2,048 aligned bf16, backward, with its column sums, up
 // to 1,024), then by four to sixteen warps, up to 8,192 columns, or 16,384 of
 // aligned bf16; wider rows are read again from the caches.  The column sums
-// stay in registers over all rows of a thread, one partial row per block goes
-// to the workspace, and a second kernel adds the partial rows in a fixed
+// stay in registers over up to 512 rows of a thread, one partial row per block
+// goes to the workspace, and a second kernel adds the partial rows in a fixed
 // order (no atomics: the same inputs give the same bits).
 //
 // Measured, bf16: forward 16,384 x 768 in 12 us, 65,536 x 4,096 in 184 us
@@ -34,6 +34,12 @@ namespace {
 constexpr int kMaxPartials = 320;      // blocks of the backward pass, at most
 constexpr int kLnThreads = 256;
 constexpr uint32_t kWideTile = 1024;   // columns of one block of the wide column sums
+// Rows whose column sums a thread adds up one after another.  Such a sum of n
+// terms of one sign is off by up to n 2^-24 of itself (1e-4 measured at 13,800
+// fp32 terms), so longer ones are taken in launches of 512 rows a thread
+// (155,648 rows and more), each adding to the partial rows of those before.
+constexpr uint64_t kRun = 512;
+constexpr int kWideRun = 256;          // the same within the wide column sums
 
 template <typename T, int V>
 struct Piece;   // V neighbouring entries as they lie in memory
@@ -215,6 +221,7 @@ struct BwdParams {
     uint64_t rows, lddy, ldx, lddx;
     uint32_t cols;
     float inv_n;
+    int add;               // to what a launch over earlier rows left in the partials
 };
 
 // AHEAD: the next row's pieces are fetched while this one's are used, where
@@ -327,7 +334,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) zero1_layernorm_bwd_ke
             if (c < p.cols) {
                 float *to = kRows > 1 ? fold + (uint64_t)lane_row * p.cols + c : part + c;
 #pragma unroll
-                for (int i = 0; i < V; ++i) to[i] = a[j * V + i];
+                for (int i = 0; i < V; ++i) to[i] = (kRows == 1 && p.add ? to[i] : 0.f) + a[j * V + i];
             }
         }
         if (kRows > 1) {
@@ -336,7 +343,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) zero1_layernorm_bwd_ke
                 float s = 0.f;
 #pragma unroll
                 for (int r = 0; r < kRows; ++r) s += fold[(uint64_t)r * p.cols + c];
-                part[c] = s;
+                part[c] = (p.add ? part[c] : 0.f) + s;
             }
             __syncthreads();
         }
@@ -385,11 +392,16 @@ __global__ void __launch_bounds__(kLnThreads) zero1_layernorm_cols_wide_kernel(c
     float *part = p.partials + (uint64_t)blockIdx.x * 2 * p.cols;
     for (uint32_t c = blockIdx.y * kWideTile + threadIdx.x; c < min(p.cols, (blockIdx.y + 1) * kWideTile); c += kLnThreads) {
         float ag = 0.f, ab = 0.f, x[1], d[1];
-        for (uint64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
-            fetch<T, 1>(p.x + r * p.ldx + c).get(x);
-            fetch<T, 1>(p.dy + r * p.lddy + c).get(d);
-            ag += d[0] * ((x[0] - p.mean[r]) * p.rstd[r]);
-            ab += d[0];
+        for (uint64_t r = blockIdx.x; r < p.rows;) {
+            float sg = 0.f, sb = 0.f;
+            for (int i = 0; i < kWideRun && r < p.rows; ++i, r += gridDim.x) {
+                fetch<T, 1>(p.x + r * p.ldx + c).get(x);
+                fetch<T, 1>(p.dy + r * p.lddy + c).get(d);
+                sg += d[0] * ((x[0] - p.mean[r]) * p.rstd[r]);
+                sb += d[0];
+            }
+            ag += sg;
+            ab += sb;
         }
         part[c] = ag;
         part[p.cols + c] = ab;
@@ -493,7 +505,20 @@ cudaError_t bwd(const BwdParams<T> &p, int *blocks, cudaStream_t st)
     const size_t fold = TPR < THREADS ? (size_t)(THREADS / TPR) * p.cols * sizeof(float) : 0;   // at most 32 KB
     const int n = (int)partial_rows(p.rows, THREADS / TPR);
     *blocks = n < *blocks ? n : *blocks;
-    return launch(zero1_layernorm_bwd_kernel<T, V, TPR, NV, THREADS, AHEAD>, *blocks, THREADS, fold, st, p);
+    const uint64_t piece = kRun * *blocks * (THREADS / TPR);
+    cudaError_t e = cudaSuccess;
+    for (uint64_t first = 0; e == cudaSuccess && (first == 0 || first < p.rows); first += piece) {
+        BwdParams<T> q = p;
+        q.dy += first * p.lddy;
+        q.x += first * p.ldx;
+        q.dx += first * p.lddx;
+        q.mean += first;
+        q.rstd += first;
+        q.rows = p.rows - first < piece ? p.rows - first : piece;
+        q.add = first > 0;
+        e = launch(zero1_layernorm_bwd_kernel<T, V, TPR, NV, THREADS, AHEAD>, *blocks, THREADS, fold, st, q);
+    }
+    return e;
 }
 
 // The variants by pieces of a row: a warp a row while its lanes hold the

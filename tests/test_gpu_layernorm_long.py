@@ -49,7 +49,7 @@ def test_sums_of_one_sign(rows, cols):
     (1_300_001, 40, torch.bfloat16, 0), (1_300_001, 33, torch.float32, 0),       # a warp a row
     (330_007, 301, torch.float32, 2), (160_001, 1100, torch.bfloat16, 1),         # unaligned: half a block, a block
     (160_003, 1028, torch.float32, 4), (160_001, 2056, torch.bfloat16, 0),        # a block a row
-    (90_001, 8201, torch.bfloat16, 0)])                                          # wider than registers (unaligned)
+    (90_001, 8201, torch.bfloat16, 0), (157_001, 8193, torch.bfloat16, 0)])      # wider than registers (unaligned)
 def test_rows_in_several_launches(rows, cols, dtype, pad):
     """Every row is taken once, whichever launch it falls into."""
     gen = torch.Generator(device="cuda").manual_seed(rows)

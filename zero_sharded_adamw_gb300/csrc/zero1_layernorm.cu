@@ -39,7 +39,6 @@ constexpr uint32_t kWideTile = 1024;   // columns of one block of the wide colum
 // fp32 terms), so longer ones are taken in launches of 512 rows a thread
 // (155,648 rows and more), each adding to the partial rows of those before.
 constexpr uint64_t kRun = 512;
-constexpr int kWideRun = 256;          // the same within the wide column sums
 
 template <typename T, int V>
 struct Piece;   // V neighbouring entries as they lie in memory
@@ -392,19 +391,14 @@ __global__ void __launch_bounds__(kLnThreads) zero1_layernorm_cols_wide_kernel(c
     float *part = p.partials + (uint64_t)blockIdx.x * 2 * p.cols;
     for (uint32_t c = blockIdx.y * kWideTile + threadIdx.x; c < min(p.cols, (blockIdx.y + 1) * kWideTile); c += kLnThreads) {
         float ag = 0.f, ab = 0.f, x[1], d[1];
-        for (uint64_t r = blockIdx.x; r < p.rows;) {
-            float sg = 0.f, sb = 0.f;
-            for (int i = 0; i < kWideRun && r < p.rows; ++i, r += gridDim.x) {
-                fetch<T, 1>(p.x + r * p.ldx + c).get(x);
-                fetch<T, 1>(p.dy + r * p.lddy + c).get(d);
-                sg += d[0] * ((x[0] - p.mean[r]) * p.rstd[r]);
-                sb += d[0];
-            }
-            ag += sg;
-            ab += sb;
+        for (uint64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
+            fetch<T, 1>(p.x + r * p.ldx + c).get(x);
+            fetch<T, 1>(p.dy + r * p.lddy + c).get(d);
+            ag += d[0] * ((x[0] - p.mean[r]) * p.rstd[r]);
+            ab += d[0];
         }
-        part[c] = ag;
-        part[p.cols + c] = ab;
+        part[c] = (p.add ? part[c] : 0.f) + ag;
+        part[p.cols + c] = (p.add ? part[p.cols + c] : 0.f) + ab;
     }
 }
 
@@ -499,13 +493,12 @@ uint64_t partial_rows(uint64_t rows, uint64_t at_once)
     return n < 1 ? 1 : n < (uint64_t)kMaxPartials ? n : kMaxPartials;
 }
 
-template <typename T, int V, int TPR, int NV, int THREADS = (TPR > 256 ? TPR : 256), bool AHEAD = true>
-cudaError_t bwd(const BwdParams<T> &p, int *blocks, cudaStream_t st)
+// Launches over kRun rows a thread each, of `blocks` blocks that take
+// `at_once` rows at a time.
+template <typename T, typename F>
+cudaError_t in_runs(const BwdParams<T> &p, int blocks, uint64_t at_once, F one)
 {
-    const size_t fold = TPR < THREADS ? (size_t)(THREADS / TPR) * p.cols * sizeof(float) : 0;   // at most 32 KB
-    const int n = (int)partial_rows(p.rows, THREADS / TPR);
-    *blocks = n < *blocks ? n : *blocks;
-    const uint64_t piece = kRun * *blocks * (THREADS / TPR);
+    const uint64_t piece = kRun * blocks * at_once;
     cudaError_t e = cudaSuccess;
     for (uint64_t first = 0; e == cudaSuccess && (first == 0 || first < p.rows); first += piece) {
         BwdParams<T> q = p;
@@ -516,9 +509,20 @@ cudaError_t bwd(const BwdParams<T> &p, int *blocks, cudaStream_t st)
         q.rstd += first;
         q.rows = p.rows - first < piece ? p.rows - first : piece;
         q.add = first > 0;
-        e = launch(zero1_layernorm_bwd_kernel<T, V, TPR, NV, THREADS, AHEAD>, *blocks, THREADS, fold, st, q);
+        e = one(q);
     }
     return e;
+}
+
+template <typename T, int V, int TPR, int NV, int THREADS = (TPR > 256 ? TPR : 256), bool AHEAD = true>
+cudaError_t bwd(const BwdParams<T> &p, int *blocks, cudaStream_t st)
+{
+    const size_t fold = TPR < THREADS ? (size_t)(THREADS / TPR) * p.cols * sizeof(float) : 0;   // at most 32 KB
+    const int n = (int)partial_rows(p.rows, THREADS / TPR);
+    *blocks = n < *blocks ? n : *blocks;
+    return in_runs(p, *blocks, THREADS / TPR, [&](const BwdParams<T> &q) {
+        return launch(zero1_layernorm_bwd_kernel<T, V, TPR, NV, THREADS, AHEAD>, *blocks, THREADS, fold, st, q);
+    });
 }
 
 // The variants by pieces of a row: a warp a row while its lanes hold the
@@ -605,7 +609,9 @@ int backward(uint64_t rows, uint64_t cols, const void *dy, uint64_t lddy, const 
     cudaError_t e = vec ? bwd_pick<T, V>(p, &blocks, st) : bwd_pick<T, 1>(p, &blocks, st);
     if (e == cudaErrorNotSupported) {   // wider than any
         const dim3 grid(blocks, (unsigned)((cols + kWideTile - 1) / kWideTile));
-        e = launch(zero1_layernorm_cols_wide_kernel<T>, grid, kLnThreads, 0, st, p);
+        e = in_runs(p, blocks, 1, [&](const BwdParams<T> &q) {
+            return launch(zero1_layernorm_cols_wide_kernel<T>, grid, kLnThreads, 0, st, q);
+        });
         if (e == cudaSuccess && rows > 0) e = launch(zero1_layernorm_bwd_wide_kernel<T>, (unsigned)rows, 1024, 0, st, p);
     }
     if (e == cudaSuccess) {

@@ -553,8 +553,8 @@ typedef struct zero1_matrix {
  *     A = X X^T (of the smaller side).  The coefficients (at most 8 in
  *     magnitude, ns_c not 0 and |ns_b| <= 8 |ns_c|) must keep every
  *     iterate's singular values below 2, as (3.4445, -4.7750, 2.0315) does:
- *     entries are held in f16 parts scaled by 4096, and beyond that range
- *     results are infinite or NaN.
+ *     entries are held in scaled f16 parts, and beyond that range results are
+ *     infinite or NaN.
  *   inject_wait_timeout: failure testing only.  1 = the tiled iteration (a
  *     side above 128) is given no tiles, so that its waits run out after
  *     their 1 s limit; the call returns, its results mean nothing, and
@@ -612,7 +612,11 @@ int zero1_muon_destroy(zero1_muon_handle h);
  *     state, so a checkpoint is these two.
  * All buffers 16-byte aligned; entries outside the matrices are neither read
  * nor written.  The products run as three f16 products with fp32
- * accumulators (each factor in a high and a low part), as exact as fp32.
+ * accumulators (each factor in a high and a low part).  By the matrix's norm
+ * the iterated X is about as far from 64 bits as the iteration in fp32 (0.35 to
+ * 2.6 times as far in the matrices measured); entries of U below 7.6e-6 |U| enter it
+ * with an absolute error of up to 1.8e-12 |U|, where fp32 would keep their
+ * leading bits.
  * A matrix of zeros is moved by its decay alone.  A gradient with an
  * infinity or a NaN makes its own matrix NaN, and no other.  Deterministic:
  * the same inputs give the same bits.

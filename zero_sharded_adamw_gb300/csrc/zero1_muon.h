@@ -16,10 +16,15 @@ constexpr uint32_t kNsRows = 256;
 constexpr int kNsParts = 32;           // arrivals a finished tile makes: one by each warp that writes it
 constexpr int kNsTileK = 64;           // K of one pipeline stage
 constexpr uint32_t kMaxSide = 1u << 22;
-// Powers of two the f16 operands are scaled by: every iterate has entries
-// below 2 in magnitude and the Gram matrices below 4, so 4096 keeps them
-// under f16's 65,504 and keeps entries down to 1.5e-8 in its normal range.
-constexpr float kNsScale = 4096.0f;
+// Powers of two the f16 operands are scaled by: singular values below 2 keep
+// every iterate's entries below 2 and the Gram matrices' (and the linear
+// term's beside them) below 14, so 2^14 and 2^12 keep them under f16's 65,504.
+// An operand is held in a high and a low f16 part whose last places are 2^-24
+// at the finest: an entry of X, whose norm starts at one, keeps 22 bits down
+// to 2^-17 = 7.6e-6, and below that the absolute error 2^-25 / 2^14 = 1.8e-12;
+// a Gram matrix's entries keep 22 bits down to 3.1e-5, and 7.3e-12 below.
+constexpr float kXScale = 16384.0f;
+constexpr float kGramScale = 4096.0f;
 
 // One matrix of the plan, in device memory.  X (rows x cols) lives in one
 // half of a two-region ping-pong; a region holds either two f16 planes (the

@@ -58,7 +58,7 @@ __device__ __forceinline__ float load1(const uint16_t *p) { return __uint_as_flo
 __device__ __forceinline__ void store1(float *p, float v) { *p = v; }
 __device__ __forceinline__ void store1(uint16_t *p, float v) { *p = __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
 
-// hi + lo = v to 22 bits, of two neighbours (one conversion of a pair takes
+// hi + lo = v to 22 bits or to 2^-25, whichever is coarser, of two neighbours (one conversion of a pair takes
 // the time of a quarter of one of a single value).
 __device__ __forceinline__ void split(float v, float w, uint32_t &hi, uint32_t &lo)
 {

@@ -8,11 +8,15 @@
 // Singular values far below one grow by a = 3.4 a step, 480-fold over five:
 // an error that a rounding of X leaves there grows with them, and with X in
 // bf16 (2^-9) the result of a matrix with a few strong directions is half
-// noise.  So every operand is kept as two f16 parts, hi + lo = 22 bits, and
-// a product is hi*hi + hi*lo + lo*hi into one fp32 accumulator (the dropped
-// lo*lo is 2^-24).  The result is as exact as the iteration in fp32 (2e-6 of
-// X against 64 bits at 768 x 3072, plain fp32 4e-6), for three tensor-core
-// products in place of one.
+// noise.  So every operand is kept as two f16 parts, hi + lo = 22 bits (fewer
+// for entries far below the others, zero1_muon.h), and a product is hi*hi +
+// hi*lo + lo*hi into one fp32 accumulator (the dropped lo*lo is 2^-24), for
+// three tensor-core products in place of one.  Against 64 bits, by the
+// matrix's norm, the result is off by 1.7e-6 at 768 x 768 (the iteration in
+// plain fp32 by 2.5e-6), 4.4e-6 (7.2e-6) at 4096 x 16384, 2.9e-6 (2.5e-6) at
+// 1031 x 257 and 1.4e-6 (1.0e-6) at 64 x 64; 0.35 to 2.6 times plain fp32's
+// error over all matrices measured.  Half the rows of 768 x 2304 1e-6 of the
+// others in size come out 1e-3 of themselves off (plain fp32: 5e-7).
 //
 // Bound by the tensor cores where tiles are many: five steps of 4096 x 4096
 // take 2.41 ms, 1.76 PFLOP/s over the three products (tensor pipe 79%
@@ -182,7 +186,7 @@ __global__ void __launch_bounds__(kElemThreads) muon_split_kernel(MuonDev d, con
     __syncthreads();
     if (threadIdx.x == 0) {
         for (int i = 1; i < kElemThreads / 32; ++i) t += part[i];
-        factor = (float)((double)kNsScale / (sqrt(t) + (double)eps));
+        factor = (float)((double)kXScale / (sqrt(t) + (double)eps));
     }
     __syncthreads();
     const float k = factor;
@@ -357,17 +361,17 @@ __device__ __forceinline__ void describe(const NsParams &p, uint32_t ticket, Til
     need = iter * (m.parts[0] + m.parts[1] + m.parts[2]) + (t.phase > 0 ? m.parts[0] : 0) + (t.phase > 1 ? m.parts[1] : 0);
     const uint32_t maps = t.mat * kMapsPerMat, x = maps + (iter & 1 ? kMapX1 : kMapX0);
     constexpr uint32_t kAlways = 0xFFFFFFFFu;
-    constexpr float inv = 1.0f / kNsScale;
+    constexpr float inv = 1.0f / kGramScale;
     t.row = ti * kNsRows;
     t.col = tj * p.d.tile;
     const uint32_t block = t.col / kNsRows * kNsRows;   // the diagonal block beside the tile's columns
     const float alpha = alpha_of(iter, p.steps);
-    t.v = (p.b + 2.f * p.c * alpha) / p.c * kNsScale;
+    t.v = (p.b + 2.f * p.c * alpha) / p.c * kGramScale;
     t.diag = 0;
     t.also = nullptr;
     t.also_plane = (uint64_t)m.s * (kNsRows * 2);
     t.last = t.phase == 2 && (int)iter + 1 == p.steps;
-    t.factor = t.phase == 1 ? p.c * inv : t.last ? inv * inv : inv;
+    t.factor = t.phase == 0 ? kGramScale / (kXScale * kXScale) : t.phase == 1 ? p.c * inv : t.last ? inv / kXScale : inv;
     t.on_diagonal = 0.f;
     if (t.phase < 2) {
         t.rows = t.cols = m.s;
@@ -378,7 +382,7 @@ __device__ __forceinline__ void describe(const NsParams &p, uint32_t ticket, Til
             t.map_a = t.map_b = x;
             t.k = m.tall ? m.rows : m.cols;
             t.a_turn = t.b_turn = m.tall ? kAlways : 0;
-            t.on_diagonal = -alpha * kNsScale;
+            t.on_diagonal = -alpha * kGramScale;
             if (t.row == block) t.also = m.diag;
         } else {
             t.map_a = t.map_b = maps + kMapA;
@@ -386,7 +390,7 @@ __device__ __forceinline__ void describe(const NsParams &p, uint32_t ticket, Til
             t.a_turn = t.row;
             t.b_turn = block;
             t.diag = maps + kMapD;
-            t.on_diagonal = (p.a + alpha * (p.b + alpha * p.c)) * kNsScale;
+            t.on_diagonal = (p.a + alpha * (p.b + alpha * p.c)) * kGramScale;
         }
     } else {
         t.rows = m.rows;

@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1) muon_small_kernel(const __grid_co
     ptx::cluster_sync();
     double sum = 0.0;
     for (uint32_t i = 0; i < blocks; ++i) sum += norms[i];
-    const float scale = (float)((double)kNsScale / (sqrt(sum) + (double)p.sc.eps));
+    const float scale = (float)((double)kXScale / (sqrt(sum) + (double)p.sc.eps));
 
     // ---- X = U / (|U| + eps) in two f16 parts, in the place of U: all reads, then all writes
     {
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1) muon_small_kernel(const __grid_co
     const uint32_t n = (s + 15) & ~15u;        // rows of X the products take
     const bool active = (warp & 3) * 32 < n;   // this warp's rows
     const auto unit = [&](int q) { return (2 * q + half) * 16; };   // its q-th 16 columns
-    constexpr float inv = 1.0f / kNsScale;
+    constexpr float inv = 1.0f / kGramScale;
     uint32_t waits = 0;
     // Shared memory written by this block's threads is ready for the products.
     const auto ready = [&]() {
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1) muon_small_kernel(const __grid_co
         for (int q = 0; q < 4; ++q)
             if (active && unit(q) < n) {
 #pragma unroll
-                for (uint32_t e = 0; e < 16; ++e) w[16 * q + e] = w[16 * q + e] * inv - (unit(q) + e == r ? alpha * kNsScale : 0.f);
+                for (uint32_t e = 0; e < 16; ++e) w[16 * q + e] = w[16 * q + e] * (kGramScale / (kXScale * kXScale)) - (unit(q) + e == r ? alpha * kGramScale : 0.f);
                 put_gram(q);
             }
 
@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1) muon_small_kernel(const __grid_co
                 tc::tmem_load16(v, tmem + kGramTmem + lanes + unit(q));
 #pragma unroll
                 for (uint32_t e = 0; e < 16; ++e)
-                    w[16 * q + e] = p.sc.c * inv * v[e] + linear * w[16 * q + e] + (unit(q) + e == r ? constant * kNsScale : 0.f);
+                    w[16 * q + e] = p.sc.c * inv * v[e] + linear * w[16 * q + e] + (unit(q) + e == r ? constant * kGramScale : 0.f);
                 put_gram(q);
             }
 
@@ -363,8 +363,8 @@ __global__ void __launch_bounds__(kThreads, 1) muon_small_kernel(const __grid_co
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
                     tc::st_shared(f32_piece(x, r, (c >> 2) + q, quads),
-                                  as_u4(v[4 * q] * (inv * inv), v[4 * q + 1] * (inv * inv), v[4 * q + 2] * (inv * inv),
-                                        v[4 * q + 3] * (inv * inv)));
+                                  as_u4(v[4 * q] * (inv / kXScale), v[4 * q + 1] * (inv / kXScale),
+                                        v[4 * q + 2] * (inv / kXScale), v[4 * q + 3] * (inv / kXScale)));
             } else {
                 uint4 h[2], lo[2];
 #pragma unroll

@@ -22,7 +22,8 @@ SOURCES = ["zero1_host.cu", "zero1_kernels.cu", "zero1_noalloc.cu", "zero1_allre
            "zero1_muon.cu", "zero1_muon_kernels.cu", "zero1_muon_small.cu",
            "zero1_layernorm.cu"]
 HEADERS = [os.path.join(CSRC, "zero1_internal.h"), os.path.join(CSRC, "zero1_ptx.cuh"), os.path.join(CSRC, "zero1_policy.h"),
-           os.path.join(CSRC, "zero1_muon.h"), os.path.join(CSRC, "zero1_muon_device.cuh"), os.path.join(CSRC, "zero1_tc.cuh"),
+           os.path.join(CSRC, "zero1_muon.h"), os.path.join(CSRC, "zero1_muon_tiles.h"),
+           os.path.join(CSRC, "zero1_muon_device.cuh"), os.path.join(CSRC, "zero1_tc.cuh"),
            os.path.join(CSRC, "zero1_launch.h"),
            os.path.join(INCLUDE, "zero1.h")]
 

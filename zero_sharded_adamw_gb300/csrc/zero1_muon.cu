@@ -64,7 +64,7 @@ bool muon_live(zero1_muon_ctx *h)
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 uint64_t round_up(uint64_t x, uint64_t a) { return (x + a - 1) / a * a; }
-uint64_t blocks(uint64_t n, uint64_t tile) { return (n + tile - 1) / tile; }
+uint64_t blocks(uint64_t n, uint64_t tile) { return zero1::tile_blocks(n, tile); }
 bool finite_nonneg(double v) { return std::isfinite(v) && v >= 0.0; }
 
 // Make the handle's device current for the duration of a call.
@@ -176,52 +176,6 @@ bool encode(EncodeFn fn, CUtensorMap *map, void *base, uint64_t rows, uint64_t c
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Tiles of one product: of a Gram-sized matrix from its diagonal blocks on,
-// and of X.
-struct Tiles {
-    uint64_t gram, full;
-};
-
-Tiles tiles_of(const MuonMat &m, uint32_t tile)
-{
-    const uint64_t rb = blocks(m.s, zero1::kNsRows), cb = blocks(m.s, tile), per_row = zero1::kNsRows / tile;
-    return Tiles{rb * cb - per_row * (rb * (rb - 1) / 2), blocks(m.rows, zero1::kNsRows) * blocks(m.cols, tile)};
-}
-
-// Columns of a tile: whichever of 256 and 128 ends one iteration sooner by
-// measured times.  A step of 64 of K takes 0.85 us for a tile of 256 and
-// 0.57 us for one of 128 (two wide products where the other has three), and
-// each of the three phases costs 7 or 5 us beside its steps.  An iteration ends no sooner
-// than its longest chain of products and than all steps over all block pairs.
-uint32_t tile_columns(const std::vector<MuonMat> &plan, const std::vector<uint32_t> &large, int sms)
-{
-    const double pairs = std::max(1, sms / 2);
-    const auto time = [&](uint32_t tile, double step, double each) {
-        double all = 0.0, chain = 0.0;
-        for (const uint32_t i : large) {
-            const MuonMat &m = plan[i];
-            const Tiles t = tiles_of(m, tile);
-            const double gram = (double)blocks(std::max(m.rows, m.cols), 64), rest = (double)blocks(m.s, 64);
-            all += t.gram * (gram + rest) + t.full * rest;
-            chain = std::max(chain, (gram + 2 * rest) * step + 3 * each);
-        }
-        return std::max(all * step / pairs, chain);
-    };
-    return time(128, 0.57, 5.0) <= time(256, 0.85, 7.0) ? 128 : 256;
-}
-
-// log2 of the blocks that step a small matrix in one launch, or -1.  One
-// launch of one to eight blocks takes about 5 us an iteration where the tiled
-// products take 14 and more; it holds no side above 128, nor one above 1,536.
-int small_blocks(const MuonMat &m)
-{
-    if (m.s > 128) return -1;
-    const uint32_t l = std::max(m.rows, m.cols);
-    for (int i = 0; i < zero1::kSmallSizes; ++i)
-        if (l <= (zero1::small_width(1 << i) << i)) return i;
-    return -1;
-}
-
 // SMs of the current device; where there is none, creation fails later on.
 int device_sms()
 {
@@ -292,7 +246,7 @@ int create(uint64_t n, int world, const zero1_matrix *mats, uint64_t count, cons
         m.scale = (float)(hp->update_scale *
                           std::sqrt(hp->scale_rule == ZERO1_MUON_SCALE_RMS ? std::max(r, k) : std::max(1.0, r / k)));
         entries += size;
-        const int blocks_log = small_blocks(m);
+        const int blocks_log = zero1::small_blocks(m.s, std::max(a.rows, a.cols));
         if (blocks_log >= 0) {
             small[blocks_log].push_back((uint32_t)i);
             continue;
@@ -313,10 +267,11 @@ int create(uint64_t n, int world, const zero1_matrix *mats, uint64_t count, cons
         m.chunks = (uint32_t)c;
     }
     const int sms_hint = device_sms();
-    const uint32_t tile = tile_columns(plan, large, sms_hint);
+    const auto sides = [&](size_t k, uint32_t &rows, uint32_t &cols) { rows = plan[large[k]].rows, cols = plan[large[k]].cols; };
+    const uint32_t tile = zero1::tile_columns(large.size(), sides, sms_hint);
     for (const uint32_t i : large) {
         MuonMat &m = plan[i];
-        const Tiles t = tiles_of(m, tile);
+        const zero1::Tiles t = zero1::tiles_of(m.rows, m.cols, tile);
         tiles += 2 * t.gram + t.full;
         // tickets and per-matrix counts are 32-bit, over all steps
         if (tiles * 32 * zero1::kNsParts > 0x7FFFFFFFull)

@@ -7,12 +7,10 @@
 #include <cuda_runtime.h>
 
 #include "zero1.h"
+#include "zero1_muon_tiles.h"
 
 namespace zero1 {
 
-// Output tile of the matrix products: 256 rows, 128 in each block of a pair,
-// by 256 or 128 columns (one choice for a handle, MuonDev::tile).
-constexpr uint32_t kNsRows = 256;
 constexpr int kNsParts = 32;           // arrivals a finished tile makes: one by each warp that writes it
 constexpr int kNsTileK = 64;           // K of one pipeline stage
 constexpr uint32_t kMaxSide = 1u << 22;
@@ -66,15 +64,10 @@ struct MuonDev {
 
 // Small matrices, whose whole step is one launch (zero1_muon_small.cu): lists
 // of them by the number of blocks that share one, 1, 2, 4 or 8.
-constexpr int kSmallSizes = 4;
 struct MuonSmall {
     const uint32_t *list;      // device memory: indices into MuonDev::mats
     uint32_t first[kSmallSizes], count[kSmallSizes];
 };
-// Columns of the larger side a block holds, at most: X, two f16 parts of 128
-// rows, beside the Gram matrix (64 KB) and, in a cluster, the parts of its
-// sum (64 KB).
-constexpr uint32_t small_width(int blocks) { return blocks == 1 ? 256 : 192; }
 constexpr int small_smem(int blocks) { return (int)(2 * 128 * 2 * small_width(blocks)) + (blocks == 1 ? 1 : 2) * 65536 + 1024; }
 
 // Blocks of a cluster that take tensor memory have their SMs to themselves:

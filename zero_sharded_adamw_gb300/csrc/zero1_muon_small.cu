@@ -13,9 +13,10 @@
 //
 // Bound by latency: three dependent products with an exchange between tensor
 // memory, registers and shared memory after each.  What it saves is the
-// trip of every product through L2 and a counter (about 4.5 us each), and
-// the separate kernels for momentum, norm, split and update.  A 64 x 64 step
-// at W = 4 takes 29 us (by the tiled kernels 97), alone 27 us.
+// trip of every product through L2 and a counter (a tiled product takes 13 us
+// and more from one to the next, one here 1.7), and the separate kernels for
+// momentum, norm, split and update.  A 64 x 64 step at W = 4 takes 29 us (by
+// the tiled kernels 97), alone 27 us.
 #include "zero1_internal.h"
 #include "zero1_muon.h"
 #include "zero1_muon_device.cuh"

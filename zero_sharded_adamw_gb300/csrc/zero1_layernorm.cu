@@ -496,10 +496,12 @@ cudaError_t fwd_pick(const FwdParams<T> &p, cudaStream_t st)
     if (n <= 96) return fwd<T, V, 32, 3, 256>(p, st);
     if (n <= 128) return fwd<T, V, 32, 4, 256>(p, st);
     if (n <= 256) return fwd<T, V, 32, 8, 256>(p, st);
-    if constexpr (V == 1)
+    if constexpr (V == 1) {
         if (n <= 1024) return fwd<T, V, 32, 32, 256>(p, st);
-    if (n <= 512) return fwd<T, V, 128, 4, 256>(p, st);
-    if (n <= 1024) return fwd<T, V, 256, 4, 256>(p, st);
+    } else {
+        if (n <= 512) return fwd<T, V, 128, 4, 256>(p, st);
+        if (n <= 1024) return fwd<T, V, 256, 4, 256>(p, st);
+    }
     if (n <= 2048) return fwd<T, V, 256, 8, 256>(p, st);
     if constexpr (V == 1)
         if (n <= 8192) return fwd<T, V, 512, 16, 512>(p, st);

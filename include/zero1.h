@@ -555,10 +555,13 @@ typedef struct zero1_matrix {
  *     iterate's singular values below 2, as (3.4445, -4.7750, 2.0315) does:
  *     entries are held in scaled f16 parts, and beyond that range results are
  *     infinite or NaN.
+ *     There is no cubic iteration (ns_c = 0) and no coefficients that differ
+ *     by iteration: the products form A (A + (ns_b / ns_c) I) once for all.
  *   inject_wait_timeout: failure testing only.  1 = the tiled iteration (a
- *     side above 128) is given no tiles, so that its waits run out after
- *     their 1 s limit; the call returns, its results mean nothing, and
- *     zero1_muon_status then reports ZERO1_ECUDA.
+ *     smaller side above 128, or a larger one above 1,536) is given no tiles,
+ *     so that its waits run out after their 1 s limit; the call returns, its
+ *     results mean nothing, and zero1_muon_status then reports ZERO1_ECUDA.
+ *     Matrices stepped in one launch are not affected.
  *   reserved: 0.
  *   size: sizeof(zero1_muon_hparams) (lets the struct grow). */
 typedef struct zero1_muon_hparams {
@@ -588,6 +591,8 @@ typedef struct zero1_muon_ctx *zero1_muon_handle;
  * s x s Gram matrix and 1 KB for each of its rows.  `mats` is copied.
  * Matrices may be given in any order; no two may share an entry, and two
  * whose extents interleave must have one ld.  Sides are 1 to 2^22.
+ * A handle's calls share its workspace: they have to follow one another, on
+ * one stream or ordered by events.
  * Errors: ZERO1_EINVAL (before any device call but that for the number of
  * SMs), ZERO1_ENODEV, ZERO1_ENOMEM, ZERO1_ECUDA.  On error *out is NULL. */
 int zero1_muon_create(uint64_t n, int world, const zero1_matrix *mats, uint64_t count,
@@ -613,18 +618,18 @@ int zero1_muon_destroy(zero1_muon_handle h);
  * All buffers 16-byte aligned; entries outside the matrices are neither read
  * nor written.  The products run as three f16 products with fp32
  * accumulators (each factor in a high and a low part).  By the matrix's norm
- * the iterated X is about as far from 64 bits as the iteration in fp32 (0.35 to
- * 2.6 times as far in the matrices measured); entries of U below 7.6e-6 |U| enter it
- * with an absolute error of up to 1.8e-12 |U|, where fp32 would keep their
- * leading bits.
+ * the iterated X is about as far from 64 bits as the iteration in fp32 (0.35
+ * to 2.6 times as far in the matrices measured); entries of U below
+ * 7.6e-6 |U| enter it with an absolute error of up to 1.8e-12 |U|, where fp32
+ * would keep their leading bits.
  * A matrix of zeros is moved by its decay alone.  A gradient with an
  * infinity or a NaN makes its own matrix NaN, and no other.  Deterministic:
  * the same inputs give the same bits.
- * On a stream of an SM partition: a small matrix (zero1_muon_create) of a
- * larger side above 256 runs as a cluster of 2, 4 (above 384) or 8 (above
- * 768) blocks that needs as many SMs of one processing cluster, and the rest
- * of a partition may have too few of them; the call is then refused
- * (ZERO1_EINVAL) before anything runs.
+ * On a stream of an SM partition (the orthogonalisation too): a small matrix
+ * (zero1_muon_create) of a larger side above 256 runs as a cluster of 2, 4
+ * (above 384) or 8 (above 768) blocks that needs as many SMs of one processing
+ * cluster, and the second group may have too few of them; the call is then
+ * refused (ZERO1_EINVAL) before anything runs.
  * Errors: ZERO1_EINVAL, ZERO1_EALIGN, ZERO1_ECUDA. */
 int zero1_muon_step(zero1_muon_handle h, const void *const *grad_ptrs, void *const *param_ptrs, float *master,
                     float *momentum, void *stream);
@@ -638,7 +643,10 @@ int zero1_muon_step(zero1_muon_handle h, const void *const *grad_ptrs, void *con
 int zero1_muon_orthogonalize(zero1_muon_handle h, const void *in, int in_dtype, void *out, int out_dtype,
                              void *stream);
 
-/* The learning rate of later steps.  Errors: ZERO1_EINVAL. */
+/* The learning rate of later zero1_muon_step calls.  It is an argument of
+ * their launches: a step captured in a CUDA graph keeps the rate it was
+ * captured with, so a schedule captures again (or updates the graph).
+ * Errors: ZERO1_EINVAL. */
 int zero1_muon_set_lr(zero1_muon_handle h, double lr);
 
 /* Wait for `stream` and report whether a kernel wait of this handle ever gave
@@ -659,15 +667,16 @@ int zero1_muon_layout(zero1_muon_handle h, uint64_t *entries, uint64_t *device_b
  * beta are of one type (ZERO1_DTYPE_BF16 or ZERO1_DTYPE_F32); rows start
  * ldx, ldy, lddy, lddx entries apart (>= cols, and rows times the stride at
  * most 2^50).  Buffers need the alignment of their elements only (16-byte
- * aligned rows of whole 16-byte pieces are faster).  Sums and statistics are
- * fp32.  Sizes: rows < 2^31, cols 1 to 2^24.  Asynchronous on `stream`;
+ * aligned rows of whole 16-byte pieces are faster, in all of x, y, gamma and
+ * beta, or dy, x, dx and gamma, together).  Sums and statistics are fp32,
+ * long ones in parts (of 128 or 512 terms of a thread).  Sizes: rows < 2^31, cols 1 to 2^24.  Asynchronous on `stream`;
  * allocates nothing.
  *
  * Forward: with mean and var of each row (var over cols, not cols - 1) and
  * rstd = 1/sqrt(var + eps),
  *     y = (x - mean) * rstd * gamma + beta.
  *   beta may be NULL (no bias); mean and rstd (fp32, one a row) are written
- *   for the backward pass; y may be x (with ldy == ldx).  rows = 0 does nothing.
+ *   for the backward pass and may not be NULL; y may be x (with ldy == ldx).  rows = 0 does nothing.
  * Errors: ZERO1_EINVAL, ZERO1_EALIGN, ZERO1_ECUDA. */
 int zero1_layernorm_forward(uint64_t rows, uint64_t cols, int dtype, const void *x, uint64_t ldx,
                             const void *gamma, const void *beta, double eps, void *y, uint64_t ldy, float *mean,

@@ -17,9 +17,13 @@
 // order (no atomics: the same inputs give the same bits).
 //
 // Measured, bf16: forward 16,384 x 768 in 12 us, 65,536 x 4,096 in 184 us
-// (5.8 TB/s); backward 65,536 x 4,096 in 281 us (5.7 TB/s, issue slots 66%
-// busy) and 5 us for the column sums, 16,384 x 768 in 20 and 4 us; one row of
-// 768 in 5 us, all latency.
+// (5.8 TB/s; 188 back to back); backward 65,536 x 4,096 in 279 us (5.8 TB/s,
+// issue slots 57% busy) and 5 us for the column sums, 16,384 x 768 in 21 and
+// 4 us; one row of 768 in 5 us, all latency.  Rows of single entries run at
+// half the rate: 32,768 x 1,000 at a stride of 1,001 backward in 58 us (floor
+// 29).  Past registers, two to five times the floor: 8,192 x 12,288 fp32
+// forward in 211 us (119), backward in 460 (178); 8,192 x 18,432 bf16 in 270
+// (89) and 616 (134).
 #include <cstdarg>
 #include <cstdio>
 

@@ -19,11 +19,12 @@
 // others in size come out 1e-3 of themselves off (plain fp32: 5e-7).
 //
 // Bound by the tensor cores where tiles are many: five steps of 4096 x 4096
-// take 2.41 ms, 1.76 PFLOP/s over the three products (tensor pipe 79%
-// active, DRAM 10%), of 4096 x 16384 7.17 ms, 1.9 PFLOP/s; all 48 matrices of
-// the GPT-2-small blocks 2.19 ms, 1.6 PFLOP/s.  Bound by latency where they
-// are few: three 768 x 768 take 0.23 ms, 15.5 us for each of fifteen
-// products one after another, of which 8 us are products.
+// take 2.41 to 2.49 ms, 1.74 PFLOP/s over the three products (tensor pipe 78%
+// active, DRAM 10%), of 4096 x 16384 7.1 to 7.3 ms alone, 1.9 PFLOP/s, and
+// 7.9 ms back to back, where the power limit holds the SMs at 1.4 to 1.6 GHz;
+// all 48 matrices of the GPT-2-small blocks 2.2 to 2.3 ms, 1.6 PFLOP/s.  Bound
+// by latency where they are few: three 768 x 768 take 0.23 ms, 15.5 us for
+// each of fifteen products one after another, of which 8 us are products.
 #include "zero1_internal.h"
 #include "zero1_launch.h"
 #include "zero1_muon.h"
@@ -468,6 +469,9 @@ __device__ __forceinline__ void turn_out(uint32_t mem, unsigned char *dst, uint6
 // rows in 2 KB of shared memory so that a store covers 8 rows of 64 bytes;
 // straight from the registers, a row a lane, writing took 4.5 us a tile, and
 // through TMA, 64 columns at a time in the 32 KB that the stages leave, 7.4.
+// Eighteen warps put five on one of an SM's four schedulers, which leaves a
+// thread 96 registers: a wide tile's 64 results beside the 16 just read spill
+// 72 bytes of stores and 108 of loads.
 template <int TN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNsThreads, 1)
     muon_iterate_kernel(const __grid_constant__ NsParams p)

@@ -59,7 +59,9 @@ inline Tiles tiles_of(uint32_t rows, uint32_t cols, uint32_t tile)
 // Some of those times, us an iteration at 128 | 256 columns: three 768 x 768
 // 46 | 63, twelve 73 | 77, sixteen 92 | 87; 2048 x 2048 109 | 113, 2304 x 2304
 // 187 | 152, 4096 x 16384 2267 | 1549; 40 of 300 x 517 64 | 70, 120 181 | 163;
-// one GPT-2-small block 80 | 97, two 117 | 114, all twelve 682 | 462.
+// one GPT-2-small block 80 | 97, two 117 | 114, all twelve 682 | 462.  (A trace
+// of three 768 x 768 at 128 columns gives each of three products 8 us for its
+// 12 steps and 7.5 us to hand over; the fit spreads the same time otherwise.)
 template <typename F>
 double iteration_us(size_t count, F sides, uint32_t tile, double pairs)
 {

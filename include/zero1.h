@@ -622,7 +622,7 @@ int zero1_muon_destroy(zero1_muon_handle h);
  * nor written.  The products run as three f16 products with fp32
  * accumulators (each factor in a high and a low part).  By the matrix's norm
  * the iterated X is about as far from 64 bits as the iteration in fp32 (0.28
- * to 2.6 times as far in some 130 matrices of random, decaying, low-rank and
+ * to 2.6 times as far in some 120 matrices of random, decaying, low-rank and
  * sparse spectra); entries of U below 7.6e-6 |U| enter it with an absolute
  * error of up to 1.8e-12 |U|, where fp32 would keep their leading bits.
  * A matrix of zeros is moved by its decay alone.  A gradient with an

@@ -15,9 +15,10 @@
 // matrix's norm, the result is off by 1.7e-6 at 768 x 768 (the iteration in
 // plain fp32 by 2.5e-6), 4.4e-6 (7.2e-6) at 4096 x 16384, 2.9e-6 (2.5e-6) at
 // 1031 x 257 and 1.4e-6 (1.0e-6) at 64 x 64; 0.28 to 2.6 times plain fp32's
-// error over some 130 matrices, most where a side is at most 130 and few
-// directions are strong or few entries not zero.  Half the rows of 768 x 2304 1e-6 of the
-// others in size come out 1e-3 of themselves off (plain fp32: 5e-7).
+// error over some 120 matrices, most where a side is at most 130 and few
+// directions are strong or few entries not zero.  Half the rows of 768 x 2304,
+// 1e-6 of the others in size, come out 1e-3 of themselves off (plain fp32:
+// 5e-7).
 //
 // Bound by the tensor cores where tiles are many: five steps of 4096 x 4096
 // take 2.41 to 2.49 ms, 1.74 PFLOP/s over the three products (tensor pipe 78%

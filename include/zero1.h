@@ -704,6 +704,108 @@ int zero1_layernorm_backward(uint64_t rows, uint64_t cols, int dtype, const void
                              const float *rstd, void *dx, uint64_t lddx, void *dgamma, void *dbeta,
                              int grad_dtype, void *workspace, uint64_t workspace_bytes, void *stream);
 
+/* ------------------------------------------------- AdamW over many tensors
+ *
+ * The AdamW step for a model whose parameters are a list of tensors rather
+ * than one flat buffer over W ranks: one call steps them all, in two launches
+ * (the gradients' norm and the update; one without clipping), whatever their
+ * number up to 1,900 (and two more for each 1,900 beyond).
+ *
+ * Moments are fp32 or 8 bits.  The caller owns all state, in buffers that
+ * hold the tensors one after another, each from a multiple of 256 entries on
+ * (zero1_adamw_layout): the fp32 master (bf16 parameters only: fp32 ones are
+ * their own), m and v, and for 8 bits two scales for each block of 256
+ * entries.  These and the step count are a checkpoint.  Entries between two
+ * tensors are neither read nor written.
+ *
+ * In 8 bits, with M and R the largest |m| and sqrt(v) of a block and
+ * f(k, b) = (1 + (k mod 2^b)/2^b) 2^(k div 2^b), an entry's codes stand for
+ *     m = +-(f(k, 3) - 1) M/61439  (k in the low 7 bits, the sign above it),
+ *     sqrt(v) = (f(k, 4) - 1) R/63487,
+ * and its block's scales are M/61439 and R/63487 (0 for a block whose largest
+ * value is below 2^-100: it is held as zeros).  Codes are rounded up or down
+ * at random with the exact value as their mean, by a hash of `seed`, the step
+ * and the entry's place: the same inputs give the same bits.  A block with an
+ * infinity or a NaN among its new moments has a NaN scale and stands for NaN;
+ * other blocks are not touched by it (clipping, whose norm is then infinite
+ * or NaN, turns the whole list NaN or holds it, as zero1_step does).
+ *   state_bits: 8 or 32;
+ *   param_dtype, grad_dtype: ZERO1_DTYPE_BF16 or ZERO1_DTYPE_F32;
+ *   decay_before_update: as zero1_options;
+ *   reserved: 0;  size: sizeof(zero1_adamw_options). */
+typedef struct zero1_adamw_options {
+    uint32_t size;
+    int32_t state_bits;
+    int32_t param_dtype;
+    int32_t grad_dtype;
+    int32_t decay_before_update;
+    int32_t reserved;
+    uint64_t seed;
+} zero1_adamw_options;
+
+typedef struct zero1_adamw_ctx *zero1_adamw_handle;
+
+/* Plan the step of `count` tensors (1 to 65,536) of sizes[i] entries each
+ * (empty ones are allowed; 2^40 in all), and allocate its tables on the
+ * current device with cudaMalloc: 4 bytes for each 256 entries, 32 a tensor
+ * and the bias corrections (as zero1_options.capturable: beta2 = 0.999999 is
+ * refused).  decays[i] = 0 spares tensor i the weight decay (vectors,
+ * usually); NULL: all decay.  opts may be NULL: fp32 moments, bf16 parameters
+ * and gradients.  hp as zero1_create; max_norm <= 0: no norm is formed.
+ * The step count and the learning rate live in device memory, so that a step
+ * captured in a CUDA graph replays as the next step.  A handle's calls follow
+ * one another, on one stream or ordered by events.
+ * Errors: ZERO1_EINVAL (before any device call), ZERO1_ENODEV, ZERO1_ENOMEM,
+ * ZERO1_ECUDA.  On error *out is NULL. */
+int zero1_adamw_create(const uint64_t *sizes, const uint8_t *decays, uint64_t count, const zero1_hparams *hp,
+                       const zero1_adamw_options *opts, zero1_adamw_handle *out);
+
+/* Free the handle and its tables after synchronizing the device.  NULL is
+ * accepted and ignored.  Returns ZERO1_OK, ZERO1_EINVAL or ZERO1_ECUDA. */
+int zero1_adamw_destroy(zero1_adamw_handle h);
+
+/* One step (t -> t+1) of all tensors, asynchronous and allocation-free:
+ *     c = min(1, max_norm / |all gradients|)   (1 without clipping)
+ *     m = beta1 m + (1-beta1) (c g),   v = beta2 v + ((1-beta2) (c g)) (c g)
+ *     p = p - (lr sqrt(1-beta2^t)/(1-beta1^t)) (m / (sqrt(v) + eps))
+ *     p = p (1 - lr weight_decay)              (tensors that decay)
+ * in fp32, every operation rounded by itself, on the master (or the fp32
+ * parameters); bf16 parameters receive its rounding.
+ *   grad_ptrs, param_ptrs: host arrays of one device pointer a tensor (NULL
+ *     for empty ones), aligned to their elements (16-byte aligned tensors
+ *     are faster); the pointers are copied into the launches.  No parameter
+ *     tensor may overlap another or a gradient (ZERO1_EINVAL).
+ *   master, m, v, scales: the state, 16-byte aligned; m and v fp32 or bytes;
+ *     master NULL with fp32 parameters, scales NULL with fp32 moments.
+ * Errors: ZERO1_EINVAL, ZERO1_EALIGN, ZERO1_ENOMEM, ZERO1_ECUDA. */
+int zero1_adamw_step(zero1_adamw_handle h, const void *const *grad_ptrs, void *const *param_ptrs, float *master, void *m,
+                     void *v, float *scales, void *stream);
+
+/* The fp32 values that 8-bit moments stand for (a checkpoint that other
+ * programs read, say): m_out and v_out laid out as m and v; either may be
+ * NULL.  Asynchronous.  Errors: ZERO1_EINVAL (a handle of 32 bits),
+ * ZERO1_EALIGN, ZERO1_ECUDA. */
+int zero1_adamw_moments(zero1_adamw_handle h, const void *m, const void *v, const float *scales, float *m_out,
+                        float *v_out, void *stream);
+
+/* The steps taken (of a checkpoint) and the learning rate of later steps, set
+ * in stream order: replays of a captured step that come after see them.
+ * Errors: ZERO1_EINVAL, ZERO1_ECUDA. */
+int zero1_adamw_set_steps(zero1_adamw_handle h, uint64_t t, void *stream);
+int zero1_adamw_set_lr(zero1_adamw_handle h, double lr, void *stream);
+
+/* The steps taken; the gradients' norm and clip coefficient of the latest step
+ * of a handle that clips (0 before the first).  Both wait for `stream`; either
+ * output of the second may be NULL.  Errors: ZERO1_EINVAL, ZERO1_ECUDA. */
+int zero1_adamw_get_steps(zero1_adamw_handle h, uint64_t *t, void *stream);
+int zero1_adamw_get_grad_norm(zero1_adamw_handle h, double *norm, float *clip_coef, void *stream);
+
+/* Host-only: entries of each state buffer (a multiple of 256; the scales are
+ * entries/128 floats), where each tensor starts in them (count numbers), and
+ * the bytes of device memory the handle holds.  Any output may be NULL.
+ * Errors: ZERO1_EINVAL. */
+int zero1_adamw_layout(zero1_adamw_handle h, uint64_t *entries, uint64_t *starts, uint64_t *device_bytes);
+
 /* Message for the last error on this thread ("" if none). */
 const char *zero1_last_error(void);
 

@@ -28,6 +28,9 @@ __all__ = [
     "MuonHparams", "Muon", "zero1_muon_create", "zero1_muon_destroy", "zero1_muon_step", "zero1_muon_orthogonalize",
     "zero1_muon_set_lr", "zero1_muon_status", "zero1_muon_layout",
     "zero1_layernorm_forward", "zero1_layernorm_backward", "zero1_layernorm_workspace",
+    "AdamWOptions", "AdamW", "zero1_adamw_create", "zero1_adamw_destroy", "zero1_adamw_step", "zero1_adamw_moments",
+    "zero1_adamw_set_steps", "zero1_adamw_set_lr", "zero1_adamw_get_steps", "zero1_adamw_get_grad_norm",
+    "zero1_adamw_layout",
     "library_path", "EXPORTED_SYMBOLS",
 ]
 
@@ -82,6 +85,15 @@ _SIGS = {
     "zero1_layernorm_workspace": (_I32, [_U64, _U64, _P]),
     "zero1_layernorm_backward": (_I32, [_U64, _U64, _I32, _P, _U64, _P, _U64, _P, _P, _P, _P, _U64, _P, _P, _I32, _P,
                                         _U64, _P]),
+    "zero1_adamw_create": (_I32, [_P, _P, _U64, _P, _P, _P]),
+    "zero1_adamw_destroy": (_I32, [_P]),
+    "zero1_adamw_step": (_I32, [_P, _P, _P, _P, _P, _P, _P, _P]),
+    "zero1_adamw_moments": (_I32, [_P, _P, _P, _P, _P, _P, _P]),
+    "zero1_adamw_set_steps": (_I32, [_P, _U64, _P]),
+    "zero1_adamw_set_lr": (_I32, [_P, _F64, _P]),
+    "zero1_adamw_get_steps": (_I32, [_P, _P, _P]),
+    "zero1_adamw_get_grad_norm": (_I32, [_P, _P, _P, _P]),
+    "zero1_adamw_layout": (_I32, [_P, _P, _P, _P]),
     "zero1_last_error": (C.c_char_p, []),
 }
 EXPORTED_SYMBOLS = tuple(_SIGS)
@@ -215,7 +227,7 @@ class PtrTable:
 
 # Element kinds a C entry point expects behind a pointer: torch dtype name
 # and element size in bytes.
-_KINDS = {"bf16": ("torch.bfloat16", 2), "f32": ("torch.float32", 4)}
+_KINDS = {"bf16": ("torch.bfloat16", 2), "f32": ("torch.float32", 4), "u8": ("torch.uint8", 1)}
 _DTYPE_NAMES: dict = {}    # torch dtype -> its name (naming one takes longer than the other checks together)
 _TORCH_DTYPES: dict = {}   # element kind -> torch dtype, as they are met
 
@@ -745,6 +757,183 @@ def zero1_layernorm_backward(rows: int, cols: int, dtype: int, dy, lddy: int, x,
         _take_rows(dx, rows, cols, lddx, kind, "dx"), lddx, _take_vector(dgamma, cols, grad_kind, "dgamma"),
         _take_vector(dbeta, cols, grad_kind, "dbeta"), grad_dtype, workspace.data_ptr(),
         workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+# --------------------------------------------------------- AdamW over many tensors
+
+class _CAdamWOptions(C.Structure):
+    _fields_ = [("size", C.c_uint32), ("state_bits", C.c_int32), ("param_dtype", C.c_int32), ("grad_dtype", C.c_int32),
+                ("decay_before_update", C.c_int32), ("reserved", C.c_int32), ("seed", C.c_uint64)]
+
+
+@dataclass
+class AdamWOptions:
+    """Moments in 8 or 32 bits, the tensors' element types, torch's decay
+    order, and the seed of the 8-bit codes' random rounding."""
+    state_bits: int = 32
+    param_dtype: int = DTYPE_BF16
+    grad_dtype: int = DTYPE_BF16
+    decay_before_update: bool = False
+    seed: int = 0
+
+    def _c(self) -> _CAdamWOptions:
+        if not 0 <= self.seed < 1 << 64:
+            raise Zero1ArgumentError(f"seed: {self.seed} is not an unsigned 64-bit number")
+        return _CAdamWOptions(C.sizeof(_CAdamWOptions), self.state_bits, self.param_dtype, self.grad_dtype,
+                              int(self.decay_before_update), 0, self.seed)
+
+
+# (sizes, options, entries of the state) of every list handle this binding created.
+_ADAMW_HANDLES: dict[int, tuple[tuple[int, ...], AdamWOptions, int]] = {}
+
+
+def zero1_adamw_create(sizes, hp: Hparams | None = None, opts: AdamWOptions | None = None, decays=None) -> int:
+    """Create a handle for tensors of these many entries; `decays` holds a
+    truth value a tensor (None: all decay)."""
+    sizes, opts = tuple(int(n) for n in sizes), opts or AdamWOptions()
+    if any(not 0 <= n < 1 << 63 for n in sizes):
+        raise Zero1ArgumentError("sizes: a size is out of range")
+    if decays is not None:
+        decays = [1 if d else 0 for d in decays]
+        if len(decays) != len(sizes):
+            raise Zero1ArgumentError(f"decays: {len(decays)} values given for {len(sizes)} tensors")
+        decays = (C.c_uint8 * max(1, len(sizes)))(*decays)
+    h = C.c_void_p()
+    c, o = (hp or Hparams())._c(), opts._c()
+    _check(_load().zero1_adamw_create((C.c_uint64 * max(1, len(sizes)))(*sizes), decays, len(sizes), C.byref(c),
+                                      C.byref(o), C.byref(h)))
+    _ADAMW_HANDLES[h.value] = (sizes, opts, sum(-(-n // 256) * 256 for n in sizes))
+    return h.value
+
+
+def zero1_adamw_destroy(h: int | None) -> None:
+    _check(_load().zero1_adamw_destroy(h))
+    _ADAMW_HANDLES.pop(h, None)
+
+
+def _list_ptrs(xs, sizes, kind: str, what: str) -> C.Array:
+    """The host array of one pointer a tensor, each checked to hold its
+    tensor's entries."""
+    if sizes is None:
+        return xs.array if isinstance(xs, PtrTable) else (C.c_void_p * len(xs))(*[_addr(x) for x in xs])
+    if len(xs) != len(sizes):
+        raise Zero1ArgumentError(f"{what}: {len(xs)} pointers given, the call reads {len(sizes)}")
+    if not isinstance(xs, PtrTable):
+        return (C.c_void_p * len(sizes))(*[_take(x, n, kind, what, i) if n else None
+                                           for i, (x, n) in enumerate(zip(xs, sizes))])
+    key = (sizes, kind)
+    if key not in xs._checked:
+        for i, (x, n) in enumerate(zip(xs.buffers, sizes)):
+            if n:
+                _check_buffer(x, n, kind, True, f"{what}[{i}]")
+        xs._checked.add(key)
+    return xs.array
+
+
+def _check_list_state(h, master, m, v, scales) -> tuple:
+    """Addresses of the state buffers, after their checks."""
+    _, opts, n = _ADAMW_HANDLES.get(h, (None, None, None))
+    if n is None:
+        return _addr(master), _addr(m), _addr(v), _addr(scales)
+    kind = "u8" if opts.state_bits == 8 else "f32"
+    return (_take(master, n, "f32", "master"), _take(m, n, kind, "m"), _take(v, n, kind, "v"),
+            _take(scales, n // 128, "f32", "scales"))
+
+
+def zero1_adamw_step(h: int, grad_ptrs, param_ptrs, master, m, v, scales=None, stream=None) -> None:
+    """One step of all tensors; the state buffers are the caller's."""
+    sizes, opts, _ = _ADAMW_HANDLES.get(h, (None, None, None))
+    grads = _list_ptrs(grad_ptrs, sizes, _KIND_OF.get(opts.grad_dtype) if opts else None, "grads")
+    params = _list_ptrs(param_ptrs, sizes, _KIND_OF.get(opts.param_dtype) if opts else None, "params")
+    _check(_load().zero1_adamw_step(h, grads, params, *_check_list_state(h, master, m, v, scales), _stream(stream)))
+
+
+def zero1_adamw_moments(h: int, m, v, scales, m_out=None, v_out=None, stream=None) -> None:
+    """The fp32 values that 8-bit moments stand for."""
+    n = _ADAMW_HANDLES.get(h, (None, None, None))[2]
+    _, m, v, scales = _check_list_state(h, None, m, v, scales)
+    outs = [_addr(x) if n is None else _take(x, n, "f32", what) for x, what in ((m_out, "m_out"), (v_out, "v_out"))]
+    _check(_load().zero1_adamw_moments(h, m, v, scales, *outs, _stream(stream)))
+
+
+def zero1_adamw_set_steps(h: int, t: int, stream=None) -> None:
+    _check(_load().zero1_adamw_set_steps(h, t, _stream(stream)))
+
+
+def zero1_adamw_set_lr(h: int, lr: float, stream=None) -> None:
+    _check(_load().zero1_adamw_set_lr(h, lr, _stream(stream)))
+
+
+def zero1_adamw_get_steps(h: int, stream=None) -> int:
+    t = C.c_uint64()
+    _check(_load().zero1_adamw_get_steps(h, C.byref(t), _stream(stream)))
+    return t.value
+
+
+def zero1_adamw_get_grad_norm(h: int, stream=None) -> tuple[float, float]:
+    norm, clip = C.c_double(), C.c_float()
+    _check(_load().zero1_adamw_get_grad_norm(h, C.byref(norm), C.byref(clip), _stream(stream)))
+    return norm.value, clip.value
+
+
+def zero1_adamw_layout(h: int) -> tuple[int, list[int], int]:
+    """(entries of each state buffer, where each tensor starts in them, device bytes of the handle)."""
+    count = len(_ADAMW_HANDLES[h][0]) if h in _ADAMW_HANDLES else 0
+    e, b, starts = C.c_uint64(), C.c_uint64(), (C.c_uint64 * max(1, count))()
+    _check(_load().zero1_adamw_layout(h, C.byref(e), starts if count else None, C.byref(b)))
+    return e.value, list(starts[:count]), b.value
+
+
+class AdamW:
+    """Owning wrapper around a list handle (closes on ``close()`` / context exit).
+
+    ``entries`` is the length of master, m and v, ``scale_entries`` that of the
+    8-bit moments' scales, and ``starts[i]`` where tensor i's state begins."""
+
+    def __init__(self, sizes, hp: Hparams | None = None, opts: AdamWOptions | None = None, decays=None):
+        self.handle = None
+        self.hp, self.opts = hp or Hparams(), opts or AdamWOptions()
+        self.handle = zero1_adamw_create(sizes, self.hp, self.opts, decays)
+        self.entries, self.starts, _ = zero1_adamw_layout(self.handle)
+        self.scale_entries = self.entries // 128 if self.opts.state_bits == 8 else 0
+
+    def step(self, grads, params, master, m, v, scales=None, stream=None) -> None:
+        zero1_adamw_step(self.handle, grads, params, master, m, v, scales, stream)
+
+    def moments(self, m, v, scales, m_out=None, v_out=None, stream=None) -> None:
+        zero1_adamw_moments(self.handle, m, v, scales, m_out, v_out, stream)
+
+    def set_steps(self, t: int, stream=None) -> None:
+        zero1_adamw_set_steps(self.handle, t, stream)
+
+    def steps(self, stream=None) -> int:
+        return zero1_adamw_get_steps(self.handle, stream)
+
+    def set_lr(self, lr: float, stream=None) -> None:
+        zero1_adamw_set_lr(self.handle, lr, stream)
+
+    def grad_norm(self, stream=None) -> tuple[float, float]:
+        return zero1_adamw_get_grad_norm(self.handle, stream)
+
+    def layout(self) -> tuple[int, list[int], int]:
+        return zero1_adamw_layout(self.handle)
+
+    def close(self) -> None:
+        if self.handle is not None:
+            zero1_adamw_destroy(self.handle)
+            self.handle = None
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
 
 
 class _CSmPartition(C.Structure):

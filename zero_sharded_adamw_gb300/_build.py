@@ -20,7 +20,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libzero1.so")
 SOURCES = ["zero1_host.cu", "zero1_kernels.cu", "zero1_noalloc.cu", "zero1_allreduce.cu", "zero1_partition.cu",
            "zero1_muon.cu", "zero1_muon_kernels.cu", "zero1_muon_small.cu",
-           "zero1_layernorm.cu"]
+           "zero1_layernorm.cu", "zero1_adamw.cu"]
 HEADERS = [os.path.join(CSRC, "zero1_internal.h"), os.path.join(CSRC, "zero1_ptx.cuh"), os.path.join(CSRC, "zero1_policy.h"),
            os.path.join(CSRC, "zero1_muon.h"), os.path.join(CSRC, "zero1_muon_tiles.h"),
            os.path.join(CSRC, "zero1_muon_device.cuh"), os.path.join(CSRC, "zero1_tc.cuh"),

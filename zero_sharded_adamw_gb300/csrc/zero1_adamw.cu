@@ -1,0 +1,1020 @@
+// zero1_adamw.cu -- AdamW over a list of tensors, one step of all of them at
+// once, with moments in fp32 or in 8 bits (include/zero1.h, zero1_adamw_*).
+//
+// The list's state is one flat run of blocks of 256 entries; a tensor starts
+// at a block of its own, and a table names the tensor of every block.  One
+// warp takes one block: its 8 entries a lane are 16 or 32 bytes of each
+// operand, and the two largest values of a block (which its scales are formed
+// from) are one warp reduction each.  So the grid is even whatever the
+// tensors' sizes are, and a list of any length takes one pass.
+//
+// 8 bits.  With f(k, b) = (1 + (k mod 2^b)/2^b) 2^(k div 2^b):
+//     m       = +-(f(k, 3) - 1) (max|m| / 61439),        7 bits and a sign,
+//     sqrt(v) =   (f(k, 4) - 1) (max sqrt(v) / 63487),   8 bits:
+// evenly spaced near zero and by octaves beyond, a fraction 2^-4 or 2^-5 of
+// the value apart at most, over 2^-19 and 2^-20 of the block's largest.
+// A running mean moves by a fraction 1-beta of itself a step, less than half
+// a code's width (v with beta2 = 0.95 by 5% at most when it decays), so
+// rounding to nearest would hold it where it is; every code is rounded up or
+// down at random instead, by 16 bits of a hash of the seed, the step and the
+// entry's place, with the exact value as its mean.  sqrt(v) > 0 is never
+// rounded to zero: m may be rounded up where v vanishes, and m / sqrt(v)
+// would have no bound.  The update uses the new moments before they are
+// rounded.
+//
+// Every fp32 operation is rounded by itself (no fma), so master, parameters
+// and codes are those of the written formulas bit for bit.  The norm's sum
+// of squares is compensated in fp32 (each square and each addition with its
+// error) and then fp64, so that the fp32 clip coefficient is its correct
+// rounding but for values within 1e-12 of a tie.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+#include <exception>
+#include <memory>
+#include <mutex>
+#include <new>
+#include <unordered_set>
+#include <vector>
+
+#include "zero1.h"
+#include "zero1_internal.h"
+#include "zero1_launch.h"
+#include "zero1_ptx.cuh"
+
+namespace zero1 {
+namespace {
+
+constexpr uint32_t kListBlock = 256;      // entries of one block: 8 a lane of one warp
+constexpr int kListThreads = 256;
+constexpr uint32_t kWarps = kListThreads / 32;
+constexpr uint32_t kUpdateBlocks = 4;     // blocks of a warp of the update
+constexpr uint32_t kNormBlocks = 4;       // ... of the norm, at a time
+constexpr float kMTop = 61439.f, kRTop = 63487.f;       // f(127, 3) - 1, f(255, 4) - 1
+constexpr uint32_t kHeldLow = 27u << 23;                // 2^-100: a block whose largest value is smaller is all zeros
+constexpr uint32_t kInf = 0x7F800000u;
+constexpr uint64_t kMaxListTable = 1ull << 22;          // steps of the bias-correction table
+
+// What the kernels share in device memory.
+struct ListStatus {
+    double nsq, norm, lr;
+    unsigned long long t;     // steps taken
+    float clip;
+    float step_size, decay;   // of the next step
+    unsigned ticket[2];       // blocks that have finished: of the norm, of the update; 0 between launches
+};
+
+struct ListTensor {
+    uint64_t first;           // its first block
+    uint64_t n;
+    uint32_t decays, pad;
+};
+
+struct ListTables {
+    const uint32_t *tensor_of;      // of every block
+    const ListTensor *tensors;
+    ListStatus *status;
+    double *partials;               // of the norm: one for each block of its grids
+    const double *correction;       // sqrt(1 - beta2^t) / (1 - beta1^t) for t = 1 .. steps
+    uint64_t steps;
+    double weight_decay, max_norm;
+};
+
+// The scalars of step t + 1.
+__device__ void form_scalars(const ListTables &d, unsigned long long t, double lr)
+{
+    const uint64_t i = t < d.steps ? t : d.steps - 1;   // both corrections are 1 from there on
+    d.status->step_size = __double2float_rn(__dmul_rn(lr, d.correction[i]));
+    d.status->decay = __double2float_rn(__dadd_rn(1.0, -__dmul_rn(lr, d.weight_decay)));
+}
+
+// which 1: the steps taken are `t`; 2: the learning rate is `lr`; 3: both.
+__global__ void zero1_adamw_set_kernel(ListTables d, unsigned long long t, double lr, int which)
+{
+    if (which & 1) d.status->t = t;
+    if (which & 2) d.status->lr = lr;
+    form_scalars(d, d.status->t, d.status->lr);
+}
+
+template <int CAP>
+struct NormParams {
+    const void *grads[CAP];
+    ListTables d;
+    uint64_t block0, nblocks;
+    uint32_t tensor0, before;   // partial sums of earlier launches of this step
+    int last;
+};
+
+template <int CAP>
+struct UpdateParams {
+    const void *grads[CAP];
+    void *params[CAP];
+    ListTables d;
+    float *master;
+    void *m, *v;
+    float2 *scales;
+    uint64_t block0, nblocks;
+    uint64_t seed;
+    float beta1, omb1, beta2, omb2, eps;
+    uint32_t tensor0;
+    int clipped, decay_first, last;
+};
+
+// Where a block's entries lie: `count` (at most 256) from entry `first` of
+// its tensor on.
+struct Place {
+    uint64_t first;
+    uint32_t tensor, count, decays;
+};
+__device__ __forceinline__ Place place_of(const ListTables &d, uint64_t block)
+{
+    Place at;
+    at.tensor = d.tensor_of[block];
+    const ListTensor t = d.tensors[at.tensor];
+    at.first = (block - t.first) * kListBlock;
+    at.count = (uint32_t)min((uint64_t)kListBlock, t.n - at.first);
+    at.decays = t.decays;
+    return at;
+}
+
+__device__ __forceinline__ bool whole16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Eight entries of a lane: neighbours (WHOLE: a full block whose tensor is
+// 16-byte aligned) or every 32nd (its loads are then of one entry, side by
+// side over the warp), with zeros past the block's count.
+template <bool WHOLE>
+__device__ __forceinline__ uint32_t entry_of(int j)
+{
+    const uint32_t lane = threadIdx.x & 31;
+    return WHOLE ? lane * 8 + j : j * 32 + lane;
+}
+template <bool WHOLE>
+__device__ __forceinline__ void get8(float v[8], const float *p, uint32_t count)
+{
+    if (WHOLE) {
+        const float4 *q = reinterpret_cast<const float4 *>(p + entry_of<true>(0));
+        const float4 a = q[0], b = q[1];
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = entry_of<false>(j) < count ? p[entry_of<false>(j)] : 0.f;
+    }
+}
+template <bool WHOLE>
+__device__ __forceinline__ void get8(float v[8], const uint16_t *p, uint32_t count)
+{
+    if (WHOLE) {
+        ptx::set_widened(v, *reinterpret_cast<const uint4 *>(p + entry_of<true>(0)));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[j] = entry_of<false>(j) < count ? __uint_as_float((uint32_t)p[entry_of<false>(j)] << 16) : 0.f;
+    }
+}
+template <bool WHOLE>
+__device__ __forceinline__ void put8(float *p, const float v[8], uint32_t count)
+{
+    if (WHOLE) {
+        float4 *q = reinterpret_cast<float4 *>(p + entry_of<true>(0));
+        q[0] = make_float4(v[0], v[1], v[2], v[3]);
+        q[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (entry_of<false>(j) < count) p[entry_of<false>(j)] = v[j];
+    }
+}
+template <bool WHOLE>
+__device__ __forceinline__ void put8(uint16_t *p, const float v[8], uint32_t count)
+{
+    if (WHOLE) {
+        *reinterpret_cast<uint4 *>(p + entry_of<true>(0)) =
+            make_uint4(ptx::pack2(v[0], v[1]), ptx::pack2(v[2], v[3]), ptx::pack2(v[4], v[5]), ptx::pack2(v[6], v[7]));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (entry_of<false>(j) < count) p[entry_of<false>(j)] = __bfloat16_as_ushort(__float2bfloat16_rn(v[j]));
+    }
+}
+// Codes: one byte an entry.
+template <bool WHOLE>
+__device__ __forceinline__ void get8(uint32_t k[8], const uint8_t *p, uint32_t count)
+{
+    if (WHOLE) {
+        const uint2 w = *reinterpret_cast<const uint2 *>(p + entry_of<true>(0));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) k[j] = ((j < 4 ? w.x : w.y) >> (8 * (j & 3))) & 0xFFu;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) k[j] = entry_of<false>(j) < count ? p[entry_of<false>(j)] : 0u;
+    }
+}
+template <bool WHOLE>
+__device__ __forceinline__ void put8(uint8_t *p, const uint32_t k[8], uint32_t count)
+{
+    if (WHOLE) {
+        *reinterpret_cast<uint2 *>(p + entry_of<true>(0)) =
+            make_uint2(k[0] | k[1] << 8 | k[2] << 16 | k[3] << 24, k[4] | k[5] << 8 | k[6] << 16 | k[7] << 24);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (entry_of<false>(j) < count) p[entry_of<false>(j)] = (uint8_t)k[j];
+    }
+}
+
+// ------------------------------------------------------------------ codes
+
+// 32 well-mixed bits: two rounds of multiplication (by the first 32 bits of
+// the fractions of sqrt 2 and sqrt 3) and shifted exclusive or.
+__device__ __forceinline__ uint32_t mix(uint32_t x)
+{
+    x = (x ^ (x >> 16)) * 0x6A09E667u;
+    x = (x ^ (x >> 15)) * 0xBB67AE85u;
+    return x ^ (x >> 16);
+}
+// The key of a step's random bits; `high`: the upper half of an entry's place.
+__device__ __forceinline__ uint32_t key_of(uint64_t seed, unsigned long long t, uint32_t high)
+{
+    const uint32_t k = mix(mix(mix((uint32_t)seed) ^ (uint32_t)(seed >> 32)) ^ (uint32_t)t);
+    return high ? mix(k + high) : k;
+}
+
+__device__ __forceinline__ float m_value(uint32_t k, float scale)
+{
+    const float q = __fmul_rn(__uint_as_float(((k & 127u) << 20) + (127u << 23)) - 1.f, scale);
+    return k & 128u ? -q : q;
+}
+__device__ __forceinline__ float r_value(uint32_t k, float scale)
+{
+    return __fmul_rn(__uint_as_float((k << 19) + (127u << 23)) - 1.f, scale);
+}
+// x / scale as a code of 4 octave bits and BITS fraction bits, rounded at random.
+template <int BITS>
+__device__ __forceinline__ uint32_t code_of(float x, float inv, uint32_t random16)
+{
+    const int y = __float_as_int(__fadd_rn(__fmul_rn(x, inv), 1.f)) + (int)(random16 << (7 - BITS));
+    const int k = (y - (127 << 23)) >> (23 - BITS);
+    return (uint32_t)min(max(k, 0), (16 << BITS) - 1);
+}
+// A block's scale and its inverse from the bits of its largest value; NaN
+// where that is not finite (its codes are then all zero, and stand for NaN).
+__device__ __forceinline__ bool scales_of(uint32_t largest, float top, float &scale, float &inv)
+{
+    const bool held = largest >= kHeldLow && largest < kInf;
+    const float most = __uint_as_float(largest);
+    scale = held ? __fdiv_rn(most, top) : largest < kHeldLow ? 0.f : __uint_as_float(0x7FC00000u);
+    inv = held ? __fdiv_rn(top, most) : 0.f;
+    return held;
+}
+
+// --------------------------------------------------------------- the norm
+
+// A sum of squares to twice fp32's precision.
+struct Squares {
+    float sum = 0.f, rest = 0.f;
+    double wide = 0.0;
+    // Squares of these eight, each with its rounding error.  Values whose
+    // squares leave fp32's range (2^60 and more, or below 2^-50 and not
+    // zero) go to fp64 instead.
+    __device__ __forceinline__ void add(const float g[8])
+    {
+        uint32_t most = 0, least = 0xFFFFFFFFu;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t b = __float_as_uint(g[j]) & 0x7FFFFFFFu;
+            most = max(most, b);
+            least = min(least, b - 1u);   // zero wraps round to the largest
+        }
+        if (most >= (187u << 23) || least < (77u << 23)) {
+#pragma unroll 1
+            for (int j = 0; j < 8; ++j) wide += (double)g[j] * (double)g[j];
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float p = __fmul_rn(g[j], g[j]);
+            const float lost = __fmaf_rn(g[j], g[j], -p);
+            const float s = __fadd_rn(sum, p);
+            const float back = __fadd_rn(s, -sum);
+            // what the addition lost (either may be the larger)
+            rest = __fadd_rn(rest, __fadd_rn(__fadd_rn(__fadd_rn(sum, -__fadd_rn(s, -back)), __fadd_rn(p, -back)), lost));
+            sum = s;
+        }
+    }
+    __device__ __forceinline__ double total() const { return wide + ((double)sum + (double)rest); }
+};
+
+// Sum over the block in a fixed order; valid on thread 0.
+__device__ __forceinline__ double sum_block(double v)
+{
+    __shared__ double part[kWarps];
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    double s = 0.0;
+    if (threadIdx.x == 0)
+        for (uint32_t i = 0; i < kWarps; ++i) s += part[i];
+    __syncthreads();
+    return s;
+}
+
+// Whether this block is the last of its grid to get here (all threads).
+__device__ __forceinline__ bool last_block(unsigned *ticket)
+{
+    __shared__ bool is_last;
+    if (threadIdx.x == 0) {
+        __threadfence();
+        is_last = atomicAdd(ticket, 1u) + 1 == gridDim.x;
+        if (is_last) {
+            __threadfence();
+            *ticket = 0;
+        }
+    }
+    __syncthreads();
+    return is_last;
+}
+
+// Bound by HBM: one read of the gradients.  The last block of the step's last
+// launch adds up all partial sums in order and forms the clip coefficient.
+template <typename G, int CAP>
+__global__ void __launch_bounds__(kListThreads) zero1_adamw_norm_kernel(const __grid_constant__ NormParams<CAP> p)
+{
+    ptx::launch_dependents();
+    Squares ss;
+    const uint64_t step = (uint64_t)gridDim.x * kWarps * kNormBlocks;
+    for (uint64_t b0 = (uint64_t)blockIdx.x * kWarps * kNormBlocks; b0 < p.nblocks; b0 += step) {
+        Place at[kNormBlocks];
+#pragma unroll
+        for (uint32_t u = 0; u < kNormBlocks; ++u) {
+            const uint64_t b = b0 + u * kWarps + (threadIdx.x >> 5);
+            at[u].count = 0;
+            if (b < p.nblocks) at[u] = place_of(p.d, p.block0 + b);
+        }
+        float g[kNormBlocks][8];
+#pragma unroll
+        for (uint32_t u = 0; u < kNormBlocks; ++u) {
+            if (at[u].count == 0) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) g[u][j] = 0.f;
+                continue;
+            }
+            const G *src = static_cast<const G *>(p.grads[at[u].tensor - p.tensor0]) + at[u].first;
+            if (at[u].count == kListBlock && whole16(src))
+                get8<true>(g[u], src, kListBlock);
+            else
+                get8<false>(g[u], src, at[u].count);
+        }
+#pragma unroll
+        for (uint32_t u = 0; u < kNormBlocks; ++u) ss.add(g[u]);
+    }
+    const double sum = sum_block(ss.total());
+    if (threadIdx.x == 0) p.d.partials[p.before + blockIdx.x] = sum;
+    if (!last_block(&p.d.status->ticket[0]) || !p.last) return;
+    double v = 0.0;
+    for (uint32_t i = threadIdx.x; i < p.before + gridDim.x; i += kListThreads) v += __ldcg(p.d.partials + i);
+    v = sum_block(v);
+    if (threadIdx.x == 0) {
+        const double norm = sqrt(v);
+        float c = 1.f;
+        if (isnan(norm))
+            c = __int_as_float(0x7FC00000);
+        else if (p.d.max_norm / norm < 1.0)
+            c = (float)(p.d.max_norm / norm);
+        p.d.status->nsq = v;
+        p.d.status->norm = norm;
+        p.d.status->clip = c;
+    }
+}
+
+// -------------------------------------------------------------- the update
+
+// One block by one warp.
+template <typename P, typename G, int BITS, bool WHOLE, int CAP>
+__device__ __forceinline__ void update_block(const UpdateParams<CAP> &p, const Place &at, uint64_t block, float clip,
+                                             float step_size, float decay, unsigned long long t)
+{
+    const G *grad = static_cast<const G *>(p.grads[at.tensor - p.tensor0]) + at.first;
+    P *param = static_cast<P *>(p.params[at.tensor - p.tensor0]) + at.first;
+    const uint64_t flat = block * kListBlock;
+    constexpr bool kMaster = sizeof(P) == 2;
+    float g[8], w[8], m[8], v[8], r[8];
+    get8<WHOLE>(g, grad, at.count);
+    if constexpr (kMaster)
+        get8<WHOLE>(w, p.master + flat, at.count);
+    else
+        get8<WHOLE>(w, param, at.count);
+    if constexpr (BITS == 32) {
+        get8<WHOLE>(m, static_cast<const float *>(p.m) + flat, at.count);
+        get8<WHOLE>(v, static_cast<const float *>(p.v) + flat, at.count);
+    } else {
+        const float2 s = p.scales[block];
+        uint32_t km[8], kr[8];
+        get8<WHOLE>(km, static_cast<const uint8_t *>(p.m) + flat, at.count);
+        get8<WHOLE>(kr, static_cast<const uint8_t *>(p.v) + flat, at.count);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            m[j] = m_value(km[j], s.x);
+            const float root = r_value(kr[j], s.y);
+            v[j] = __fmul_rn(root, root);
+        }
+    }
+    uint32_t most_m = 0, most_r = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float c = __fmul_rn(g[j], clip);
+        m[j] = __fadd_rn(__fmul_rn(p.beta1, m[j]), __fmul_rn(p.omb1, c));
+        v[j] = __fadd_rn(__fmul_rn(p.beta2, v[j]), __fmul_rn(__fmul_rn(p.omb2, c), c));
+        r[j] = __fsqrt_rn(v[j]);
+        const float u = __fmul_rn(step_size, __fdiv_rn(m[j], __fadd_rn(r[j], p.eps)));
+        if (p.decay_first && at.decays) w[j] = __fmul_rn(w[j], decay);
+        w[j] = __fadd_rn(w[j], -u);
+        if (!p.decay_first && at.decays) w[j] = __fmul_rn(w[j], decay);
+        if (BITS == 8 && (WHOLE || entry_of<WHOLE>(j) < at.count)) {
+            most_m = max(most_m, __float_as_uint(m[j]) & 0x7FFFFFFFu);
+            most_r = max(most_r, __float_as_uint(r[j]) & 0x7FFFFFFFu);
+        }
+    }
+    put8<WHOLE>(param, w, at.count);
+    if constexpr (kMaster) put8<WHOLE>(p.master + flat, w, at.count);
+    if constexpr (BITS == 32) {
+        put8<WHOLE>(static_cast<float *>(p.m) + flat, m, at.count);
+        put8<WHOLE>(static_cast<float *>(p.v) + flat, v, at.count);
+    } else {
+        most_m = __reduce_max_sync(~0u, most_m);
+        most_r = __reduce_max_sync(~0u, most_r);
+        float2 s;
+        float inv_m, inv_r;
+        const bool held_m = scales_of(most_m, kMTop, s.x, inv_m), held_r = scales_of(most_r, kRTop, s.y, inv_r);
+        const uint32_t key = key_of(p.seed, t, (uint32_t)(flat >> 32));
+        uint32_t km[8], kr[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t random = mix(((uint32_t)flat + entry_of<WHOLE>(j)) ^ key);
+            km[j] = held_m ? code_of<3>(fabsf(m[j]), inv_m, random & 0xFFFFu) : 0u;
+            if (m[j] < 0.f) km[j] |= 128u;
+            kr[j] = code_of<4>(r[j], inv_r, random >> 16);
+            if (kr[j] == 0 && r[j] > 0.f) kr[j] = 1u;
+            if (!held_r) kr[j] = 0u;
+        }
+        put8<WHOLE>(static_cast<uint8_t *>(p.m) + flat, km, at.count);
+        put8<WHOLE>(static_cast<uint8_t *>(p.v) + flat, kr, at.count);
+        if ((threadIdx.x & 31) == 0) p.scales[block] = s;
+    }
+}
+
+template <typename P, typename G, int BITS, int CAP>
+__global__ void __launch_bounds__(kListThreads) zero1_adamw_update_kernel(const __grid_constant__ UpdateParams<CAP> p)
+{
+    const ListStatus *status = p.d.status;
+    const float step_size = status->step_size, decay = status->decay;
+    const unsigned long long t = status->t + 1;
+    const uint64_t b0 = (uint64_t)blockIdx.x * kWarps * kUpdateBlocks + (threadIdx.x >> 5);
+    Place at[kUpdateBlocks];
+#pragma unroll
+    for (uint32_t u = 0; u < kUpdateBlocks; ++u) {
+        at[u].count = 0;
+        if (b0 + u * kWarps < p.nblocks) at[u] = place_of(p.d, p.block0 + b0 + u * kWarps);
+    }
+    ptx::grid_dependency_wait();   // for the norm
+    const float clip = p.clipped ? __ldcg(&status->clip) : 1.f;
+#pragma unroll 1
+    for (uint32_t u = 0; u < kUpdateBlocks; ++u) {
+        if (at[u].count == 0) break;
+        const uint64_t block = p.block0 + b0 + u * kWarps;
+        const bool whole = at[u].count == kListBlock && whole16(p.grads[at[u].tensor - p.tensor0]) &&
+                           whole16(p.params[at[u].tensor - p.tensor0]);
+        if (whole)
+            update_block<P, G, BITS, true, CAP>(p, at[u], block, clip, step_size, decay, t);
+        else
+            update_block<P, G, BITS, false, CAP>(p, at[u], block, clip, step_size, decay, t);
+    }
+    __syncthreads();   // every warp has read the scalars
+    if (last_block(&p.d.status->ticket[1]) && p.last && threadIdx.x == 0) {
+        p.d.status->t = t;
+        form_scalars(p.d, t, p.d.status->lr);
+    }
+}
+
+// The moments that 8 bits hold, as fp32.
+__global__ void __launch_bounds__(kListThreads) zero1_adamw_moments_kernel(ListTables d, uint64_t nblocks, const uint8_t *m,
+                                                                           const uint8_t *v, const float2 *scales,
+                                                                           float *m_out, float *v_out)
+{
+    const uint64_t block = (uint64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (block >= nblocks) return;
+    const Place at = place_of(d, block);
+    const float2 s = scales[block];
+    const uint64_t flat = block * kListBlock;
+    const auto run = [&](auto whole) {
+        constexpr bool WHOLE = decltype(whole)::value;
+        uint32_t k[8];
+        float x[8];
+        if (m_out) {
+            get8<WHOLE>(k, m + flat, at.count);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = m_value(k[j], s.x);
+            put8<WHOLE>(m_out + flat, x, at.count);
+        }
+        if (v_out) {
+            get8<WHOLE>(k, v + flat, at.count);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                x[j] = r_value(k[j], s.y);
+                x[j] = __fmul_rn(x[j], x[j]);
+            }
+            put8<WHOLE>(v_out + flat, x, at.count);
+        }
+    };
+    if (at.count == kListBlock)
+        run(std::true_type{});
+    else
+        run(std::false_type{});
+}
+
+}  // namespace
+}  // namespace zero1
+
+// ------------------------------------------------------------------- host
+
+struct zero1_adamw_ctx {
+    zero1_hparams hp{};
+    zero1_adamw_options opt{};
+    std::vector<uint64_t> sizes;
+    std::vector<uint64_t> first;              // block each tensor starts at; one more at the end
+    int device = 0, num_sms = 0;
+    void *block = nullptr;                    // one cudaMalloc: tables, status, partial sums
+    uint64_t block_bytes = 0;
+    zero1::ListTables d{};
+    std::vector<const void *> checked;        // the pointers last found not to overlap
+};
+
+namespace {
+
+using zero1::kListBlock;
+
+std::mutex g_adamw_mu;
+std::unordered_set<zero1_adamw_ctx *> g_adamw_live;
+
+int afail(int code, const char *fmt, ...)
+{
+    char msg[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(msg, sizeof msg, fmt, ap);
+    va_end(ap);
+    zero1::set_error_message(msg);
+    return code;
+}
+
+int acuda(cudaError_t e, const char *what)
+{
+    cudaGetLastError();   // reported here, and not again by the caller's next launch
+    return afail(e == cudaErrorMemoryAllocation ? ZERO1_ENOMEM : ZERO1_ECUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+bool adamw_live(zero1_adamw_ctx *h)
+{
+    std::lock_guard<std::mutex> lk(g_adamw_mu);
+    return h && g_adamw_live.count(h);
+}
+
+bool on16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool fine(double v) { return std::isfinite(v) && v >= 0.0; }
+size_t bytes_of(int dtype) { return dtype == ZERO1_DTYPE_BF16 ? 2 : 4; }
+
+struct AdamwDeviceGuard {
+    int prev = -1;
+    explicit AdamwDeviceGuard(int dev)
+    {
+        if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
+        if (prev != dev) cudaSetDevice(dev);
+    }
+    ~AdamwDeviceGuard()
+    {
+        if (prev >= 0) cudaSetDevice(prev);
+    }
+};
+
+struct FreeAdamw {
+    void operator()(zero1_adamw_ctx *h) const
+    {
+        if (h->block) cudaFree(h->block);
+        delete h;
+    }
+};
+
+// Blocks of a norm launch: eight of 256 threads an SM, or one for each 32 blocks of the list.
+uint32_t norm_grid(uint64_t nblocks, int sms)
+{
+    const uint64_t need = (nblocks + zero1::kWarps * zero1::kNormBlocks - 1) / (zero1::kWarps * zero1::kNormBlocks);
+    return (uint32_t)std::min<uint64_t>(need, 8ull * (uint64_t)sms);
+}
+
+// Tensors whose pointers one launch holds: kernel arguments are 32,764 bytes
+// at most, and longer ones take longer to launch.
+constexpr int kCaps[3] = {32, 256, 1900};
+
+int create(const uint64_t *sizes, const uint8_t *decays, uint64_t count, const zero1_hparams *hp,
+           const zero1_adamw_options *opts, zero1_adamw_handle *out)
+{
+    if (out == nullptr) return afail(ZERO1_EINVAL, "out is NULL");
+    *out = nullptr;
+    if (hp == nullptr || sizes == nullptr) return afail(ZERO1_EINVAL, "sizes or hparams is NULL");
+    if (count == 0 || count > 65536) return afail(ZERO1_EINVAL, "count must be in [1, 65536]");
+    zero1_adamw_options o{};
+    o.state_bits = 32;
+    if (opts) {
+        if (opts->size != sizeof(zero1_adamw_options)) return afail(ZERO1_EINVAL, "options size does not match");
+        o = *opts;
+    }
+    if (o.state_bits != 8 && o.state_bits != 32) return afail(ZERO1_EINVAL, "state_bits must be 8 or 32");
+    for (const int t : {o.param_dtype, o.grad_dtype})
+        if (t != ZERO1_DTYPE_BF16 && t != ZERO1_DTYPE_F32) return afail(ZERO1_EINVAL, "bad dtype");
+    if (o.decay_before_update != 0 && o.decay_before_update != 1)
+        return afail(ZERO1_EINVAL, "decay_before_update must be 0 or 1");
+    if (o.reserved != 0) return afail(ZERO1_EINVAL, "reserved must be 0");
+    if (!fine(hp->lr)) return afail(ZERO1_EINVAL, "lr must be finite and >= 0");
+    if (!(hp->beta1 >= 0.0 && hp->beta1 < 1.0) || !(hp->beta2 >= 0.0 && hp->beta2 < 1.0))
+        return afail(ZERO1_EINVAL, "betas must be in [0, 1)");
+    if (!fine(hp->eps)) return afail(ZERO1_EINVAL, "eps must be finite and >= 0");
+    if (!fine(hp->weight_decay)) return afail(ZERO1_EINVAL, "weight_decay must be finite and >= 0");
+    if (!std::isfinite(hp->max_norm)) return afail(ZERO1_EINVAL, "max_norm must be finite");
+    for (uint64_t i = 0; i < count; ++i)
+        if (sizes[i] > (1ull << 40)) return afail(ZERO1_EINVAL, "tensor %llu has more than 2^40 entries", (unsigned long long)i);
+
+    // ---- the plan
+    std::vector<zero1::ListTensor> tensors(count);
+    std::vector<uint64_t> first(count + 1);
+    uint64_t blocks = 0;
+    for (uint64_t i = 0; i < count; ++i) {
+        first[i] = blocks;
+        tensors[i].first = blocks;
+        tensors[i].n = sizes[i];
+        tensors[i].decays = decays ? decays[i] != 0 : 1;
+        tensors[i].pad = 0;
+        blocks += (sizes[i] + kListBlock - 1) / kListBlock;
+        // 2^40 entries of state are 4 TB: nothing below holds them, and block counts stay far from 32 bits' grids
+        if (blocks > (1ull << 32)) return afail(ZERO1_EINVAL, "the list has more than 2^40 entries");
+    }
+    first[count] = blocks;
+    if (blocks == 0) return afail(ZERO1_EINVAL, "every tensor is empty");
+    std::vector<uint32_t> tensor_of(blocks);
+    for (uint64_t i = 0; i < count; ++i) std::fill(tensor_of.begin() + first[i], tensor_of.begin() + first[i + 1], (uint32_t)i);
+    std::vector<double> correction;
+    for (uint64_t t = 1;; ++t) {
+        if (t > zero1::kMaxListTable)
+            return afail(ZERO1_EINVAL, "the bias corrections do not reach 1.0 within %llu steps",
+                         (unsigned long long)zero1::kMaxListTable);
+        const double bc1 = 1.0 - std::pow(hp->beta1, (double)t), bc2 = 1.0 - std::pow(hp->beta2, (double)t);
+        correction.push_back(std::sqrt(bc2) / bc1);
+        if (bc1 == 1.0 && bc2 == 1.0) break;
+    }
+
+    // ---- the device
+    int ndev = 0, dev = 0;
+    cudaError_t e = cudaGetDeviceCount(&ndev);
+    if (e != cudaSuccess || ndev == 0) {
+        cudaGetLastError();
+        return afail(ZERO1_ENODEV, "no CUDA device (%s)", cudaGetErrorString(e));
+    }
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return acuda(e, "cudaGetDevice");
+    int major = 0, minor = 0, sms = 0;
+    if ((e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev)) != cudaSuccess ||
+        (e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev)) != cudaSuccess ||
+        (e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
+        return acuda(e, "device query");
+    if (major != 10 || minor != 3)
+        return afail(ZERO1_ENODEV, "device %d is sm_%d%d; this library is built for sm_103a", dev, major, minor);
+
+    // partial sums of the norm, over the launches a step takes
+    uint64_t partials = 0;
+    for (uint64_t i = 0; i < count; i += kCaps[2])
+        partials += norm_grid(first[std::min<uint64_t>(i + kCaps[2], count)] - first[i], sms);
+    uint64_t at = 0;
+    const auto take = [&](uint64_t bytes) {
+        const uint64_t here = at;
+        at += (bytes + 255) / 256 * 256;
+        return here;
+    };
+    const uint64_t at_status = take(sizeof(zero1::ListStatus)), at_of = take(blocks * sizeof(uint32_t));
+    const uint64_t at_tensors = take(count * sizeof(zero1::ListTensor));
+    const uint64_t at_corr = take(correction.size() * sizeof(double)), at_part = take(partials * sizeof(double));
+    std::unique_ptr<zero1_adamw_ctx, FreeAdamw> h(new zero1_adamw_ctx);
+    h->hp = *hp;
+    h->opt = o;
+    h->sizes.assign(sizes, sizes + count);
+    h->first = first;
+    h->device = dev;
+    h->num_sms = sms;
+    h->block_bytes = at;
+    if ((e = cudaMalloc(&h->block, at)) != cudaSuccess) {
+        h->block = nullptr;
+        return acuda(e, "cudaMalloc of the list's tables");
+    }
+    unsigned char *base = static_cast<unsigned char *>(h->block);
+    e = cudaMemset(h->block, 0, at);
+    const auto put = [&](uint64_t to, const void *src, uint64_t bytes) {
+        if (e == cudaSuccess) e = cudaMemcpy(base + to, src, bytes, cudaMemcpyHostToDevice);
+    };
+    put(at_of, tensor_of.data(), blocks * sizeof(uint32_t));
+    put(at_tensors, tensors.data(), count * sizeof(zero1::ListTensor));
+    put(at_corr, correction.data(), correction.size() * sizeof(double));
+    zero1::ListTables &d = h->d;
+    d.tensor_of = reinterpret_cast<const uint32_t *>(base + at_of);
+    d.tensors = reinterpret_cast<const zero1::ListTensor *>(base + at_tensors);
+    d.status = reinterpret_cast<zero1::ListStatus *>(base + at_status);
+    d.partials = reinterpret_cast<double *>(base + at_part);
+    d.correction = reinterpret_cast<const double *>(base + at_corr);
+    d.steps = correction.size();
+    d.weight_decay = hp->weight_decay;
+    d.max_norm = hp->max_norm;
+    if (e == cudaSuccess) e = zero1::launch(zero1::zero1_adamw_set_kernel, dim3(1), 1, 0, nullptr, d, 0ull, hp->lr, 3);
+    if (e == cudaSuccess) e = cudaDeviceSynchronize();
+    if (e != cudaSuccess) return acuda(e, "filling the list's tables");
+    {
+        std::lock_guard<std::mutex> lk(g_adamw_mu);
+        g_adamw_live.insert(h.get());
+    }
+    *out = h.release();
+    return ZERO1_OK;
+}
+
+// No parameter tensor may share memory with another, or with a gradient: each
+// is written by blocks that run in any order.  Looked at again only when a
+// pointer has changed.
+int check_overlap(zero1_adamw_ctx *h, const void *const *grads, void *const *params)
+{
+    const size_t count = h->sizes.size();
+    if (h->checked.size() == 2 * count && std::equal(params, params + count, h->checked.begin()) &&
+        std::equal(grads, grads + count, h->checked.begin() + count))
+        return ZERO1_OK;
+    h->checked.clear();
+    struct Range {
+        uintptr_t from, to;
+        bool param;
+        size_t i;
+    };
+    std::vector<Range> r;
+    r.reserve(2 * count);
+    for (size_t i = 0; i < count; ++i) {
+        if (h->sizes[i] == 0) continue;
+        const uintptr_t p = reinterpret_cast<uintptr_t>(params[i]), g = reinterpret_cast<uintptr_t>(grads[i]);
+        r.push_back({p, p + h->sizes[i] * bytes_of(h->opt.param_dtype), true, i});
+        r.push_back({g, g + h->sizes[i] * bytes_of(h->opt.grad_dtype), false, i});
+    }
+    std::sort(r.begin(), r.end(), [](const Range &a, const Range &b) { return a.from < b.from; });
+    // the furthest end so far, of parameters and of anything
+    size_t any = 0, param = SIZE_MAX;
+    for (size_t k = 0; k < r.size(); ++k) {
+        if (k > 0 && ((r[k].param && r[any].to > r[k].from) || (param != SIZE_MAX && r[param].to > r[k].from)))
+            return afail(ZERO1_EINVAL, "parameter tensor %zu shares memory with another tensor of the call",
+                         r[k].param ? r[k].i : r[param].i);
+        if (k == 0 || r[k].to > r[any].to) any = k;
+        if (r[k].param && (param == SIZE_MAX || r[k].to > r[param].to)) param = k;
+    }
+    h->checked.assign(params, params + count);
+    h->checked.insert(h->checked.end(), grads, grads + count);
+    return ZERO1_OK;
+}
+
+struct StepCall {
+    const void *const *grads;
+    void *const *params;
+    float *master;
+    void *m, *v;
+    float *scales;
+    cudaStream_t stream;
+};
+
+template <typename G, int CAP>
+cudaError_t norm_t(const zero1_adamw_ctx *h, const StepCall &c, uint64_t i0, uint64_t i1, uint32_t &before)
+{
+    zero1::NormParams<CAP> p;
+    for (uint64_t i = i0; i < i1; ++i) p.grads[i - i0] = c.grads[i];
+    p.d = h->d;
+    p.block0 = h->first[i0];
+    p.nblocks = h->first[i1] - h->first[i0];
+    p.tensor0 = (uint32_t)i0;
+    p.before = before;
+    p.last = i1 == h->sizes.size();
+    uint32_t grid = norm_grid(p.nblocks, h->num_sms);
+    if (grid == 0) {
+        if (!p.last) return cudaSuccess;
+        grid = 1;   // the last tensors are empty: only the sum is formed
+    }
+    before += grid;
+    return zero1::launch(zero1::zero1_adamw_norm_kernel<G, CAP>, dim3(grid), zero1::kListThreads, 0, c.stream, p);
+}
+
+template <typename P, typename G, int BITS, int CAP>
+cudaError_t update_t(const zero1_adamw_ctx *h, const StepCall &c, uint64_t i0, uint64_t i1)
+{
+    zero1::UpdateParams<CAP> p;
+    for (uint64_t i = i0; i < i1; ++i) p.grads[i - i0] = c.grads[i], p.params[i - i0] = c.params[i];
+    p.d = h->d;
+    p.master = c.master;
+    p.m = c.m;
+    p.v = c.v;
+    p.scales = reinterpret_cast<float2 *>(c.scales);
+    p.block0 = h->first[i0];
+    p.nblocks = h->first[i1] - h->first[i0];
+    p.seed = h->opt.seed;
+    p.beta1 = (float)h->hp.beta1;
+    p.omb1 = (float)(1.0 - h->hp.beta1);
+    p.beta2 = (float)h->hp.beta2;
+    p.omb2 = (float)(1.0 - h->hp.beta2);
+    p.eps = (float)h->hp.eps;
+    p.tensor0 = (uint32_t)i0;
+    p.clipped = h->hp.max_norm > 0.0;
+    p.decay_first = h->opt.decay_before_update;
+    p.last = i1 == h->sizes.size();
+    constexpr uint64_t per = zero1::kWarps * zero1::kUpdateBlocks;
+    uint64_t grid = (p.nblocks + per - 1) / per;
+    if (grid == 0) {
+        if (!p.last) return cudaSuccess;
+        grid = 1;
+    }
+    const auto kernel = zero1::zero1_adamw_update_kernel<P, G, BITS, CAP>;
+    return p.clipped && i0 == 0 ? zero1::launch_early(kernel, dim3((unsigned)grid), zero1::kListThreads, 0, c.stream, p)
+                                : zero1::launch(kernel, dim3((unsigned)grid), zero1::kListThreads, 0, c.stream, p);
+}
+
+template <typename P, typename G, int BITS, int CAP>
+cudaError_t step_t(const zero1_adamw_ctx *h, const StepCall &c)
+{
+    const uint64_t count = h->sizes.size();
+    cudaError_t e = cudaSuccess;
+    uint32_t before = 0;
+    if (h->hp.max_norm > 0.0)
+        for (uint64_t i = 0; e == cudaSuccess && i < count; i += CAP)
+            e = norm_t<G, CAP>(h, c, i, std::min<uint64_t>(i + CAP, count), before);
+    for (uint64_t i = 0; e == cudaSuccess && i < count; i += CAP)
+        e = update_t<P, G, BITS, CAP>(h, c, i, std::min<uint64_t>(i + CAP, count));
+    return e;
+}
+
+template <typename P, typename G, int BITS>
+cudaError_t step_cap(const zero1_adamw_ctx *h, const StepCall &c)
+{
+    const uint64_t count = h->sizes.size();
+    if (count <= (uint64_t)kCaps[0]) return step_t<P, G, BITS, kCaps[0]>(h, c);
+    if (count <= (uint64_t)kCaps[1]) return step_t<P, G, BITS, kCaps[1]>(h, c);
+    return step_t<P, G, BITS, kCaps[2]>(h, c);
+}
+
+template <typename P, typename G>
+cudaError_t step_bits(const zero1_adamw_ctx *h, const StepCall &c)
+{
+    return h->opt.state_bits == 8 ? step_cap<P, G, 8>(h, c) : step_cap<P, G, 32>(h, c);
+}
+
+int check_state(const zero1_adamw_ctx *h, const void *master, const void *m, const void *v, const void *scales)
+{
+    if ((master != nullptr) != (h->opt.param_dtype == ZERO1_DTYPE_BF16))
+        return afail(ZERO1_EINVAL, "master is the fp32 copy of bf16 parameters, and NULL for fp32 ones");
+    if (!m || !v) return afail(ZERO1_EINVAL, "m or v is NULL");
+    if ((scales != nullptr) != (h->opt.state_bits == 8)) return afail(ZERO1_EINVAL, "scales go with moments in 8 bits, and only with them");
+    if (!on16(master) || !on16(m) || !on16(v) || !on16(scales))
+        return afail(ZERO1_EALIGN, "master, m, v and scales must be 16-byte aligned");
+    return ZERO1_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int zero1_adamw_create(const uint64_t *sizes, const uint8_t *decays, uint64_t count, const zero1_hparams *hp,
+                       const zero1_adamw_options *opts, zero1_adamw_handle *out)
+{
+    try {
+        return create(sizes, decays, count, hp, opts, out);
+    } catch (const std::bad_alloc &) {
+        return afail(ZERO1_ENOMEM, "host allocation failed");
+    } catch (const std::exception &x) {
+        return afail(ZERO1_EINVAL, "%s", x.what());
+    }
+}
+
+int zero1_adamw_destroy(zero1_adamw_handle h)
+{
+    if (h == nullptr) return ZERO1_OK;
+    {
+        std::lock_guard<std::mutex> lk(g_adamw_mu);
+        if (!g_adamw_live.erase(h)) return afail(ZERO1_EINVAL, "unknown or already destroyed handle");
+    }
+    AdamwDeviceGuard g(h->device);
+    const cudaError_t e1 = cudaDeviceSynchronize(), e2 = cudaFree(h->block);
+    delete h;
+    if (e1 != cudaSuccess) return acuda(e1, "cudaDeviceSynchronize in destroy");
+    if (e2 != cudaSuccess) return acuda(e2, "cudaFree");
+    return ZERO1_OK;
+}
+
+int zero1_adamw_step(zero1_adamw_handle h, const void *const *grad_ptrs, void *const *param_ptrs, float *master, void *m,
+                     void *v, float *scales, void *stream)
+{
+    if (!adamw_live(h)) return afail(ZERO1_EINVAL, "invalid handle");
+    if (!grad_ptrs || !param_ptrs) return afail(ZERO1_EINVAL, "pointer array is NULL");
+    if (const int rc = check_state(h, master, m, v, scales)) return rc;
+    const size_t gb = bytes_of(h->opt.grad_dtype), pb = bytes_of(h->opt.param_dtype);
+    for (size_t i = 0; i < h->sizes.size(); ++i) {
+        if (h->sizes[i] == 0) continue;
+        if (!grad_ptrs[i] || !param_ptrs[i]) return afail(ZERO1_EINVAL, "tensor %zu is NULL", i);
+        if (reinterpret_cast<uintptr_t>(grad_ptrs[i]) % gb || reinterpret_cast<uintptr_t>(param_ptrs[i]) % pb)
+            return afail(ZERO1_EALIGN, "tensor %zu is not aligned to its elements", i);
+    }
+    cudaError_t e;
+    try {
+        if (const int rc = check_overlap(h, grad_ptrs, param_ptrs)) return rc;
+    } catch (const std::bad_alloc &) {
+        return afail(ZERO1_ENOMEM, "host allocation failed");
+    }
+    AdamwDeviceGuard g(h->device);
+    const StepCall c{grad_ptrs, param_ptrs, master, m, v, scales, static_cast<cudaStream_t>(stream)};
+    if (h->opt.param_dtype == ZERO1_DTYPE_BF16)
+        e = h->opt.grad_dtype == ZERO1_DTYPE_BF16 ? step_bits<uint16_t, uint16_t>(h, c) : step_bits<uint16_t, float>(h, c);
+    else
+        e = h->opt.grad_dtype == ZERO1_DTYPE_BF16 ? step_bits<float, uint16_t>(h, c) : step_bits<float, float>(h, c);
+    return e == cudaSuccess ? ZERO1_OK : acuda(e, "kernel launch");
+}
+
+int zero1_adamw_moments(zero1_adamw_handle h, const void *m, const void *v, const float *scales, float *m_out, float *v_out,
+                        void *stream)
+{
+    if (!adamw_live(h)) return afail(ZERO1_EINVAL, "invalid handle");
+    if (h->opt.state_bits != 8) return afail(ZERO1_EINVAL, "the moments of this handle are fp32 already");
+    if (!m || !v || !scales) return afail(ZERO1_EINVAL, "NULL buffer");
+    if (!on16(m) || !on16(v) || !on16(scales) || !on16(m_out) || !on16(v_out))
+        return afail(ZERO1_EALIGN, "buffers must be 16-byte aligned");
+    AdamwDeviceGuard g(h->device);
+    const uint64_t blocks = h->first.back();
+    const cudaError_t e = zero1::launch(zero1::zero1_adamw_moments_kernel, dim3((unsigned)((blocks + zero1::kWarps - 1) / zero1::kWarps)),
+                                        zero1::kListThreads, 0, static_cast<cudaStream_t>(stream), h->d, blocks,
+                                        static_cast<const uint8_t *>(m), static_cast<const uint8_t *>(v),
+                                        reinterpret_cast<const float2 *>(scales), m_out, v_out);
+    return e == cudaSuccess ? ZERO1_OK : acuda(e, "kernel launch");
+}
+
+int zero1_adamw_set_steps(zero1_adamw_handle h, uint64_t t, void *stream)
+{
+    if (!adamw_live(h)) return afail(ZERO1_EINVAL, "invalid handle");
+    AdamwDeviceGuard g(h->device);
+    const cudaError_t e = zero1::launch(zero1::zero1_adamw_set_kernel, dim3(1), 1, 0, static_cast<cudaStream_t>(stream), h->d,
+                                        (unsigned long long)t, 0.0, 1);
+    return e == cudaSuccess ? ZERO1_OK : acuda(e, "kernel launch");
+}
+
+int zero1_adamw_set_lr(zero1_adamw_handle h, double lr, void *stream)
+{
+    if (!adamw_live(h)) return afail(ZERO1_EINVAL, "invalid handle");
+    if (!fine(lr)) return afail(ZERO1_EINVAL, "lr must be finite and >= 0");
+    AdamwDeviceGuard g(h->device);
+    const cudaError_t e =
+        zero1::launch(zero1::zero1_adamw_set_kernel, dim3(1), 1, 0, static_cast<cudaStream_t>(stream), h->d, 0ull, lr, 2);
+    return e == cudaSuccess ? ZERO1_OK : acuda(e, "kernel launch");
+}
+
+static int read_status(zero1_adamw_ctx *h, zero1::ListStatus *s, void *stream)
+{
+    AdamwDeviceGuard g(h->device);
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaMemcpyAsync(s, h->d.status, sizeof *s, cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    return e == cudaSuccess ? ZERO1_OK : acuda(e, "reading the status");
+}
+
+int zero1_adamw_get_steps(zero1_adamw_handle h, uint64_t *t, void *stream)
+{
+    if (!adamw_live(h)) return afail(ZERO1_EINVAL, "invalid handle");
+    if (!t) return afail(ZERO1_EINVAL, "t is NULL");
+    zero1::ListStatus s;
+    if (const int rc = read_status(h, &s, stream)) return rc;
+    *t = s.t;
+    return ZERO1_OK;
+}
+
+int zero1_adamw_get_grad_norm(zero1_adamw_handle h, double *norm, float *clip_coef, void *stream)
+{
+    if (!adamw_live(h)) return afail(ZERO1_EINVAL, "invalid handle");
+    if (!(h->hp.max_norm > 0.0)) return afail(ZERO1_EINVAL, "a handle that does not clip forms no norm");
+    zero1::ListStatus s;
+    if (const int rc = read_status(h, &s, stream)) return rc;
+    if (norm) *norm = s.norm;
+    if (clip_coef) *clip_coef = s.clip;
+    return ZERO1_OK;
+}
+
+int zero1_adamw_layout(zero1_adamw_handle h, uint64_t *entries, uint64_t *starts, uint64_t *device_bytes)
+{
+    if (!adamw_live(h)) return afail(ZERO1_EINVAL, "invalid handle");
+    if (entries) *entries = h->first.back() * kListBlock;
+    if (starts)
+        for (size_t i = 0; i < h->sizes.size(); ++i) starts[i] = h->first[i] * kListBlock;
+    if (device_bytes) *device_bytes = h->block_bytes;
+    return ZERO1_OK;
+}
+
+}  // extern "C"

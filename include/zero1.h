@@ -704,6 +704,88 @@ int zero1_layernorm_backward(uint64_t rows, uint64_t cols, int dtype, const void
                              const float *rstd, void *dx, uint64_t lddx, void *dgamma, void *dbeta,
                              int grad_dtype, void *workspace, uint64_t workspace_bytes, void *stream);
 
+/* ---------------------------------------------- gated feed-forward block
+ *
+ * The feed-forward block of `rows` rows, a gate on its first layer:
+ *     gate = x Wg,  up = x Wu,  h = act(gate) * up (entry by entry),  y = h Wd,
+ * with x and y rows x width, Wg and Wu width x hidden, Wd hidden x width, all
+ * bf16, row by row with strides of their own.  The matrices and their
+ * gradients are entries of the flat buffers like any others (zero1_matrix):
+ * Wg and Wu may be column slices of one matrix.  Both projections, the
+ * activation and the product are one kernel.  Sums are fp32; h, and in the
+ * backward pass dgate and dup, are rounded to bf16 once, as they are the next
+ * products' operands.
+ *   activation: g sigmoid(g) (SILU), g Phi(g) (GELU, Phi the normal
+ *     distribution function), the latter's tanh form (GELU_TANH), or
+ *     max(g, 0) (RELU, NaN stays NaN);
+ *   rows < 2^31; width 1 to 65,536; hidden 1 to 2^20;
+ *   ldx (x, dx), ldy (y, dy), ldh (gate, up, h), ld_gate (Wg, dWg), ld_up,
+ *     ld_down: entries between rows, at least the matrix's columns; 0 means
+ *     just these.  Entries between rows are not written.  Strides that are
+ *     not multiples of 8 cost a copy of that operand in the workspace;
+ *   unaligned 1: buffers need the alignment of their elements only (0: of 16
+ *     bytes, ZERO1_EALIGN otherwise), at the cost of a copy of each operand
+ *     that is not 16-byte aligned, and of workspace for all of them;
+ *   inject_wait_timeout: failure testing only.  1 = the matrix kernels load
+ *     nothing, so that their waits run out after their 1 s limit (bit 0 of
+ *     *errors); the results mean nothing;
+ *   size: sizeof(zero1_ffn_shape) (lets the struct grow). */
+#define ZERO1_ACT_SILU      0
+#define ZERO1_ACT_GELU      1
+#define ZERO1_ACT_GELU_TANH 2
+#define ZERO1_ACT_RELU      3
+
+typedef struct zero1_ffn_shape {
+    uint32_t size;
+    int32_t activation;
+    uint64_t rows;
+    uint64_t width;
+    uint64_t hidden;
+    uint64_t ldx;
+    uint64_t ldy;
+    uint64_t ldh;
+    uint64_t ld_gate;
+    uint64_t ld_up;
+    uint64_t ld_down;
+    int32_t unaligned;
+    int32_t inject_wait_timeout;
+} zero1_ffn_shape;
+
+/* Host-only: the bytes of workspace a forward (backward = 0) or backward call
+ * of this shape needs: copies of operands (see above), partial sums where few
+ * tiles share a long sum, and in the backward pass dgate and dup.
+ * Errors: ZERO1_EINVAL. */
+int zero1_ffn_workspace(const zero1_ffn_shape *shape, int backward, uint64_t *bytes);
+
+/* Forward.
+ *   gate, up: kept for the backward pass, or both NULL (serving);
+ *   h: written (the backward pass needs it too);
+ *   workspace: device memory of at least zero1_ffn_workspace bytes, 256-byte
+ *     aligned (NULL if 0), used by one call at a time; its contents need not
+ *     be kept;
+ *   errors: optional device word (NULL = none); bit 0 is set if a kernel
+ *     wait gave up (1 s limit), in which case the outputs are not valid.
+ * No output may share an entry with another buffer of the call.  rows = 0
+ * does nothing.  Asynchronous on `stream`; allocates nothing; may be captured.
+ * Errors: ZERO1_EINVAL, ZERO1_EALIGN, ZERO1_ECUDA. */
+int zero1_ffn_forward(const zero1_ffn_shape *shape, const void *x, const void *w_gate, const void *w_up,
+                      const void *w_down, void *gate, void *up, void *h, void *y, void *workspace,
+                      uint64_t workspace_bytes, unsigned *errors, void *stream);
+
+/* Backward, from the forward pass's gate, up and h:
+ *     dh = dy Wd^T,  dup = dh act(gate),  dgate = dh up act'(gate),
+ *     dx = dgate Wg^T + dup Wu^T,
+ *     dWg = x^T dgate,  dWu = x^T dup,  dWd = h^T dy.
+ *   dx: may be NULL (not wanted); dw_gate, dw_up, dw_down: bf16, overwritten,
+ *   each with its weight's stride.  Sums over rows are taken in a fixed
+ *   order: the same inputs give the same bits.  rows = 0 writes zeros to the
+ *   weights' gradients.  The rest as the forward pass.
+ * Errors: ZERO1_EINVAL, ZERO1_EALIGN, ZERO1_ECUDA. */
+int zero1_ffn_backward(const zero1_ffn_shape *shape, const void *dy, const void *x, const void *w_gate,
+                       const void *w_up, const void *w_down, const void *gate, const void *up, const void *h, void *dx,
+                       void *dw_gate, void *dw_up, void *dw_down, void *workspace, uint64_t workspace_bytes,
+                       unsigned *errors, void *stream);
+
 /* ------------------------------------------------- AdamW over many tensors
  *
  * The AdamW step for a model whose parameters are a list of tensors rather

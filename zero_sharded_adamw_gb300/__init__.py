@@ -28,6 +28,8 @@ __all__ = [
     "MuonHparams", "Muon", "zero1_muon_create", "zero1_muon_destroy", "zero1_muon_step", "zero1_muon_orthogonalize",
     "zero1_muon_set_lr", "zero1_muon_status", "zero1_muon_layout",
     "zero1_layernorm_forward", "zero1_layernorm_backward", "zero1_layernorm_workspace",
+    "ACT_SILU", "ACT_GELU", "ACT_GELU_TANH", "ACT_RELU", "FfnShape", "zero1_ffn_workspace", "zero1_ffn_forward",
+    "zero1_ffn_backward",
     "AdamWOptions", "AdamW", "zero1_adamw_create", "zero1_adamw_destroy", "zero1_adamw_step", "zero1_adamw_moments",
     "zero1_adamw_set_steps", "zero1_adamw_set_lr", "zero1_adamw_get_steps", "zero1_adamw_get_grad_norm",
     "zero1_adamw_layout",
@@ -85,6 +87,9 @@ _SIGS = {
     "zero1_layernorm_workspace": (_I32, [_U64, _U64, _P]),
     "zero1_layernorm_backward": (_I32, [_U64, _U64, _I32, _P, _U64, _P, _U64, _P, _P, _P, _P, _U64, _P, _P, _I32, _P,
                                         _U64, _P]),
+    "zero1_ffn_workspace": (_I32, [_P, _I32, _P]),
+    "zero1_ffn_forward": (_I32, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _U64, _P, _P]),
+    "zero1_ffn_backward": (_I32, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _U64, _P, _P]),
     "zero1_adamw_create": (_I32, [_P, _P, _U64, _P, _P, _P]),
     "zero1_adamw_destroy": (_I32, [_P]),
     "zero1_adamw_step": (_I32, [_P, _P, _P, _P, _P, _P, _P, _P]),
@@ -757,6 +762,99 @@ def zero1_layernorm_backward(rows: int, cols: int, dtype: int, dy, lddy: int, x,
         _take_rows(dx, rows, cols, lddx, kind, "dx"), lddx, _take_vector(dgamma, cols, grad_kind, "dgamma"),
         _take_vector(dbeta, cols, grad_kind, "dbeta"), grad_dtype, workspace.data_ptr(),
         workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+# --------------------------------------------------------- gated feed-forward block
+
+ACT_SILU, ACT_GELU, ACT_GELU_TANH, ACT_RELU = 0, 1, 2, 3
+
+
+class _CFfnShape(C.Structure):
+    _fields_ = [("size", C.c_uint32), ("activation", C.c_int32)] + \
+               [(k, C.c_uint64) for k in ("rows", "width", "hidden", "ldx", "ldy", "ldh", "ld_gate", "ld_up", "ld_down")] + \
+               [("unaligned", C.c_int32), ("inject_wait_timeout", C.c_int32)]
+
+
+@dataclass(frozen=True)
+class FfnShape:
+    """Sizes, activation and row strides of a gated feed-forward block (a
+    stride of 0: rows one after another); `unaligned`: buffers need the
+    alignment of their elements only."""
+    rows: int
+    width: int
+    hidden: int
+    activation: int = ACT_SILU
+    ldx: int = 0
+    ldy: int = 0
+    ldh: int = 0
+    ld_gate: int = 0
+    ld_up: int = 0
+    ld_down: int = 0
+    unaligned: bool = False
+    inject_wait_timeout: bool = False    # failure testing: the matrix kernels' waits run out
+
+    def __post_init__(self):
+        for k in ("rows", "width", "hidden", "ldx", "ldy", "ldh", "ld_gate", "ld_up", "ld_down"):
+            if not 0 <= getattr(self, k) < 1 << 63:
+                raise Zero1ArgumentError(f"{k}: {getattr(self, k)} is out of range")
+        c = _CFfnShape(C.sizeof(_CFfnShape), self.activation, self.rows, self.width, self.hidden, self.ldx, self.ldy,
+                       self.ldh, self.ld_gate, self.ld_up, self.ld_down, int(self.unaligned),
+                       int(self.inject_wait_timeout))
+        r, w, h = self.rows, self.width, self.hidden
+        # (rows, columns, stride) of the buffers, for the checks of every call
+        mats = {"x": (r, w, self.ldx or w), "y": (r, w, self.ldy or w), "h": (r, h, self.ldh or h),
+                "w_gate": (w, h, self.ld_gate or h), "w_up": (w, h, self.ld_up or h), "w_down": (h, w, self.ld_down or w)}
+        object.__setattr__(self, "_c", c)
+        object.__setattr__(self, "_mats", mats)
+
+
+def _ffn_mats(shape: FfnShape, **buffers):
+    """Addresses of a call's buffers, each checked as the matrix it is (dx as
+    x, dw_gate as w_gate, ...)."""
+    return [_take_matrix(x, *shape._mats[_FFN_KINDS.get(k, k)], k) for k, x in buffers.items()]
+
+
+_FFN_KINDS = {"dx": "x", "dy": "y", "gate": "h", "up": "h", "dw_gate": "w_gate", "dw_up": "w_up", "dw_down": "w_down"}
+
+
+def _take_matrix(x, rows: int, cols: int, ld: int, what: str) -> int | None:
+    """_take_rows of bf16, a two-dimensional tensor having to be this matrix."""
+    if x is not None and hasattr(x, "data_ptr") and x.dim() == 2 and x.shape != (rows, cols):
+        raise Zero1ArgumentError(f"{what}: expected {rows} x {cols}, got {tuple(x.shape)}")
+    return _take_rows(x, rows, cols, ld, "bf16", what)
+
+
+def _ffn_workspace(workspace) -> tuple[int | None, int]:
+    if workspace is None:
+        return None, 0
+    if not hasattr(workspace, "numel") or not workspace.is_cuda or not workspace.is_contiguous():
+        raise Zero1ArgumentError("workspace: expected a contiguous CUDA tensor")
+    return workspace.data_ptr() or None, workspace.numel() * workspace.element_size()
+
+
+def zero1_ffn_workspace(shape: FfnShape, backward: bool = False) -> int:
+    """Bytes of workspace a forward or backward call needs (host only, no device)."""
+    b = C.c_uint64()
+    _check(_load().zero1_ffn_workspace(C.byref(shape._c), int(backward), C.byref(b)))
+    return b.value
+
+
+def zero1_ffn_forward(shape: FfnShape, x, w_gate, w_up, w_down, gate, up, h, y, workspace=None, stream=None,
+                      errors=None) -> None:
+    """y = (act(x w_gate) * (x w_up)) w_down, keeping h and, unless both are
+    None, gate and up; `workspace` is a CUDA tensor of at least
+    zero1_ffn_workspace bytes, `errors` an optional CUDA word."""
+    mats = _ffn_mats(shape, x=x, w_gate=w_gate, w_up=w_up, w_down=w_down, gate=gate, up=up, h=h, y=y)
+    _check(_load().zero1_ffn_forward(C.byref(shape._c), *mats, *_ffn_workspace(workspace), _addr(errors), _stream(stream)))
+
+
+def zero1_ffn_backward(shape: FfnShape, dy, x, w_gate, w_up, w_down, gate, up, h, dx, dw_gate, dw_up, dw_down,
+                       workspace=None, stream=None, errors=None) -> None:
+    """The gradients of x (None: not wanted) and of the three matrices, from the forward pass's gate, up and h."""
+    mats = _ffn_mats(shape, dy=dy, x=x, w_gate=w_gate, w_up=w_up, w_down=w_down, gate=gate, up=up, h=h, dx=dx,
+                     dw_gate=dw_gate, dw_up=dw_up, dw_down=dw_down)
+    _check(_load().zero1_ffn_backward(C.byref(shape._c), *mats, *_ffn_workspace(workspace), _addr(errors),
+                                      _stream(stream)))
 
 
 # --------------------------------------------------------- AdamW over many tensors

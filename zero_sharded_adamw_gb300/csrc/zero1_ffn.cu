@@ -1,0 +1,419 @@
+// zero1_ffn.cu -- C ABI of the gated feed-forward block (include/zero1.h,
+// zero1_ffn_*): argument checks, the workspace, copies of operands whose rows
+// TMA cannot address, tensor maps and launches.
+#include <cuda_runtime.h>
+
+#include <cstdarg>
+#include <cstdio>
+#include <cstring>
+
+#include "zero1.h"
+#include "zero1_ffn.h"
+#include "zero1_internal.h"
+#include "zero1_launch.h"
+
+namespace zero1 {
+namespace {
+
+constexpr uint64_t kMaxWidth = 65536, kMaxHidden = 1ull << 20;
+
+int ffail(int code, const char *fmt, ...)
+{
+    char msg[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(msg, sizeof msg, fmt, ap);
+    va_end(ap);
+    set_error_message(msg);
+    return code;
+}
+
+int fcuda(cudaError_t e, const char *what)
+{
+    cudaGetLastError();   // reported here, and not again by the caller's next launch
+    return ffail(ZERO1_ECUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+// A matrix of a call: bf16, rows `ld` entries apart.
+struct Mat {
+    const void *p;
+    uint64_t rows, cols, ld;
+    const char *name;
+    bool written;
+    bool aligned() const { return ld % 8 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+    uint64_t extent() const { return (rows - 1) * ld + cols; }   // entries from the first to one past the last
+};
+
+// The shape with its defaults put in.
+int check_shape(const zero1_ffn_shape *in, zero1_ffn_shape &s)
+{
+    if (!in) return ffail(ZERO1_EINVAL, "shape is NULL");
+    if (in->size != sizeof(zero1_ffn_shape)) return ffail(ZERO1_EINVAL, "shape size does not match");
+    s = *in;
+    if (s.activation < ZERO1_ACT_SILU || s.activation > ZERO1_ACT_RELU) return ffail(ZERO1_EINVAL, "unknown activation %d", (int)s.activation);
+    if (s.unaligned != 0 && s.unaligned != 1) return ffail(ZERO1_EINVAL, "unaligned must be 0 or 1");
+    if (s.inject_wait_timeout != 0 && s.inject_wait_timeout != 1) return ffail(ZERO1_EINVAL, "inject_wait_timeout must be 0 or 1");
+    if (s.rows > 0x7FFFFFFFull) return ffail(ZERO1_EINVAL, "rows must be below 2^31");
+    if (s.width < 1 || s.width > kMaxWidth) return ffail(ZERO1_EINVAL, "width must be in [1, 65536]");
+    if (s.hidden < 1 || s.hidden > kMaxHidden) return ffail(ZERO1_EINVAL, "hidden must be in [1, 2^20]");
+    const struct {
+        uint64_t *ld, cols, rows;
+        const char *name;
+    } lds[6] = {{&s.ldx, s.width, s.rows, "ldx"},          {&s.ldy, s.width, s.rows, "ldy"},
+                {&s.ldh, s.hidden, s.rows, "ldh"},         {&s.ld_gate, s.hidden, s.width, "ld_gate"},
+                {&s.ld_up, s.hidden, s.width, "ld_up"},    {&s.ld_down, s.width, s.hidden, "ld_down"}};
+    for (const auto &l : lds) {
+        if (*l.ld == 0) *l.ld = l.cols;
+        // strides whose last row is past 2^50 entries name no memory; a tensor map's are below 2^40 bytes
+        if (*l.ld < l.cols || *l.ld >= (1ull << 38) || *l.ld > (1ull << 50) / (l.rows ? l.rows : 1))
+            return ffail(ZERO1_EINVAL, "%s must be at least its matrix's columns, below 2^38, and times the rows at most 2^50", l.name);
+    }
+    // tiles of 256 x 256 (gated: of 128 columns) in one launch
+    const uint64_t m = (s.rows + kFfnTile - 1) / kFfnTile, h = (s.hidden + 127) / 128, w = (s.width + kFfnTile - 1) / kFfnTile;
+    if (m * h >= (1ull << 26) || m * w >= (1ull << 26)) return ffail(ZERO1_EINVAL, "rows times hidden or width is too large");
+    return ZERO1_OK;
+}
+
+// Whether two matrices share an entry.  With rows equally far apart it is
+// exact (column slices of one matrix share none); else their extents decide.
+bool share(Mat a, Mat b)
+{
+    if (reinterpret_cast<uintptr_t>(a.p) > reinterpret_cast<uintptr_t>(b.p)) {
+        const Mat t = a;
+        a = b;
+        b = t;
+    }
+    const uint64_t bytes = reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p);
+    if (bytes >= 2 * a.extent()) return false;
+    if (a.rows == 1) a.ld = b.ld;
+    if (b.rows == 1) b.ld = a.ld;
+    if (a.ld != b.ld || bytes % 2) return true;
+    const uint64_t d = bytes / 2, q = d / a.ld, c = d % a.ld;
+    return (q < a.rows && c < a.cols) || (q + 1 < a.rows && c + b.cols > a.ld);
+}
+
+int check_mats(const zero1_ffn_shape &s, const Mat *m, int count)
+{
+    for (int i = 0; i < count; ++i) {
+        if (!m[i].p) continue;
+        const uintptr_t at = reinterpret_cast<uintptr_t>(m[i].p);
+        if (at % 2 || (!s.unaligned && at % 16))
+            return ffail(ZERO1_EALIGN, "%s is not %s", m[i].name,
+                         at % 2 ? "aligned to its elements" : "16-byte aligned (set `unaligned` in the shape for such buffers)");
+    }
+    for (int i = 0; i < count; ++i)
+        for (int j = i + 1; j < count; ++j)
+            if (m[i].p && m[j].p && (m[i].written || m[j].written) && share(m[i], m[j]))
+                return ffail(ZERO1_EINVAL, "%s and %s share memory", m[i].name, m[j].name);
+    return ZERO1_OK;
+}
+
+// ------------------------------------------------------------- workspace
+
+uint64_t round_up(uint64_t x, uint64_t a) { return (x + a - 1) / a * a; }
+uint64_t tiles_of(uint64_t m, uint64_t n) { return round_up(m, kFfnTile) / kFfnTile * (round_up(n, kFfnTile) / kFfnTile); }
+uint64_t steps_of(uint64_t k) { return (k + kFfnStep - 1) / kFfnStep; }
+
+// A matrix's copy in the workspace, rows padded to 16 bytes.
+uint64_t copy_bytes(uint64_t rows, uint64_t cols) { return round_up(rows * round_up(cols, 8) * 2, 256); }
+
+uint64_t partial_bytes(uint64_t tiles, uint64_t steps)
+{
+    const uint64_t s = ffn_slices(tiles, steps);
+    return s > 1 ? tiles * s * kFfnPartial : 0;
+}
+
+// Tiles of the three weight gradients, which one launch takes.
+uint64_t weight_tiles(const zero1_ffn_shape &s) { return 2 * tiles_of(s.width, s.hidden) + tiles_of(s.hidden, s.width); }
+
+uint64_t workspace_of(const zero1_ffn_shape &s, bool backward)
+{
+    if (s.rows == 0) return 0;
+    const auto copy = [&](uint64_t rows, uint64_t cols, uint64_t ld) {
+        return s.unaligned || ld % 8 ? copy_bytes(rows, cols) : 0;
+    };
+    uint64_t b = copy(s.rows, s.width, s.ldx) + copy(s.rows, s.hidden, s.ldh) + copy(s.width, s.hidden, s.ld_gate) +
+                 copy(s.width, s.hidden, s.ld_up) + copy(s.hidden, s.width, s.ld_down);
+    uint64_t partials = partial_bytes(tiles_of(s.rows, s.width), steps_of(s.hidden));
+    if (backward) {
+        b += copy(s.rows, s.width, s.ldy) + 2 * copy_bytes(s.rows, s.hidden);
+        const uint64_t dx = partial_bytes(tiles_of(s.rows, s.width), 2 * steps_of(s.hidden));
+        const uint64_t dw = partial_bytes(weight_tiles(s), steps_of(s.rows));
+        partials = dx > dw ? dx : dw;
+    }
+    return b + partials;
+}
+
+// ---------------------------------------------------------------- copies
+
+// Rows that start off a 16-byte boundary, copied to rows that start on one.
+__global__ void __launch_bounds__(256) zero1_ffn_copy_kernel(const uint16_t *src, uint64_t ld, uint16_t *dst, uint64_t ld_to,
+                                                             uint64_t rows, uint32_t cols)
+{
+    const uint32_t c = blockIdx.x * 256 + threadIdx.x;
+    if (c >= cols) return;
+    for (uint64_t r = blockIdx.y; r < rows; r += gridDim.y) dst[r * ld_to + c] = src[r * ld + c];
+}
+
+typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                             const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encoder()
+{
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+        return nullptr;
+    return reinterpret_cast<EncodeFn>(f);
+}
+
+// One call's state: the first error sticks, and nothing is launched after it.
+struct Call {
+    const zero1_ffn_shape &s;
+    unsigned char *space;
+    uint64_t at = 0;
+    cudaStream_t stream;
+    int sms = 0;
+    unsigned *errors;
+    EncodeFn fn = nullptr;
+    int rc = ZERO1_OK;
+
+    Call(const zero1_ffn_shape &shape, void *workspace, unsigned *err, void *st)
+        : s(shape), space(static_cast<unsigned char *>(workspace)), stream(static_cast<cudaStream_t>(st)), errors(err)
+    {
+        static const EncodeFn found = encoder();
+        fn = found;
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) rc = fcuda(e, "device query");
+        else if (!fn) rc = ffail(ZERO1_ECUDA, "the driver has no tensor-map encoder");
+    }
+    void check(cudaError_t e, const char *what)
+    {
+        if (rc == ZERO1_OK && e != cudaSuccess) rc = fcuda(e, what);
+    }
+    void *take(uint64_t bytes)
+    {
+        void *here = space + at;
+        at += round_up(bytes, 256);
+        return here;
+    }
+    // The matrix itself, or a copy that TMA can address.
+    Mat addressable(Mat m)
+    {
+        if (m.aligned()) return m;
+        const uint64_t ld = round_up(m.cols, 8);
+        uint16_t *to = static_cast<uint16_t *>(take(copy_bytes(m.rows, m.cols)));
+        if (rc == ZERO1_OK) {
+            const dim3 grid((unsigned)((m.cols + 255) / 256), (unsigned)(m.rows < 8192 ? m.rows : 8192));
+            check(launch(zero1_ffn_copy_kernel, grid, 256, 0, stream, static_cast<const uint16_t *>(m.p), m.ld, to, ld, m.rows,
+                         (uint32_t)m.cols),
+                  "kernel launch");
+        }
+        m.p = to;
+        m.ld = ld;
+        return m;
+    }
+    void map(CUtensorMap *to, const Mat &m)
+    {
+        if (rc != ZERO1_OK) return;
+        const cuuint64_t dims[3] = {m.cols, m.rows, 1}, strides[2] = {m.ld * 2, m.ld * 2};
+        const cuuint32_t box[3] = {64, 64, 1}, unit[3] = {1, 1, 1};
+        if (fn(to, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(m.p), dims, strides, box, unit,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            rc = ffail(ZERO1_ECUDA, "encoding the tensor map of %s failed", m.name);
+    }
+    void out(FfnJob &j, int i, const Mat &m)
+    {
+        j.out[i] = static_cast<uint16_t *>(const_cast<void *>(m.p));
+        j.ld_out = m.ld;
+        if (m.p) j.vec_out = (i == 0 || j.vec_out) && m.aligned();
+    }
+};
+
+void size_job(FfnParams &p, int i, uint64_t m, uint64_t n, uint64_t tile_n)
+{
+    FfnJob &j = p.job[i];
+    j.m = (uint32_t)m;
+    j.n = (uint32_t)n;
+    j.tiles_m = (uint32_t)((m + kFfnTile - 1) / kFfnTile);
+    j.tiles_n = (uint32_t)((n + tile_n - 1) / tile_n);
+    j.first = p.tiles;
+    p.tiles += j.tiles_m * j.tiles_n;
+    p.jobs = (uint32_t)i + 1;
+}
+
+FfnParams params_of(const Call &c, uint64_t k, uint32_t segments)
+{
+    FfnParams p;
+    memset(&p, 0, sizeof p);
+    p.steps = (uint32_t)steps_of(k);
+    p.segments = segments;
+    p.slices = 1;
+    p.act = c.s.activation;
+    p.stall = c.s.inject_wait_timeout;
+    p.errors = c.errors;
+    return p;
+}
+
+void slice(FfnParams &p, void *partials)
+{
+    p.slices = ffn_slices(p.tiles, (uint64_t)p.steps * p.segments);
+    p.partials = static_cast<float *>(partials);
+}
+
+int check_workspace(const zero1_ffn_shape &s, bool backward, const void *workspace, uint64_t bytes)
+{
+    const uint64_t need = workspace_of(s, backward);
+    if (bytes < need) return ffail(ZERO1_EINVAL, "the workspace holds %llu bytes, the call needs %llu", (unsigned long long)bytes, (unsigned long long)need);
+    if (need && !workspace) return ffail(ZERO1_EINVAL, "workspace is NULL");
+    if (reinterpret_cast<uintptr_t>(workspace) % 256) return ffail(ZERO1_EALIGN, "the workspace is not 256-byte aligned");
+    return ZERO1_OK;
+}
+
+}  // namespace
+}  // namespace zero1
+
+extern "C" {
+
+int zero1_ffn_workspace(const zero1_ffn_shape *shape, int backward, uint64_t *bytes)
+{
+    using namespace zero1;
+    if (!bytes) return ffail(ZERO1_EINVAL, "bytes is NULL");
+    zero1_ffn_shape s;
+    if (const int rc = check_shape(shape, s)) return rc;
+    *bytes = workspace_of(s, backward != 0);
+    return ZERO1_OK;
+}
+
+int zero1_ffn_forward(const zero1_ffn_shape *shape, const void *x, const void *w_gate, const void *w_up, const void *w_down,
+                      void *gate, void *up, void *h, void *y, void *workspace, uint64_t workspace_bytes, unsigned *errors,
+                      void *stream)
+{
+    using namespace zero1;
+    zero1_ffn_shape s;
+    if (const int rc = check_shape(shape, s)) return rc;
+    if (s.rows == 0) return ZERO1_OK;
+    if (!x || !w_gate || !w_up || !w_down || !h || !y) return ffail(ZERO1_EINVAL, "NULL pointer argument");
+    if ((gate == nullptr) != (up == nullptr)) return ffail(ZERO1_EINVAL, "gate and up are kept together, or neither");
+    if (reinterpret_cast<uintptr_t>(errors) % 4) return ffail(ZERO1_EALIGN, "errors is not 4-byte aligned");
+    const Mat mats[8] = {{x, s.rows, s.width, s.ldx, "x", false},
+                         {w_gate, s.width, s.hidden, s.ld_gate, "w_gate", false},
+                         {w_up, s.width, s.hidden, s.ld_up, "w_up", false},
+                         {w_down, s.hidden, s.width, s.ld_down, "w_down", false},
+                         {h, s.rows, s.hidden, s.ldh, "h", true},
+                         {y, s.rows, s.width, s.ldy, "y", true},
+                         {gate, s.rows, s.hidden, s.ldh, "gate", true},
+                         {up, s.rows, s.hidden, s.ldh, "up", true}};
+    if (const int rc = check_mats(s, mats, 8)) return rc;
+    if (const int rc = check_workspace(s, false, workspace, workspace_bytes)) return rc;
+    Call c(s, workspace, errors, stream);
+    if (c.rc) return c.rc;
+
+    const Mat ax = c.addressable(mats[0]), ag = c.addressable(mats[1]), au = c.addressable(mats[2]), ad = c.addressable(mats[3]);
+    FfnParams p = params_of(c, s.width, 1);
+    c.map(&p.job[0].a[0], ax);
+    c.map(&p.job[0].b[0], ag);
+    c.map(&p.job[0].b[1], au);
+    size_job(p, 0, s.rows, s.hidden, kFfnTile / 2);
+    c.out(p.job[0], 0, mats[4]);
+    c.out(p.job[0], 1, mats[6]);
+    c.out(p.job[0], 2, mats[7]);
+    if (c.rc == ZERO1_OK) c.check(launch_ffn_gated(p, c.sms, c.stream), "kernel launch");
+
+    const Mat ah = c.addressable(mats[4]);
+    FfnParams q = params_of(c, s.hidden, 1);
+    c.map(&q.job[0].a[0], ah);
+    c.map(&q.job[0].b[0], ad);
+    size_job(q, 0, s.rows, s.width, kFfnTile);
+    c.out(q.job[0], 0, mats[5]);
+    slice(q, c.space + c.at);
+    if (c.rc == ZERO1_OK) c.check(launch_ffn_plain(q, false, true, c.sms, c.stream), "kernel launch");
+    return c.rc;
+}
+
+int zero1_ffn_backward(const zero1_ffn_shape *shape, const void *dy, const void *x, const void *w_gate, const void *w_up,
+                       const void *w_down, const void *gate, const void *up, const void *h, void *dx, void *dw_gate,
+                       void *dw_up, void *dw_down, void *workspace, uint64_t workspace_bytes, unsigned *errors, void *stream)
+{
+    using namespace zero1;
+    zero1_ffn_shape s;
+    if (const int rc = check_shape(shape, s)) return rc;
+    if (!dw_gate || !dw_up || !dw_down) return ffail(ZERO1_EINVAL, "NULL pointer argument");
+    const Mat mats[12] = {{dw_gate, s.width, s.hidden, s.ld_gate, "dw_gate", true},
+                          {dw_up, s.width, s.hidden, s.ld_up, "dw_up", true},
+                          {dw_down, s.hidden, s.width, s.ld_down, "dw_down", true},
+                          {dx, s.rows, s.width, s.ldx, "dx", true},
+                          {dy, s.rows, s.width, s.ldy, "dy", false},
+                          {x, s.rows, s.width, s.ldx, "x", false},
+                          {gate, s.rows, s.hidden, s.ldh, "gate", false},
+                          {up, s.rows, s.hidden, s.ldh, "up", false},
+                          {h, s.rows, s.hidden, s.ldh, "h", false},
+                          {w_gate, s.width, s.hidden, s.ld_gate, "w_gate", false},
+                          {w_up, s.width, s.hidden, s.ld_up, "w_up", false},
+                          {w_down, s.hidden, s.width, s.ld_down, "w_down", false}};
+    if (s.rows == 0) {   // sums over no rows
+        if (const int rc = check_mats(s, mats, 3)) return rc;
+        for (int i = 0; i < 3; ++i) {
+            const cudaError_t e = cudaMemset2DAsync(const_cast<void *>(mats[i].p), mats[i].ld * 2, 0, mats[i].cols * 2, mats[i].rows,
+                                                    static_cast<cudaStream_t>(stream));
+            if (e != cudaSuccess) return fcuda(e, "cudaMemset2DAsync");
+        }
+        return ZERO1_OK;
+    }
+    if (!dy || !x || !w_gate || !w_up || !w_down || !gate || !up || !h) return ffail(ZERO1_EINVAL, "NULL pointer argument");
+    if (reinterpret_cast<uintptr_t>(errors) % 4) return ffail(ZERO1_EALIGN, "errors is not 4-byte aligned");
+    if (const int rc = check_mats(s, mats, 12)) return rc;
+    if (const int rc = check_workspace(s, true, workspace, workspace_bytes)) return rc;
+    Call c(s, workspace, errors, stream);
+    if (c.rc) return c.rc;
+
+    const uint64_t ldw = round_up(s.hidden, 8);
+    const Mat dgate{c.take(copy_bytes(s.rows, s.hidden)), s.rows, s.hidden, ldw, "dgate", true};
+    const Mat dup{c.take(copy_bytes(s.rows, s.hidden)), s.rows, s.hidden, ldw, "dup", true};
+    const Mat ady = c.addressable(mats[4]), ax = c.addressable(mats[5]), ah = c.addressable(mats[8]);
+    const Mat ag = c.addressable(mats[9]), au = c.addressable(mats[10]), ad = c.addressable(mats[11]);
+    void *partials = c.space + c.at;
+
+    FfnParams p = params_of(c, s.width, 1);          // dh, and from it dgate and dup
+    c.map(&p.job[0].a[0], ady);
+    c.map(&p.job[0].b[0], ad);
+    size_job(p, 0, s.rows, s.hidden, kFfnTile);
+    c.out(p.job[0], 0, dgate);
+    c.out(p.job[0], 1, dup);
+    p.job[0].in[0] = static_cast<const uint16_t *>(gate);
+    p.job[0].in[1] = static_cast<const uint16_t *>(up);
+    p.job[0].ld_in = s.ldh;
+    p.job[0].vec_in = mats[6].aligned() && mats[7].aligned();
+    if (c.rc == ZERO1_OK) c.check(launch_ffn_slope(p, c.sms, c.stream), "kernel launch");
+
+    FfnParams w = params_of(c, s.rows, 1);           // the weights' gradients
+    const Mat a[3] = {ax, ax, ah}, b[3] = {dgate, dup, ady};
+    for (int i = 0; i < 3; ++i) {
+        c.map(&w.job[i].a[0], a[i]);
+        c.map(&w.job[i].b[0], b[i]);
+        size_job(w, i, mats[i].rows, mats[i].cols, kFfnTile);
+        c.out(w.job[i], 0, mats[i]);
+    }
+    slice(w, partials);
+    if (c.rc == ZERO1_OK) c.check(launch_ffn_plain(w, true, true, c.sms, c.stream), "kernel launch");
+
+    if (dx) {
+        FfnParams q = params_of(c, s.hidden, 2);
+        c.map(&q.job[0].a[0], dgate);
+        c.map(&q.job[0].b[0], ag);
+        c.map(&q.job[0].a[1], dup);
+        c.map(&q.job[0].b[1], au);
+        size_job(q, 0, s.rows, s.width, kFfnTile);
+        c.out(q.job[0], 0, mats[3]);
+        slice(q, partials);
+        if (c.rc == ZERO1_OK) c.check(launch_ffn_plain(q, false, false, c.sms, c.stream), "kernel launch");
+    }
+    return c.rc;
+}
+
+}  // extern "C"

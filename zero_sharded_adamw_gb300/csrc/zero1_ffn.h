@@ -1,0 +1,66 @@
+// zero1_ffn.h -- what the gated feed-forward block's host code (zero1_ffn.cu)
+// and its kernels share.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda.h>   // CUtensorMap
+#include <cuda_runtime.h>
+
+namespace zero1 {
+
+// Tiles of 256 x 256 accumulators by pairs of blocks, 64 of K a step.
+constexpr uint32_t kFfnTile = 256;
+constexpr uint32_t kFfnStep = 64;
+constexpr uint32_t kFfnJobs = 3;
+constexpr uint32_t kFfnPairs = 76;            // pairs of SMs the rules below count on; results do not depend on it
+constexpr uint64_t kFfnPartial = (uint64_t)kFfnTile * kFfnTile * sizeof(float);   // bytes of one tile's partial sums
+
+// What a product does with its tiles.
+enum FfnMode : int {
+    kFfnGated = 0,   // columns 0..127 of a tile are x Wg, the others x Wu of the same 128 hidden columns
+    kFfnPlain = 1,   // out = the sum of its segments' products
+    kFfnSlope = 2,   // the product is dh: out are dgate and dup
+};
+
+// One product: out (m x n) = sum over segments of a[s] b[s].
+struct FfnJob {
+    CUtensorMap a[2], b[2];       // gated: b = gate's and up's weights; plain: one a segment
+    uint16_t *out[3];             // gated: h, gate, up (the last two may be null); plain: out; slope: dgate, dup
+    const uint16_t *in[2];        // slope: gate, up
+    uint64_t ld_out, ld_in;
+    uint32_t m, n;                // rows, columns of the result
+    uint32_t tiles_m, tiles_n;
+    uint32_t first;               // its first tile in the launch
+    uint32_t vec_out, vec_in;     // 16-byte aligned rows
+};
+
+struct FfnParams {
+    FfnJob job[kFfnJobs];
+    uint32_t jobs, tiles, slices;
+    uint32_t steps, segments;     // of 64 of K in a segment
+    int act, stall;
+    float *partials;              // of slices > 1
+    unsigned *errors;             // may be null
+};
+
+// In how many slices K is taken, so that few tiles still fill the pairs: as
+// many as leave every slice 8 steps (512 of K), fewer than make a second
+// round.  A long sum is taken in slices of 65,536 in any case: the tensor
+// cores cut every addition of 16 products off below the sum's last place, so
+// a sum of one sign falls short by 8e-8 of itself for each, 3.3e-4 there, an
+// eighth of a bf16 rounding.
+inline uint32_t ffn_slices(uint64_t tiles, uint64_t steps)
+{
+    uint64_t s = tiles ? kFfnPairs / tiles : 1;
+    if (s > steps / 8) s = steps / 8;
+    const uint64_t least = (steps * kFfnStep + 65535) / 65536;
+    return (uint32_t)(s < least ? least : s < 1 ? 1 : s);
+}
+
+cudaError_t launch_ffn_gated(const FfnParams &p, int sms, cudaStream_t stream);
+cudaError_t launch_ffn_slope(const FfnParams &p, int sms, cudaStream_t stream);
+// a_cols, b_cols: the operand's rows in memory are K (and its columns those of the result).
+cudaError_t launch_ffn_plain(const FfnParams &p, bool a_cols, bool b_cols, int sms, cudaStream_t stream);
+
+}  // namespace zero1

@@ -1,0 +1,415 @@
+// zero1_ffn_gemm.cu -- the matrix products of the gated feed-forward block on
+// the tensor cores, with its activation and that one's gradient as their
+// epilogues.
+//
+//   forward:  gate = x Wg, up = x Wu, h = act(gate) up       (one launch)
+//             y = h Wd
+//   backward: dh = dy Wd^T, dup = dh act(gate),
+//             dgate = dh up act'(gate)                       (one launch)
+//             dWg = x^T dgate, dWu = x^T dup, dWd = h^T dy   (one launch)
+//             dx = dgate Wg^T + dup Wu^T                     (one launch)
+//
+// Operands are bf16 as they lie in memory (K- or MN-major, no transposed
+// copies), sums fp32 in tensor memory.  What is written between the launches
+// (h; dgate and dup) is bf16: the next product takes bf16, and a rounding of
+// 2^-9 of each of its K terms adds up to one of 2^-9 of the result, as much
+// as the result's own.
+#include "zero1_ffn.h"
+#include "zero1_internal.h"
+#include "zero1_launch.h"
+#include "zero1_muon.h"
+#include "zero1_tc.cuh"
+
+namespace zero1 {
+namespace {
+
+constexpr uint32_t kBox = 8192;                     // 64 x 64 bf16
+constexpr uint32_t kStageBytes = 4 * kBox;          // one block's 128 rows of A and 128 of B
+constexpr int kStages = 6;
+constexpr int kEpilogueWarps = 8;
+constexpr int kGemmThreads = 64 + 32 * kEpilogueWarps;
+constexpr uint32_t kWarpTurn = 4096;                // 32 rows x 32 fp32 of an epilogue warp
+constexpr int kGemmSmem = kStages * kStageBytes + kEpilogueWarps * kWarpTurn + 1024;
+static_assert(kGemmSmem >= kAloneSmem, "two pairs could wait for each other's tensor memory");
+
+struct GemmShared {
+    uint64_t full[kStages], empty[kStages];
+    uint64_t acc_full[2], acc_empty[2];
+    uint64_t drain;
+    uint32_t tmem;
+    int abort;
+    unsigned errors;
+};
+
+// bf16 operands (formats 1) of tc::instr_desc's f16 products.
+__device__ __forceinline__ uint32_t bf16_desc(bool a_mn, bool b_mn)
+{
+    return tc::instr_desc(kFfnTile, kFfnTile, a_mn, b_mn) | (1u << 7) | (1u << 10);
+}
+
+// Where an item's tile lies: items are tiles, `slices` of K of each one after
+// another, in groups of 8 tile rows (all columns of a group before the next),
+// so that the pairs at work share operands in L2.
+struct Item {
+    uint32_t job, row, col, begin, end;             // k steps [begin, end) over all segments
+};
+template <int MODE>
+__device__ __forceinline__ Item item_of(const FfnParams &p, uint32_t i)
+{
+    Item t;
+    const uint32_t slice = i % p.slices, tile = i / p.slices;
+    t.job = 0;
+    while (t.job + 1 < p.jobs && tile >= p.job[t.job + 1].first) ++t.job;
+    const FfnJob &j = p.job[t.job];
+    const uint32_t at = tile - j.first, span = 8 * j.tiles_n, group = at / span;
+    const uint32_t height = min(8u, j.tiles_m - group * 8), in = at - group * span;
+    t.row = (group * 8 + in % height) * kFfnTile;
+    t.col = in / height * (MODE == kFfnGated ? kFfnTile / 2 : kFfnTile);
+    const uint32_t steps = p.steps * p.segments;
+    t.begin = (uint32_t)((uint64_t)steps * slice / p.slices);
+    t.end = (uint32_t)((uint64_t)steps * (slice + 1) / p.slices);
+    return t;
+}
+
+// ------------------------------------------------------------- activation
+
+// act(g), and its derivative, in fp32.  The sigmoid from the approximate
+// exponential and quotient: 2e-6 of itself at |g| = 20, a thousandth of a
+// bf16 rounding.
+__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
+
+constexpr float kRootHalf = 0.70710678118654752f, kDensity = 0.39894228040143268f;   // sqrt(1/2), 1/sqrt(2 pi)
+constexpr float kRoot2Pi = 0.79788456080286536f, kCube = 0.044715f;                  // sqrt(2/pi)
+
+template <bool SLOPE>
+__device__ __forceinline__ void activate(int act, float g, float &a, float &slope)
+{
+    if (act == 0) {              // silu
+        const float s = sigmoid(g);
+        a = g * s;
+        if (SLOPE) slope = s + a * (1.f - s);
+    } else if (act == 1) {       // gelu
+        const float cdf = 0.5f + 0.5f * erff(g * kRootHalf);
+        a = g * cdf;
+        if (SLOPE) slope = cdf + g * kDensity * __expf(-0.5f * g * g);
+    } else if (act == 2) {       // gelu, its tanh form: (1 + tanh(z)) / 2 = sigmoid(2 z)
+        const float s = sigmoid(2.f * kRoot2Pi * (g + kCube * g * g * g));
+        a = g * s;
+        if (SLOPE) slope = s + 2.f * a * (1.f - s) * kRoot2Pi * (1.f + 3.f * kCube * g * g);
+    } else {                     // relu; NaN stays NaN
+        a = g <= 0.f ? 0.f : g;
+        if (SLOPE) slope = g <= 0.f ? 0.f : 1.f;
+    }
+}
+
+// --------------------------------------------------------------- epilogue
+
+// 32 x 32 fp32 of a warp, from one row a lane to 4 rows of 8 columns a lane:
+// lane l gets rows 8 i + l / 4, columns 8 (l % 4) on, so that a warp's
+// accesses to global memory are of 64 bytes a row.  Row r keeps its 16-byte
+// pieces exchanged by r % 8: no bank conflicts either way.
+__device__ __forceinline__ uint32_t piece_at(uint32_t mem, uint32_t row, uint32_t piece)
+{
+    return mem + row * 128 + ((piece ^ (row & 7u)) * 16);
+}
+__device__ __forceinline__ void turn(uint32_t mem, const float x[32], float y[4][8])
+{
+    const uint32_t lane = threadIdx.x & 31;
+#pragma unroll
+    for (uint32_t j = 0; j < 8; ++j)
+        tc::st_shared(piece_at(mem, lane, j), make_uint4(__float_as_uint(x[4 * j]), __float_as_uint(x[4 * j + 1]),
+                                                         __float_as_uint(x[4 * j + 2]), __float_as_uint(x[4 * j + 3])));
+    __syncwarp();
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i) {
+#pragma unroll
+        for (uint32_t j = 0; j < 2; ++j) {
+            const uint4 v = tc::ld_shared(piece_at(mem, 8 * i + (lane >> 2), 2 * (lane & 3) + j));
+            y[i][4 * j] = __uint_as_float(v.x);
+            y[i][4 * j + 1] = __uint_as_float(v.y);
+            y[i][4 * j + 2] = __uint_as_float(v.z);
+            y[i][4 * j + 3] = __uint_as_float(v.w);
+        }
+    }
+    __syncwarp();
+}
+__device__ __forceinline__ void tmem_load32(float x[32], uint32_t addr)
+{
+    tc::tmem_load16(x, addr);
+    tc::tmem_load16(x + 16, addr + 16);
+}
+
+// Eight entries of a row, of which `left` are inside the matrix.
+__device__ __forceinline__ void store_row8(uint16_t *p, const float v[8], uint32_t left, bool vec)
+{
+    if (vec && left >= 8) {
+        *reinterpret_cast<uint4 *>(p) =
+            make_uint4(ptx::pack2(v[0], v[1]), ptx::pack2(v[2], v[3]), ptx::pack2(v[4], v[5]), ptx::pack2(v[6], v[7]));
+    } else {
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k)
+            if (k < left) p[k] = __bfloat16_as_ushort(__float2bfloat16_rn(v[k]));
+    }
+}
+__device__ __forceinline__ uint4 load_row8(const uint16_t *p, uint32_t left, bool vec)
+{
+    if (vec && left >= 8) return *reinterpret_cast<const uint4 *>(p);
+    uint32_t w[8];
+#pragma unroll
+    for (uint32_t k = 0; k < 8; ++k) w[k] = k < left ? p[k] : 0u;
+    return make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+}
+
+// Per pair: one thread of each block loads operands (TMA), one thread of the
+// first issues the products, eight warps of each block take its 128 rows of a
+// finished tile out of one accumulator while the other fills.
+template <bool A_MN, bool B_MN, int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
+    zero1_ffn_gemm_kernel(const __grid_constant__ FfnParams p)
+{
+    extern __shared__ unsigned char raw[];
+    __shared__ GemmShared sh;
+    const uint32_t ring = (tc::smem_u32(raw) + 1023u) & ~1023u;
+    const int warp = threadIdx.x >> 5;
+    const uint32_t rank = tc::cluster_rank();
+    unsigned *errors = p.errors ? p.errors : &sh.errors;
+    volatile int *abort = &sh.abort;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) ptx::mbar_init(&sh.full[i], 1), ptx::mbar_init(&sh.empty[i], 1);
+        for (int i = 0; i < 2; ++i) ptx::mbar_init(&sh.acc_full[i], 1), ptx::mbar_init(&sh.acc_empty[i], 2 * kEpilogueWarps);
+        ptx::mbar_init(&sh.drain, 1);
+        sh.abort = 0;
+        sh.errors = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        __syncwarp();
+        tc::tmem_alloc(&sh.tmem, 512);
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    ptx::cluster_sync();
+    tc::fence_after_sync();
+    const uint32_t tmem = sh.tmem;
+    const uint32_t items = p.tiles * p.slices, pairs = gridDim.x / 2, pair = blockIdx.x / 2;
+
+    if (threadIdx.x == 0) {
+        // ---- loads
+        uint32_t issued = 0;
+        bool ok = !p.stall;
+        for (uint32_t i = pair; ok && i < items; i += pairs) {
+            const Item t = item_of<MODE>(p, i);
+            const FfnJob &j = p.job[t.job];
+            const int row = (int)(t.row + rank * 128);
+            const int col = (int)(t.col + (MODE == kFfnGated ? 0 : rank * 128));
+            for (uint32_t s = t.begin; s < t.end; ++s) {
+                const uint32_t stage = issued % kStages;
+                if (issued >= kStages) ok = tc::pair_wait(&sh.empty[stage], (issued / kStages - 1) & 1u, abort, errors);
+                if (!ok) break;
+                const uint32_t seg = s >= p.steps;
+                const int k = (int)((s - seg * p.steps) * kFfnStep);
+                const CUtensorMap *ma = &j.a[seg], *mb = &j.b[MODE == kFfnGated ? rank : seg];
+                if (rank == 0) ptx::mbar_arrive_expect_tx(&sh.full[stage], 2 * kStageBytes);
+                const uint32_t bar = tc::map_to(tc::smem_u32(&sh.full[stage]), 0), dst = ring + stage * kStageBytes;
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const int r = row + 64 * b, c = col + 64 * b;
+                    tc::tma_box_pair(dst + b * kBox, ma, A_MN ? r : k, A_MN ? k : r, 0, bar);
+                    tc::tma_box_pair(dst + (2 + b) * kBox, mb, B_MN ? c : k, B_MN ? k : c, 0, bar);
+                }
+                ++issued;
+            }
+        }
+        if (*abort && rank == 0) ptx::drain_loads<kStages>(sh.full, issued);
+    } else if (threadIdx.x == 32 && rank == 0) {
+        // ---- products
+        uint32_t taken = 0, used = 0;   // stages, accumulators
+        bool ok = true;
+        constexpr uint32_t kAStep = A_MN ? 2048 >> 4 : 32 >> 4, kBStep = B_MN ? 2048 >> 4 : 32 >> 4;   // 16 of K
+        const uint32_t idesc = bf16_desc(A_MN, B_MN);
+        for (uint32_t i = pair; ok && i < items; i += pairs, ++used) {
+            const Item t = item_of<MODE>(p, i);
+            const uint32_t acc = used & 1, d = tmem + acc * kFfnTile;
+            if (used >= 2) {
+                if (!(ok = tc::pair_wait(&sh.acc_empty[acc], (used / 2 - 1) & 1u, abort, errors))) break;
+                tc::fence_after_sync();
+            }
+            for (uint32_t s = t.begin; s < t.end; ++s) {
+                const uint32_t stage = taken % kStages;
+                if (!(ok = tc::pair_wait(&sh.full[stage], (taken / kStages) & 1u, abort, errors))) break;
+                tc::fence_after_sync();
+                const uint32_t src = ring + stage * kStageBytes;
+                const uint64_t a = tc::smem_desc(src, A_MN), b = tc::smem_desc(src + 2 * kBox, B_MN);
+#pragma unroll
+                for (uint32_t q = 0; q < kFfnStep / 16; ++q)
+                    tc::mma_f16(d, a + q * kAStep, b + q * kBStep, idesc, s > t.begin || q > 0);
+                tc::mma_commit(&sh.empty[stage]);
+                ++taken;
+            }
+            if (!ok) break;
+            tc::mma_commit(&sh.acc_full[acc]);
+        }
+        if (!ok) {   // let the products in flight end before the operands and TMEM go
+            tc::mma_commit(&sh.drain);
+            const unsigned long long t0 = ptx::global_ns();
+            while (!ptx::mbar_test(&sh.drain, 0) && ptx::global_ns() - t0 < ptx::kWaitLimitNs) {
+            }
+        }
+    } else if (warp >= 2) {
+        // ---- finished tiles: this block's 128 rows; each group of four warps half of the columns
+        const uint32_t group = (uint32_t)(warp - 2) >> 2, quarter = (uint32_t)warp & 3, lane = threadIdx.x & 31;
+        const uint32_t mem = ring + kStages * kStageBytes + (uint32_t)(warp - 2) * kWarpTurn;
+        constexpr uint32_t kHalf = MODE == kFfnGated ? 64 : 128;      // columns of a group
+        const uint32_t at = tmem + (quarter << 21) + group * kHalf;
+        const uint32_t own_row = rank * 128 + quarter * 32 + (lane >> 2), own_col = group * kHalf + (lane & 3) * 8;
+        uint32_t used = 0;
+        for (uint32_t i = pair; i < items; i += pairs, ++used) {
+            const Item t = item_of<MODE>(p, i);
+            const FfnJob &j = p.job[t.job];
+            const uint32_t acc = used & 1, row = t.row + own_row, col = t.col + own_col, m = j.m, n = j.n;
+            const bool vec_out = j.vec_out, vec_in = j.vec_in;
+            uint4 in[2][4];
+            const auto fetch = [&](uint32_t c) {   // gate and up of 32 columns, while the product is still being formed
+                const uint32_t left = col + c < n ? n - col - c : 0;
+#pragma unroll
+                for (uint32_t q = 0; q < 4; ++q) {
+                    const uint64_t o = (uint64_t)(row + 8 * q) * j.ld_in + col + c;
+                    const uint32_t here = row + 8 * q < m ? left : 0;
+                    in[0][q] = here ? load_row8(j.in[0] + o, here, vec_in) : make_uint4(0, 0, 0, 0);
+                    in[1][q] = here ? load_row8(j.in[1] + o, here, vec_in) : make_uint4(0, 0, 0, 0);
+                }
+            };
+            if (MODE == kFfnSlope) fetch(0);
+            if (!__all_sync(~0u, tc::pair_wait(&sh.acc_full[acc], (used >> 1) & 1u, abort, errors))) break;
+            tc::fence_after_sync();
+#pragma unroll 1
+            for (uint32_t c = 0; c < kHalf; c += 32) {
+                float x[32], y[4][8];
+                tmem_load32(x, at + acc * kFfnTile + c);
+                turn(mem, x, y);
+                float z[4][8];
+                if (MODE == kFfnGated) {
+                    tmem_load32(x, at + acc * kFfnTile + 128 + c);
+                    turn(mem, x, z);
+                }
+                if (c + 32 == kHalf) {   // the accumulator may be written again
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) tc::arrive_cluster_relaxed(tc::map_to(tc::smem_u32(&sh.acc_empty[acc]), 0));
+                }
+                if (MODE == kFfnPlain && p.slices > 1) {
+                    float *to = p.partials + (uint64_t)i * (kFfnTile * kFfnTile) + own_row * kFfnTile + own_col + c;
+#pragma unroll
+                    for (uint32_t q = 0; q < 4; ++q) {
+                        *reinterpret_cast<float4 *>(to + 8 * q * kFfnTile) = make_float4(y[q][0], y[q][1], y[q][2], y[q][3]);
+                        *reinterpret_cast<float4 *>(to + 8 * q * kFfnTile + 4) = make_float4(y[q][4], y[q][5], y[q][6], y[q][7]);
+                    }
+                    continue;
+                }
+                const uint32_t left = col + c < n ? n - col - c : 0;
+                if (MODE == kFfnSlope) {
+#pragma unroll
+                    for (uint32_t q = 0; q < 4; ++q) {
+                        float g[8], u[8];
+                        ptx::set_widened(g, in[0][q]);
+                        ptx::set_widened(u, in[1][q]);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            float a, slope;
+                            activate<true>(p.act, g[k], a, slope);
+                            z[q][k] = y[q][k] * a;
+                            y[q][k] = y[q][k] * u[k] * slope;
+                        }
+                    }
+                    if (c + 32 < kHalf) fetch(c + 32);
+                }
+#pragma unroll
+                for (uint32_t q = 0; q < 4; ++q) {
+                    if (row + 8 * q >= m || left == 0) continue;
+                    const uint64_t o = (uint64_t)(row + 8 * q) * j.ld_out + col + c;
+                    if (MODE == kFfnGated) {
+                        if (j.out[1]) {
+                            store_row8(j.out[1] + o, y[q], left, vec_out);
+                            store_row8(j.out[2] + o, z[q], left, vec_out);
+                        }
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            float a, none;
+                            activate<false>(p.act, y[q][k], a, none);
+                            y[q][k] = a * z[q][k];
+                        }
+                    }
+                    store_row8(j.out[0] + o, y[q], left, vec_out);
+                    if (MODE == kFfnSlope) store_row8(j.out[1] + o, z[q], left, vec_out);
+                }
+            }
+        }
+    }
+    if (*abort) {   // give copies that nothing above waits for (the second block's loads) 1 ms to land
+        const unsigned long long t0 = ptx::global_ns();
+        while (ptx::global_ns() - t0 < 1000000ull) {
+        }
+    }
+    // Neither block leaves, nor gives up its tensor memory, while the other
+    // may still reach into it.
+    __syncwarp();
+    tc::fence_before_sync();
+    __syncthreads();
+    ptx::cluster_sync();
+    tc::fence_after_sync();
+    if (warp == 1) tc::tmem_free(tmem, 512);
+}
+
+// The slices' partial sums, added in order: one warp a row of a tile.
+__global__ void __launch_bounds__(256) zero1_ffn_join_kernel(const __grid_constant__ FfnParams p)
+{
+    const uint32_t tile = blockIdx.x / (kFfnTile / 8), lane = threadIdx.x & 31;
+    const Item t = item_of<kFfnPlain>(p, tile * p.slices);
+    const FfnJob &j = p.job[t.job];
+    const uint32_t r = blockIdx.x % (kFfnTile / 8) * 8 + (threadIdx.x >> 5), row = t.row + r, col = t.col + lane * 8;
+    if (row >= j.m || col >= j.n) return;
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = 0.f;
+    const float *src = p.partials + (uint64_t)tile * p.slices * (kFfnTile * kFfnTile) + r * kFfnTile + lane * 8;
+#pragma unroll 4
+    for (uint32_t s = 0; s < p.slices; ++s, src += kFfnTile * kFfnTile) {
+        const float4 a = reinterpret_cast<const float4 *>(src)[0], b = reinterpret_cast<const float4 *>(src)[1];
+        v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w, v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+    }
+    store_row8(j.out[0] + (uint64_t)row * j.ld_out + col, v, j.n - col, j.vec_out);
+}
+
+template <bool A_MN, bool B_MN, int MODE>
+cudaError_t gemm(const FfnParams &p, int sms, cudaStream_t stream)
+{
+    const auto kernel = zero1_ffn_gemm_kernel<A_MN, B_MN, MODE>;
+    cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), kGemmSmem);
+    if (e != cudaSuccess) return e;
+    const uint32_t pairs = (uint32_t)sms / 2, items = p.tiles * p.slices;
+    e = launch(kernel, dim3(2 * (items < pairs ? items : pairs)), kGemmThreads, kGemmSmem, stream, p);
+    if (e == cudaSuccess && p.slices > 1)
+        e = launch(zero1_ffn_join_kernel, dim3(p.tiles * (kFfnTile / 8)), 256, 0, stream, p);
+    return e;
+}
+
+}  // namespace
+
+cudaError_t launch_ffn_gated(const FfnParams &p, int sms, cudaStream_t stream)
+{
+    return gemm<false, true, kFfnGated>(p, sms, stream);
+}
+
+cudaError_t launch_ffn_slope(const FfnParams &p, int sms, cudaStream_t stream)
+{
+    return gemm<false, false, kFfnSlope>(p, sms, stream);
+}
+
+cudaError_t launch_ffn_plain(const FfnParams &p, bool a_cols, bool b_cols, int sms, cudaStream_t stream)
+{
+    if (a_cols) return gemm<true, true, kFfnPlain>(p, sms, stream);
+    return b_cols ? gemm<false, true, kFfnPlain>(p, sms, stream) : gemm<false, false, kFfnPlain>(p, sms, stream);
+}
+
+}  // namespace zero1

@@ -712,9 +712,11 @@ int zero1_layernorm_backward(uint64_t rows, uint64_t cols, int dtype, const void
  * bf16, row by row with strides of their own.  The matrices and their
  * gradients are entries of the flat buffers like any others (zero1_matrix):
  * Wg and Wu may be column slices of one matrix.  Both projections, the
- * activation and the product are one kernel.  Sums are fp32; h, and in the
- * backward pass dgate and dup, are rounded to bf16 once, as they are the next
- * products' operands.
+ * activation and the product are one kernel.  Sums are fp32; h (of more than
+ * 16 rows), and in the backward pass dgate and dup, are rounded to bf16 once,
+ * as they are the next products' operands.  The sums' order of a forward pass
+ * of at most 128 rows goes by the SMs that the stream may use
+ * (zero1_sm_partition), all others' by the shape alone.
  *   activation: g sigmoid(g) (SILU), g Phi(g) (GELU, Phi the normal
  *     distribution function), the latter's tanh form (GELU_TANH), or
  *     max(g, 0) (RELU, NaN stays NaN);
@@ -752,8 +754,9 @@ typedef struct zero1_ffn_shape {
 } zero1_ffn_shape;
 
 /* Host-only: the bytes of workspace a forward (backward = 0) or backward call
- * of this shape needs: copies of operands (see above), partial sums where few
- * tiles share a long sum, and in the backward pass dgate and dup.
+ * of this shape needs: copies of operands (see above), h (forward, at most 128
+ * rows) or partial sums where few tiles share a long sum, and in the backward
+ * pass dgate and dup.
  * Errors: ZERO1_EINVAL. */
 int zero1_ffn_workspace(const zero1_ffn_shape *shape, int backward, uint64_t *bytes);
 

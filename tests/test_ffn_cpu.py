@@ -77,7 +77,7 @@ def test_unaligned_buffers_refused_to_the_element():
 def test_column_slices_of_one_matrix_share_nothing():
     """Rows equally far apart, side by side: only then the workspace is looked
     at (and refused), not the overlap."""
-    shape = z.FfnShape(40, 16, 32, ldh=96, ld_gate=64, ld_up=64)
+    shape = z.FfnShape(200, 16, 32, ldh=96, ld_gate=64, ld_up=64)
     slices = dict(w_gate=fake(1), w_up=fake(1, 64), gate=fake(4), up=fake(4, 64), h=fake(4, 128))
     with pytest.raises(z.Zero1Error, match="device query|no CUDA|driver|ECUDA"):
         if torch.cuda.is_available():
@@ -87,7 +87,7 @@ def test_column_slices_of_one_matrix_share_nothing():
         fwd(shape, **{**slices, "h": fake(4, 126 - 14)})
     # the last columns of one run into the next row of the other
     with pytest.raises(z.Zero1Error, match="share"):
-        fwd(z.FfnShape(40, 16, 32, ldh=96), gate=fake(4), up=fake(4, 160))
+        fwd(z.FfnShape(200, 16, 32, ldh=96), gate=fake(4), up=fake(4, 160))
 
 
 def test_workspace():

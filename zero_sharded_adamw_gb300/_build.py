@@ -20,11 +20,13 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libzero1.so")
 SOURCES = ["zero1_host.cu", "zero1_kernels.cu", "zero1_noalloc.cu", "zero1_allreduce.cu", "zero1_partition.cu",
            "zero1_muon.cu", "zero1_muon_kernels.cu", "zero1_muon_small.cu",
-           "zero1_layernorm.cu", "zero1_adamw.cu", "zero1_ffn.cu", "zero1_ffn_gemm.cu"]
+           "zero1_layernorm.cu", "zero1_adamw.cu", "zero1_ffn.cu", "zero1_ffn_gemm.cu",
+           "zero1_ffn_thin.cu"]
 HEADERS = [os.path.join(CSRC, "zero1_internal.h"), os.path.join(CSRC, "zero1_ptx.cuh"), os.path.join(CSRC, "zero1_policy.h"),
            os.path.join(CSRC, "zero1_muon.h"), os.path.join(CSRC, "zero1_muon_tiles.h"),
            os.path.join(CSRC, "zero1_muon_device.cuh"), os.path.join(CSRC, "zero1_tc.cuh"),
            os.path.join(CSRC, "zero1_launch.h"), os.path.join(CSRC, "zero1_ffn.h"),
+           os.path.join(CSRC, "zero1_ffn_device.cuh"),
            os.path.join(INCLUDE, "zero1.h")]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")

@@ -126,14 +126,19 @@ uint64_t partial_bytes(uint64_t tiles, uint64_t steps)
 // Tiles of the three weight gradients, which one launch takes.
 uint64_t weight_tiles(const zero1_ffn_shape &s) { return 2 * tiles_of(s.width, s.hidden) + tiles_of(s.hidden, s.width); }
 
+// The forward pass of few rows has kernels of its own.
+bool thin_rows(const zero1_ffn_shape &s, bool backward) { return !backward && s.rows <= kFfnThinRows; }
+
 uint64_t workspace_of(const zero1_ffn_shape &s, bool backward)
 {
     if (s.rows == 0) return 0;
     const auto copy = [&](uint64_t rows, uint64_t cols, uint64_t ld) {
         return s.unaligned || ld % 8 ? copy_bytes(rows, cols) : 0;
     };
-    uint64_t b = copy(s.rows, s.width, s.ldx) + copy(s.rows, s.hidden, s.ldh) + copy(s.width, s.hidden, s.ld_gate) +
-                 copy(s.width, s.hidden, s.ld_up) + copy(s.hidden, s.width, s.ld_down);
+    uint64_t b = copy(s.rows, s.width, s.ldx) + copy(s.width, s.hidden, s.ld_gate) + copy(s.width, s.hidden, s.ld_up) +
+                 copy(s.hidden, s.width, s.ld_down);
+    if (thin_rows(s, backward)) return b + 2 * copy_bytes(s.rows, s.hidden);   // h in two parts
+    b += copy(s.rows, s.hidden, s.ldh);
     uint64_t partials = partial_bytes(tiles_of(s.rows, s.width), steps_of(s.hidden));
     if (backward) {
         b += copy(s.rows, s.width, s.ldy) + 2 * copy_bytes(s.rows, s.hidden);
@@ -217,11 +222,12 @@ struct Call {
         m.ld = ld;
         return m;
     }
-    void map(CUtensorMap *to, const Mat &m)
+    // Boxes of 64 columns and `box_rows` rows; `planes` matrices `plane` entries apart.
+    void map(CUtensorMap *to, const Mat &m, uint32_t box_rows = 64, uint64_t planes = 1, uint64_t plane = 0)
     {
         if (rc != ZERO1_OK) return;
-        const cuuint64_t dims[3] = {m.cols, m.rows, 1}, strides[2] = {m.ld * 2, m.ld * 2};
-        const cuuint32_t box[3] = {64, 64, 1}, unit[3] = {1, 1, 1};
+        const cuuint64_t dims[3] = {m.cols, m.rows, planes}, strides[2] = {m.ld * 2, (planes > 1 ? plane : m.ld) * 2};
+        const cuuint32_t box[3] = {64, box_rows, 1}, unit[3] = {1, 1, 1};
         if (fn(to, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(m.p), dims, strides, box, unit,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
@@ -315,6 +321,35 @@ int zero1_ffn_forward(const zero1_ffn_shape *shape, const void *x, const void *w
     if (c.rc) return c.rc;
 
     const Mat ax = c.addressable(mats[0]), ag = c.addressable(mats[1]), au = c.addressable(mats[2]), ad = c.addressable(mats[3]);
+    if (thin_rows(s, false)) {
+        const uint32_t box = ffn_thin_box(s.rows);
+        const uint64_t plane = copy_bytes(s.rows, s.hidden) / 2;
+        const Mat parts{c.take(4 * plane), s.rows, s.hidden, round_up(s.hidden, 8), "h", true};
+        FfnThin f;
+        memset(&f, 0, sizeof f);
+        c.map(&f.x, ax, box);
+        c.map(&f.w_gate, ag);
+        c.map(&f.w_up, au);
+        c.map(&f.w_down, ad);
+        c.map(&f.h, parts, box, 2, plane);
+        f.out[0] = static_cast<uint16_t *>(h);
+        f.out[1] = static_cast<uint16_t *>(gate);
+        f.out[2] = static_cast<uint16_t *>(up);
+        f.y = static_cast<uint16_t *>(y);
+        f.part = static_cast<uint16_t *>(const_cast<void *>(parts.p));
+        f.ldh = s.ldh;
+        f.ldy = s.ldy;
+        f.ld_part = parts.ld;
+        f.plane = plane;
+        f.rows = (uint32_t)s.rows;
+        f.width = (uint32_t)s.width;
+        f.hidden = (uint32_t)s.hidden;
+        f.act = s.activation;
+        f.stall = s.inject_wait_timeout;
+        f.errors = errors;
+        if (c.rc == ZERO1_OK) c.check(launch_ffn_thin(f, c.sms, c.stream), "kernel launch");
+        return c.rc;
+    }
     FfnParams p = params_of(c, s.width, 1);
     c.map(&p.job[0].a[0], ax);
     c.map(&p.job[0].b[0], ag);

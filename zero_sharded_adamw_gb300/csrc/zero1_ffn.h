@@ -58,6 +58,23 @@ inline uint32_t ffn_slices(uint64_t tiles, uint64_t steps)
     return (uint32_t)(s < least ? least : s < 1 ? 1 : s);
 }
 
+// The forward pass of at most kFfnThinRows rows (zero1_ffn_thin.cu).
+constexpr uint64_t kFfnThinRows = 128;
+
+// Rows of x and of h that one box of the narrow operand holds.
+inline uint32_t ffn_thin_box(uint64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+
+struct FfnThin {
+    CUtensorMap x, w_gate, w_up, w_down, h;   // h: the parts in the workspace
+    uint16_t *out[3], *y, *part;              // h, gate, up (the last two may be null); high and low parts of h
+    uint64_t ldh, ldy, ld_part, plane;
+    uint32_t rows, width, hidden;
+    int act, stall;
+    unsigned *errors;
+};
+
+cudaError_t launch_ffn_thin(const FfnThin &f, int sms, cudaStream_t stream);
+
 cudaError_t launch_ffn_gated(const FfnParams &p, int sms, cudaStream_t stream);
 cudaError_t launch_ffn_slope(const FfnParams &p, int sms, cudaStream_t stream);
 // a_cols, b_cols: the operand's rows in memory are K (and its columns those of the result).

@@ -346,6 +346,8 @@ int zero1_ffn_forward(const zero1_ffn_shape *shape, const void *x, const void *w
         f.hidden = (uint32_t)s.hidden;
         f.act = s.activation;
         f.stall = s.inject_wait_timeout;
+        f.vec[0] = mats[4].aligned() && (!gate || (mats[6].aligned() && mats[7].aligned()));
+        f.vec[1] = mats[5].aligned();
         f.errors = errors;
         if (c.rc == ZERO1_OK) c.check(launch_ffn_thin(f, c.sms, c.stream), "kernel launch");
         return c.rc;

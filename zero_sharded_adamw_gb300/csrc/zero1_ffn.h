@@ -70,6 +70,7 @@ struct FfnThin {
     uint64_t ldh, ldy, ld_part, plane;
     uint32_t rows, width, hidden;
     int act, stall;
+    bool vec[2];                              // aligned rows of h, gate and up; of y
     unsigned *errors;
 };
 

@@ -54,7 +54,7 @@ struct ThinParams {
     uint16_t *part;                            // first: high parts of h, then `plane` entries further the low ones
     uint64_t ld_out, ld_part, plane;
     uint32_t rows, n, steps;                   // rows of x, columns of the result, 64s of K
-    int act, stall;
+    int act, stall, vec;                       // vec: rows of the outputs start at 8 bytes
     unsigned *errors;                          // may be null
 };
 
@@ -67,11 +67,37 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap *map, in
         : "memory");
 }
 
-__device__ __forceinline__ float ld_cluster(uint32_t local, uint32_t rank)
+__device__ __forceinline__ float4 ld_cluster(uint32_t local, uint32_t rank)
 {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(tc::map_to(local, rank)) : "memory");
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(tc::map_to(local, rank)));
     return v;
+}
+// The blocks' sums of four neighbouring columns, added in block order; their
+// loads are in flight together.
+__device__ __forceinline__ void sum_cluster(float out[4], uint32_t local, uint32_t ranks)
+{
+    float4 v[8];
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i)
+        if (i < ranks) v[i] = ld_cluster(local, i);
+    out[0] = out[1] = out[2] = out[3] = 0.f;
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i)
+        if (i < ranks) out[0] += v[i].x, out[1] += v[i].y, out[2] += v[i].z, out[3] += v[i].w;
+}
+// Four neighbouring entries of a row, `left` of them inside the matrix.
+__device__ __forceinline__ void store4(uint16_t *p, const float v[4], uint32_t left, bool vec)
+{
+    if (vec && left >= 4) {
+        *reinterpret_cast<uint2 *>(p) = make_uint2(ptx::pack2(v[0], v[1]), ptx::pack2(v[2], v[3]));
+    } else {
+#pragma unroll
+        for (uint32_t k = 0; k < 4; ++k)
+            if (k < left) p[k] = __bfloat16_as_ushort(__float2bfloat16_rn(v[k]));
+    }
 }
 
 template <int N, bool GATED>
@@ -184,34 +210,36 @@ __global__ void __launch_bounds__(kThinThreads) zero1_ffn_thin_kernel(const __gr
     ptx::cluster_sync();
     tc::fence_after_sync();
     if (warp == 1) tc::tmem_free1(tmem, S::kSums);
-    for (uint32_t o = threadIdx.x + kThinThreads * rank; o < p.rows * 128; o += kThinThreads * ranks) {
-        const uint32_t r = o / 128, c = col0 + o % 128;
+    for (uint32_t o = threadIdx.x + kThinThreads * rank; o < p.rows * 32; o += kThinThreads * ranks) {
+        const uint32_t r = o / 32, c = col0 + o % 32 * 4;
         if (c >= p.n) continue;
-        float a = 0.f, b = 0.f;
-        for (uint32_t i = 0; i < ranks; ++i) {
-            a += ld_cluster(ring + o * 4, i);
-            if (GATED || S::kParts == 2) b += ld_cluster(ring + (N * 128 + o) * 4, i);
-        }
+        const uint32_t left = p.n - c;
+        float a[4], b[4];
+        sum_cluster(a, ring + o * 16, ranks);
+        if (GATED || S::kParts == 2) sum_cluster(b, ring + (N * 32 + o) * 16, ranks);
         const uint64_t at = (uint64_t)r * p.ld_out + c;
         if (GATED) {
             if (p.out[1]) {
-                p.out[1][at] = __bfloat16_as_ushort(__float2bfloat16_rn(a));
-                p.out[2][at] = __bfloat16_as_ushort(__float2bfloat16_rn(b));
+                store4(p.out[1] + at, a, left, p.vec);
+                store4(p.out[2] + at, b, left, p.vec);
             }
-            float v, none;
-            activate<false>(p.act, a, v, none);
-            a = v * b;
-            const __nv_bfloat16 high = __float2bfloat16_rn(a);
-            uint16_t *to = p.part + (uint64_t)r * p.ld_part + c;
-            to[0] = __bfloat16_as_ushort(high);
-            if (N == 16) {   // an infinite h has no low part
-                const float rest = a - __bfloat162float(high);
-                to[p.plane] = isfinite(rest) ? __bfloat16_as_ushort(__float2bfloat16_rn(rest)) : 0;
+            float rest[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float v, none;
+                activate<false>(p.act, a[k], v, none);
+                a[k] = v * b[k];
+                rest[k] = a[k] - __bfloat162float(__float2bfloat16_rn(a[k]));
+                if (!isfinite(rest[k])) rest[k] = 0.f;   // an infinite h has no low part
             }
-        } else {
-            a += b;
+            uint16_t *to = p.part + (uint64_t)r * p.ld_part + c;   // padded to 8 entries
+            store4(to, a, left, true);
+            if (N == 16) store4(to + p.plane, rest, left, true);
+        } else if (S::kParts == 2) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) a[k] += b[k];
         }
-        p.out[0][at] = __bfloat16_as_ushort(__float2bfloat16_rn(a));
+        store4(p.out[0] + at, a, left, p.vec);
     }
     ptx::cluster_sync();   // no block's sums go while another reads them
 }
@@ -288,6 +316,7 @@ cudaError_t launch_ffn_thin(const FfnThin &f, int sms, cudaStream_t stream)
     p.n = f.hidden;
     p.steps = (f.width + 63) / 64;
     p.act = f.act;
+    p.vec = f.vec[0];
     p.stall = f.stall;
     p.errors = f.errors;
     cudaError_t e = thin<true>(p, sms, stream);
@@ -296,6 +325,7 @@ cudaError_t launch_ffn_thin(const FfnThin &f, int sms, cudaStream_t stream)
     p.narrow = f.h;
     p.out[0] = f.y;
     p.ld_out = f.ldy;
+    p.vec = f.vec[1];
     p.n = f.width;
     p.steps = (f.hidden + 63) / 64;
     return thin<false>(p, sms, stream);

@@ -794,7 +794,7 @@ int zero1_ffn_backward(const zero1_ffn_shape *shape, const void *dy, const void 
  * The AdamW step for a model whose parameters are a list of tensors rather
  * than one flat buffer over W ranks: one call steps them all, in two launches
  * (the gradients' norm and the update; one without clipping), whatever their
- * number up to 1,900 (and two more for each 1,900 beyond).
+ * number up to 1,600 (and two more for each 1,600 beyond).
  *
  * Moments are fp32 or 8 bits.  The caller owns all state, in buffers that
  * hold the tensors one after another, each from a multiple of 256 entries on
@@ -832,8 +832,8 @@ typedef struct zero1_adamw_ctx *zero1_adamw_handle;
 
 /* Plan the step of `count` tensors (1 to 65,536) of sizes[i] entries each
  * (empty ones are allowed; 2^40 in all), and allocate its tables on the
- * current device with cudaMalloc: 4 bytes for each 256 entries, 32 a tensor
- * and the bias corrections (as zero1_options.capturable: beta2 = 0.999999 is
+ * current device with cudaMalloc: 4 bytes for each 256 entries and the bias
+ * corrections (as zero1_options.capturable: beta2 = 0.999999 is
  * refused).  decays[i] = 0 spares tensor i the weight decay (vectors,
  * usually); NULL: all decay.  opts may be NULL: fp32 moments, bf16 parameters
  * and gradients.  hp as zero1_create; max_norm <= 0: no norm is formed.

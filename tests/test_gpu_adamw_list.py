@@ -298,6 +298,26 @@ def test_norm_of_extreme_gradients(size):
     assert clip == (1.0 if exact <= 1 else float(torch.tensor(1.0 / exact, dtype=torch.float64).float()))
 
 
+@pytest.mark.parametrize("grad", ["bf16", "f32"])
+@pytest.mark.parametrize("sizes", [[512], [256 * 40], [256 * 31 + 5, 700]])
+@pytest.mark.parametrize("at", [0, 3, 300, 511])
+def test_norm_with_one_extreme_entry(sizes, at, grad):
+    """One entry of 2^62 among ordinary ones: its thread's sum is taken again, of the same entries."""
+    c = Case(sizes, "f32", grad, hp=z.Hparams(max_norm=1.0))
+    c.draw()
+    c.grads[0][at] = 2.0 ** 62
+    c.run()
+    exact = float(torch.cat([g.double() for g in c.grads]).square().sum().sqrt())
+    assert abs(c.opt.grad_norm()[0] - exact) <= exact * 2.0 ** -40
+    # and the others still count
+    c.grads[0].mul_(0)
+    c.grads[0][:5] = 3.0
+    c.grads[0][at] = 2.0 ** -60
+    c.run()
+    exact = float(torch.cat([g.double() for g in c.grads]).square().sum().sqrt())
+    assert abs(c.opt.grad_norm()[0] - exact) <= exact * 2.0 ** -40
+
+
 def test_zeros_and_blocks_below_the_least_scale():
     c = Case([512, 256], bits=8, hp=z.Hparams(max_norm=0.0))
     c.grads[0].zero_()

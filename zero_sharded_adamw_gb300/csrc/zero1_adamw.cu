@@ -67,15 +67,8 @@ struct ListStatus {
     unsigned ticket[2];       // blocks that have finished: of the norm, of the update; 0 between launches
 };
 
-struct ListTensor {
-    uint64_t first;           // its first block
-    uint64_t n;
-    uint32_t decays, pad;
-};
-
 struct ListTables {
-    const uint32_t *tensor_of;      // of every block
-    const ListTensor *tensors;
+    const uint32_t *blocks;         // of every block: its tensor, its entries less one above that, whether it decays
     ListStatus *status;
     double *partials;               // of the norm: one for each block of its grids
     const double *correction;       // sqrt(1 - beta2^t) / (1 - beta1^t) for t = 1 .. steps
@@ -102,6 +95,7 @@ __global__ void zero1_adamw_set_kernel(ListTables d, unsigned long long t, doubl
 template <int CAP>
 struct NormParams {
     const void *grads[CAP];
+    uint32_t first[CAP];        // block that each tensor starts at
     ListTables d;
     uint64_t block0, nblocks;
     uint32_t tensor0, before;   // partial sums of earlier launches of this step
@@ -112,6 +106,7 @@ template <int CAP>
 struct UpdateParams {
     const void *grads[CAP];
     void *params[CAP];
+    uint32_t first[CAP];
     ListTables d;
     float *master;
     void *m, *v;
@@ -119,26 +114,14 @@ struct UpdateParams {
     uint64_t block0, nblocks;
     uint64_t seed;
     float beta1, omb1, beta2, omb2, eps;
-    uint32_t tensor0;
+    uint32_t tensor0, per_warp;   // blocks that a warp takes, one after another
     int clipped, decay_first, last;
 };
 
-// Where a block's entries lie: `count` (at most 256) from entry `first` of
-// its tensor on.
-struct Place {
-    uint64_t first;
-    uint32_t tensor, count, decays;
-};
-__device__ __forceinline__ Place place_of(const ListTables &d, uint64_t block)
-{
-    Place at;
-    at.tensor = d.tensor_of[block];
-    const ListTensor t = d.tensors[at.tensor];
-    at.first = (block - t.first) * kListBlock;
-    at.count = (uint32_t)min((uint64_t)kListBlock, t.n - at.first);
-    at.decays = t.decays;
-    return at;
-}
+constexpr uint32_t pack_block(uint32_t tensor, uint32_t count, bool decays) { return tensor | (count - 1) << 16 | (uint32_t)decays << 24; }
+__device__ __forceinline__ uint32_t tensor_of(uint32_t word) { return word & 0xFFFFu; }
+__device__ __forceinline__ uint32_t count_of(uint32_t word) { return ((word >> 16) & 0xFFu) + 1; }
+__device__ __forceinline__ bool decays_of(uint32_t word) { return word >> 24; }
 
 __device__ __forceinline__ bool whole16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -272,40 +255,70 @@ __device__ __forceinline__ bool scales_of(uint32_t largest, float top, float &sc
 
 // --------------------------------------------------------------- the norm
 
+// Two fp32 numbers in one instruction each, every one rounded by itself.
+struct Two {
+    unsigned long long v;
+};
+__device__ __forceinline__ Two two(float a, float b)
+{
+    Two r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void apart(Two x, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v)); }
+__device__ __forceinline__ Two add(Two a, Two b)
+{
+    Two r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ Two mul(Two a, Two b)
+{
+    Two r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ Two fma(Two a, Two b, Two c)
+{
+    Two r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+
 // A sum of squares to twice fp32's precision.
 struct Squares {
-    float sum = 0.f, rest = 0.f;
-    double wide = 0.0;
-    // Squares of these eight, each with its rounding error.  Values whose
-    // squares leave fp32's range (2^60 and more, or below 2^-50 and not
-    // zero) go to fp64 instead.
-    __device__ __forceinline__ void add(const float g[8])
+    Two sum = two(0.f, 0.f), rest = two(0.f, 0.f);
+    // Squares of two entries with the error of each addition and, where a
+    // square may have one (fp32 entries: bf16's squares have 16 bits), of each square.
+    template <bool EXACT>
+    __device__ __forceinline__ void add2(Two g)
     {
-        uint32_t most = 0, least = 0xFFFFFFFFu;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t b = __float_as_uint(g[j]) & 0x7FFFFFFFu;
-            most = max(most, b);
-            least = min(least, b - 1u);   // zero wraps round to the largest
-        }
-        if (most >= (187u << 23) || least < (77u << 23)) {
-#pragma unroll 1
-            for (int j = 0; j < 8; ++j) wide += (double)g[j] * (double)g[j];
-            return;
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float p = __fmul_rn(g[j], g[j]);
-            const float lost = __fmaf_rn(g[j], g[j], -p);
-            const float s = __fadd_rn(sum, p);
-            const float back = __fadd_rn(s, -sum);
-            // what the addition lost (either may be the larger)
-            rest = __fadd_rn(rest, __fadd_rn(__fadd_rn(__fadd_rn(sum, -__fadd_rn(s, -back)), __fadd_rn(p, -back)), lost));
-            sum = s;
-        }
+        const Two minus = two(-1.f, -1.f);
+        const Two p = mul(g, g), s = add(sum, p);
+        const Two back = fma(sum, minus, s);                              // s - sum
+        Two lost = add(fma(fma(back, minus, s), minus, sum), fma(back, minus, p));
+        if (!EXACT) lost = add(lost, fma(g, g, mul(p, minus)));
+        rest = add(rest, lost);
+        sum = s;
     }
-    __device__ __forceinline__ double total() const { return wide + ((double)sum + (double)rest); }
+    __device__ __forceinline__ float size() const
+    {
+        float a, b;
+        apart(sum, a, b);
+        return a + b;
+    }
+    __device__ __forceinline__ double total() const
+    {
+        float a, b, c, d;
+        apart(sum, a, b);
+        apart(rest, c, d);
+        return ((double)a + (double)b) + ((double)c + (double)d);
+    }
 };
+// Sums whose squares left fp32's range are taken again in fp64: entries from
+// 2^60 on, or only ones below 2^-45 (a square that is cut off at 2^-149 counts
+// in no larger sum).
+constexpr float kSumHigh = 1.3292279957849159e36f, kSumLow = 8.0779356694631609e-28f;   // 2^120, 2^-90
 
 // Sum over the block in a fixed order; valid on thread 0.
 __device__ __forceinline__ double sum_block(double v)
@@ -337,40 +350,98 @@ __device__ __forceinline__ bool last_block(unsigned *ticket)
     return is_last;
 }
 
+// Every kNormBlocks blocks of 256 entries that this warp takes: visit(gradient, entries).
+template <typename G, int CAP, typename F>
+__device__ __forceinline__ void for_grads(const NormParams<CAP> &p, F visit)
+{
+    const uint64_t step = (uint64_t)gridDim.x * kWarps * kNormBlocks;
+    for (uint64_t b0 = (uint64_t)blockIdx.x * kWarps * kNormBlocks + (threadIdx.x >> 5); b0 < p.nblocks; b0 += step) {
+        uint32_t word[kNormBlocks];
+#pragma unroll
+        for (uint32_t u = 0; u < kNormBlocks; ++u)
+            word[u] = b0 + u * kWarps < p.nblocks ? __ldg(p.d.blocks + p.block0 + b0 + u * kWarps) : 0u;
+        const G *src[kNormBlocks];
+        uint32_t count[kNormBlocks];
+#pragma unroll
+        for (uint32_t u = 0; u < kNormBlocks; ++u) {
+            const bool there = b0 + u * kWarps < p.nblocks;
+            const uint32_t i = there ? tensor_of(word[u]) - p.tensor0 : 0;
+            src[u] = static_cast<const G *>(p.grads[i]) + (uint64_t)((uint32_t)(p.block0 + b0) + u * kWarps - p.first[i]) * kListBlock;
+            count[u] = there ? count_of(word[u]) : 0;
+        }
+        visit(src, count);
+    }
+}
+
 // Bound by HBM: one read of the gradients.  The last block of the step's last
 // launch adds up all partial sums in order and forms the clip coefficient.
 template <typename G, int CAP>
-__global__ void __launch_bounds__(kListThreads) zero1_adamw_norm_kernel(const __grid_constant__ NormParams<CAP> p)
+__global__ void __launch_bounds__(kListThreads, 4) zero1_adamw_norm_kernel(const __grid_constant__ NormParams<CAP> p)
 {
+    constexpr bool kExact = sizeof(G) == 2;
     ptx::launch_dependents();
     Squares ss;
-    const uint64_t step = (uint64_t)gridDim.x * kWarps * kNormBlocks;
-    for (uint64_t b0 = (uint64_t)blockIdx.x * kWarps * kNormBlocks; b0 < p.nblocks; b0 += step) {
-        Place at[kNormBlocks];
+    uint32_t any = 0;
+    for_grads<G, CAP>(p, [&](const G *const src[kNormBlocks], const uint32_t count[kNormBlocks]) {
+        bool all = true;
 #pragma unroll
-        for (uint32_t u = 0; u < kNormBlocks; ++u) {
-            const uint64_t b = b0 + u * kWarps + (threadIdx.x >> 5);
-            at[u].count = 0;
-            if (b < p.nblocks) at[u] = place_of(p.d, p.block0 + b);
-        }
-        float g[kNormBlocks][8];
+        for (uint32_t u = 0; u < kNormBlocks; ++u) all = all && count[u] == kListBlock && whole16(src[u]);
+        if (all) {   // as they lie in memory: their bits are looked at by the word
+            constexpr int kPieces = sizeof(G) / 2;
+            uint4 raw[kNormBlocks][kPieces];
 #pragma unroll
-        for (uint32_t u = 0; u < kNormBlocks; ++u) {
-            if (at[u].count == 0) {
+            for (uint32_t u = 0; u < kNormBlocks; ++u)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) g[u][j] = 0.f;
-                continue;
+                for (int q = 0; q < kPieces; ++q) raw[u][q] = reinterpret_cast<const uint4 *>(src[u] + entry_of<true>(0))[q];
+#pragma unroll
+            for (uint32_t u = 0; u < kNormBlocks; ++u)
+#pragma unroll
+                for (int q = 0; q < kPieces; ++q) {
+                    const uint32_t w[4] = {raw[u][q].x, raw[u][q].y, raw[u][q].z, raw[u][q].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        any |= w[k];
+                        if (kExact)
+                            ss.add2<kExact>(two(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u)));
+                        else if (k % 2 == 0)
+                            ss.add2<kExact>(two(__uint_as_float(w[k]), __uint_as_float(w[k + 1])));
+                    }
+                }
+        } else {
+#pragma unroll 1
+            for (uint32_t u = 0; u < kNormBlocks; ++u) {
+                float g[8];
+                get8<false>(g, src[u], count[u]);
+#pragma unroll
+                for (int k = 0; k < 8; k += 2) {
+                    any |= __float_as_uint(g[k]) | __float_as_uint(g[k + 1]);
+                    ss.add2<kExact>(two(g[k], g[k + 1]));
+                }
             }
-            const G *src = static_cast<const G *>(p.grads[at[u].tensor - p.tensor0]) + at[u].first;
-            if (at[u].count == kListBlock && whole16(src))
-                get8<true>(g[u], src, kListBlock);
-            else
-                get8<false>(g[u], src, at[u].count);
         }
+    });
+    double mine = ss.total();
+    const float size = ss.size();
+    // (a sign bit alone may send a thread there: a sum of zeros again)
+    if (!(size < kSumHigh) || (size < kSumLow && any != 0)) {
+        mine = 0.0;
+        for_grads<G, CAP>(p, [&](const G *const src[kNormBlocks], const uint32_t count[kNormBlocks]) {
+            bool all = true;   // the same entries as above
 #pragma unroll
-        for (uint32_t u = 0; u < kNormBlocks; ++u) ss.add(g[u]);
+            for (uint32_t u = 0; u < kNormBlocks; ++u) all = all && count[u] == kListBlock && whole16(src[u]);
+#pragma unroll 1
+            for (uint32_t u = 0; u < kNormBlocks; ++u) {
+                float g[8];
+                if (all)
+                    get8<true>(g, src[u], kListBlock);
+                else
+                    get8<false>(g, src[u], count[u]);
+#pragma unroll 1
+                for (int k = 0; k < 8; ++k) mine += (double)g[k] * (double)g[k];
+            }
+        });
     }
-    const double sum = sum_block(ss.total());
+    const double sum = sum_block(mine);
     if (threadIdx.x == 0) p.d.partials[p.before + blockIdx.x] = sum;
     if (!last_block(&p.d.status->ticket[0]) || !p.last) return;
     double v = 0.0;
@@ -393,27 +464,25 @@ __global__ void __launch_bounds__(kListThreads) zero1_adamw_norm_kernel(const __
 
 // One block by one warp.
 template <typename P, typename G, int BITS, bool WHOLE, int CAP>
-__device__ __forceinline__ void update_block(const UpdateParams<CAP> &p, const Place &at, uint64_t block, float clip,
-                                             float step_size, float decay, unsigned long long t)
+__device__ __forceinline__ void update_block(const UpdateParams<CAP> &p, const G *grad, P *param, uint32_t count, bool decays,
+                                             uint64_t block, float clip, float step_size, float decay, unsigned long long t)
 {
-    const G *grad = static_cast<const G *>(p.grads[at.tensor - p.tensor0]) + at.first;
-    P *param = static_cast<P *>(p.params[at.tensor - p.tensor0]) + at.first;
     const uint64_t flat = block * kListBlock;
     constexpr bool kMaster = sizeof(P) == 2;
     float g[8], w[8], m[8], v[8], r[8];
-    get8<WHOLE>(g, grad, at.count);
+    get8<WHOLE>(g, grad, count);
     if constexpr (kMaster)
-        get8<WHOLE>(w, p.master + flat, at.count);
+        get8<WHOLE>(w, p.master + flat, count);
     else
-        get8<WHOLE>(w, param, at.count);
+        get8<WHOLE>(w, param, count);
     if constexpr (BITS == 32) {
-        get8<WHOLE>(m, static_cast<const float *>(p.m) + flat, at.count);
-        get8<WHOLE>(v, static_cast<const float *>(p.v) + flat, at.count);
+        get8<WHOLE>(m, static_cast<const float *>(p.m) + flat, count);
+        get8<WHOLE>(v, static_cast<const float *>(p.v) + flat, count);
     } else {
         const float2 s = p.scales[block];
         uint32_t km[8], kr[8];
-        get8<WHOLE>(km, static_cast<const uint8_t *>(p.m) + flat, at.count);
-        get8<WHOLE>(kr, static_cast<const uint8_t *>(p.v) + flat, at.count);
+        get8<WHOLE>(km, static_cast<const uint8_t *>(p.m) + flat, count);
+        get8<WHOLE>(kr, static_cast<const uint8_t *>(p.v) + flat, count);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             m[j] = m_value(km[j], s.x);
@@ -429,19 +498,19 @@ __device__ __forceinline__ void update_block(const UpdateParams<CAP> &p, const P
         v[j] = __fadd_rn(__fmul_rn(p.beta2, v[j]), __fmul_rn(__fmul_rn(p.omb2, c), c));
         r[j] = __fsqrt_rn(v[j]);
         const float u = __fmul_rn(step_size, __fdiv_rn(m[j], __fadd_rn(r[j], p.eps)));
-        if (p.decay_first && at.decays) w[j] = __fmul_rn(w[j], decay);
+        if (p.decay_first && decays) w[j] = __fmul_rn(w[j], decay);
         w[j] = __fadd_rn(w[j], -u);
-        if (!p.decay_first && at.decays) w[j] = __fmul_rn(w[j], decay);
-        if (BITS == 8 && (WHOLE || entry_of<WHOLE>(j) < at.count)) {
+        if (!p.decay_first && decays) w[j] = __fmul_rn(w[j], decay);
+        if (BITS == 8 && (WHOLE || entry_of<WHOLE>(j) < count)) {
             most_m = max(most_m, __float_as_uint(m[j]) & 0x7FFFFFFFu);
             most_r = max(most_r, __float_as_uint(r[j]) & 0x7FFFFFFFu);
         }
     }
-    put8<WHOLE>(param, w, at.count);
-    if constexpr (kMaster) put8<WHOLE>(p.master + flat, w, at.count);
+    put8<WHOLE>(param, w, count);
+    if constexpr (kMaster) put8<WHOLE>(p.master + flat, w, count);
     if constexpr (BITS == 32) {
-        put8<WHOLE>(static_cast<float *>(p.m) + flat, m, at.count);
-        put8<WHOLE>(static_cast<float *>(p.v) + flat, v, at.count);
+        put8<WHOLE>(static_cast<float *>(p.m) + flat, m, count);
+        put8<WHOLE>(static_cast<float *>(p.v) + flat, v, count);
     } else {
         most_m = __reduce_max_sync(~0u, most_m);
         most_r = __reduce_max_sync(~0u, most_r);
@@ -459,8 +528,8 @@ __device__ __forceinline__ void update_block(const UpdateParams<CAP> &p, const P
             if (kr[j] == 0 && r[j] > 0.f) kr[j] = 1u;
             if (!held_r) kr[j] = 0u;
         }
-        put8<WHOLE>(static_cast<uint8_t *>(p.m) + flat, km, at.count);
-        put8<WHOLE>(static_cast<uint8_t *>(p.v) + flat, kr, at.count);
+        put8<WHOLE>(static_cast<uint8_t *>(p.m) + flat, km, count);
+        put8<WHOLE>(static_cast<uint8_t *>(p.v) + flat, kr, count);
         if ((threadIdx.x & 31) == 0) p.scales[block] = s;
     }
 }
@@ -471,25 +540,25 @@ __global__ void __launch_bounds__(kListThreads) zero1_adamw_update_kernel(const 
     const ListStatus *status = p.d.status;
     const float step_size = status->step_size, decay = status->decay;
     const unsigned long long t = status->t + 1;
-    const uint64_t b0 = (uint64_t)blockIdx.x * kWarps * kUpdateBlocks + (threadIdx.x >> 5);
-    Place at[kUpdateBlocks];
+    const uint64_t b0 = (uint64_t)blockIdx.x * kWarps * p.per_warp + (threadIdx.x >> 5);
+    uint32_t word[kUpdateBlocks];
 #pragma unroll
-    for (uint32_t u = 0; u < kUpdateBlocks; ++u) {
-        at[u].count = 0;
-        if (b0 + u * kWarps < p.nblocks) at[u] = place_of(p.d, p.block0 + b0 + u * kWarps);
-    }
+    for (uint32_t u = 0; u < kUpdateBlocks; ++u)
+        word[u] = u < p.per_warp && b0 + u * kWarps < p.nblocks ? __ldg(p.d.blocks + p.block0 + b0 + u * kWarps) : 0u;
     ptx::grid_dependency_wait();   // for the norm
     const float clip = p.clipped ? __ldcg(&status->clip) : 1.f;
-#pragma unroll 1
+#pragma unroll
     for (uint32_t u = 0; u < kUpdateBlocks; ++u) {
-        if (at[u].count == 0) break;
+        if (u >= p.per_warp || b0 + u * kWarps >= p.nblocks) break;
         const uint64_t block = p.block0 + b0 + u * kWarps;
-        const bool whole = at[u].count == kListBlock && whole16(p.grads[at[u].tensor - p.tensor0]) &&
-                           whole16(p.params[at[u].tensor - p.tensor0]);
-        if (whole)
-            update_block<P, G, BITS, true, CAP>(p, at[u], block, clip, step_size, decay, t);
+        const uint32_t i = tensor_of(word[u]) - p.tensor0, count = count_of(word[u]);
+        const uint64_t at = (uint64_t)((uint32_t)block - p.first[i]) * kListBlock;
+        const G *grad = static_cast<const G *>(p.grads[i]) + at;
+        P *param = static_cast<P *>(p.params[i]) + at;
+        if (count == kListBlock && whole16(grad) && whole16(param))
+            update_block<P, G, BITS, true, CAP>(p, grad, param, kListBlock, decays_of(word[u]), block, clip, step_size, decay, t);
         else
-            update_block<P, G, BITS, false, CAP>(p, at[u], block, clip, step_size, decay, t);
+            update_block<P, G, BITS, false, CAP>(p, grad, param, count, decays_of(word[u]), block, clip, step_size, decay, t);
     }
     __syncthreads();   // every warp has read the scalars
     if (last_block(&p.d.status->ticket[1]) && p.last && threadIdx.x == 0) {
@@ -505,7 +574,7 @@ __global__ void __launch_bounds__(kListThreads) zero1_adamw_moments_kernel(ListT
 {
     const uint64_t block = (uint64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (block >= nblocks) return;
-    const Place at = place_of(d, block);
+    const uint32_t count = count_of(d.blocks[block]);
     const float2 s = scales[block];
     const uint64_t flat = block * kListBlock;
     const auto run = [&](auto whole) {
@@ -513,22 +582,22 @@ __global__ void __launch_bounds__(kListThreads) zero1_adamw_moments_kernel(ListT
         uint32_t k[8];
         float x[8];
         if (m_out) {
-            get8<WHOLE>(k, m + flat, at.count);
+            get8<WHOLE>(k, m + flat, count);
 #pragma unroll
             for (int j = 0; j < 8; ++j) x[j] = m_value(k[j], s.x);
-            put8<WHOLE>(m_out + flat, x, at.count);
+            put8<WHOLE>(m_out + flat, x, count);
         }
         if (v_out) {
-            get8<WHOLE>(k, v + flat, at.count);
+            get8<WHOLE>(k, v + flat, count);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 x[j] = r_value(k[j], s.y);
                 x[j] = __fmul_rn(x[j], x[j]);
             }
-            put8<WHOLE>(v_out + flat, x, at.count);
+            put8<WHOLE>(v_out + flat, x, count);
         }
     };
-    if (at.count == kListBlock)
+    if (count == kListBlock)
         run(std::true_type{});
     else
         run(std::false_type{});
@@ -615,7 +684,7 @@ uint32_t norm_grid(uint64_t nblocks, int sms)
 
 // Tensors whose pointers one launch holds: kernel arguments are 32,764 bytes
 // at most, and longer ones take longer to launch.
-constexpr int kCaps[3] = {32, 256, 1900};
+constexpr int kCaps[3] = {32, 256, 1600};
 
 int create(const uint64_t *sizes, const uint8_t *decays, uint64_t count, const zero1_hparams *hp,
            const zero1_adamw_options *opts, zero1_adamw_handle *out)
@@ -646,23 +715,24 @@ int create(const uint64_t *sizes, const uint8_t *decays, uint64_t count, const z
         if (sizes[i] > (1ull << 40)) return afail(ZERO1_EINVAL, "tensor %llu has more than 2^40 entries", (unsigned long long)i);
 
     // ---- the plan
-    std::vector<zero1::ListTensor> tensors(count);
     std::vector<uint64_t> first(count + 1);
     uint64_t blocks = 0;
     for (uint64_t i = 0; i < count; ++i) {
         first[i] = blocks;
-        tensors[i].first = blocks;
-        tensors[i].n = sizes[i];
-        tensors[i].decays = decays ? decays[i] != 0 : 1;
-        tensors[i].pad = 0;
         blocks += (sizes[i] + kListBlock - 1) / kListBlock;
-        // 2^40 entries of state are 4 TB: nothing below holds them, and block counts stay far from 32 bits' grids
-        if (blocks > (1ull << 32)) return afail(ZERO1_EINVAL, "the list has more than 2^40 entries");
+        // 2^40 entries of state are 4 TB: block numbers stay below 2^32
+        if (blocks >= (1ull << 32)) return afail(ZERO1_EINVAL, "the list has more than 2^40 entries");
     }
     first[count] = blocks;
     if (blocks == 0) return afail(ZERO1_EINVAL, "every tensor is empty");
-    std::vector<uint32_t> tensor_of(blocks);
-    for (uint64_t i = 0; i < count; ++i) std::fill(tensor_of.begin() + first[i], tensor_of.begin() + first[i + 1], (uint32_t)i);
+    std::vector<uint32_t> words(blocks);
+    for (uint64_t i = 0; i < count; ++i) {
+        const bool d = decays ? decays[i] != 0 : true;
+        if (first[i] == first[i + 1]) continue;
+        std::fill(words.begin() + first[i], words.begin() + first[i + 1], zero1::pack_block((uint32_t)i, kListBlock, d));
+        const uint64_t rest = sizes[i] % kListBlock;
+        if (rest) words[first[i + 1] - 1] = zero1::pack_block((uint32_t)i, (uint32_t)rest, d);
+    }
     std::vector<double> correction;
     for (uint64_t t = 1;; ++t) {
         if (t > zero1::kMaxListTable)
@@ -700,7 +770,6 @@ int create(const uint64_t *sizes, const uint8_t *decays, uint64_t count, const z
         return here;
     };
     const uint64_t at_status = take(sizeof(zero1::ListStatus)), at_of = take(blocks * sizeof(uint32_t));
-    const uint64_t at_tensors = take(count * sizeof(zero1::ListTensor));
     const uint64_t at_corr = take(correction.size() * sizeof(double)), at_part = take(partials * sizeof(double));
     std::unique_ptr<zero1_adamw_ctx, FreeAdamw> h(new zero1_adamw_ctx);
     h->hp = *hp;
@@ -719,12 +788,10 @@ int create(const uint64_t *sizes, const uint8_t *decays, uint64_t count, const z
     const auto put = [&](uint64_t to, const void *src, uint64_t bytes) {
         if (e == cudaSuccess) e = cudaMemcpy(base + to, src, bytes, cudaMemcpyHostToDevice);
     };
-    put(at_of, tensor_of.data(), blocks * sizeof(uint32_t));
-    put(at_tensors, tensors.data(), count * sizeof(zero1::ListTensor));
+    put(at_of, words.data(), blocks * sizeof(uint32_t));
     put(at_corr, correction.data(), correction.size() * sizeof(double));
     zero1::ListTables &d = h->d;
-    d.tensor_of = reinterpret_cast<const uint32_t *>(base + at_of);
-    d.tensors = reinterpret_cast<const zero1::ListTensor *>(base + at_tensors);
+    d.blocks = reinterpret_cast<const uint32_t *>(base + at_of);
     d.status = reinterpret_cast<zero1::ListStatus *>(base + at_status);
     d.partials = reinterpret_cast<double *>(base + at_part);
     d.correction = reinterpret_cast<const double *>(base + at_corr);
@@ -793,7 +860,7 @@ template <typename G, int CAP>
 cudaError_t norm_t(const zero1_adamw_ctx *h, const StepCall &c, uint64_t i0, uint64_t i1, uint32_t &before)
 {
     zero1::NormParams<CAP> p;
-    for (uint64_t i = i0; i < i1; ++i) p.grads[i - i0] = c.grads[i];
+    for (uint64_t i = i0; i < i1; ++i) p.grads[i - i0] = c.grads[i], p.first[i - i0] = (uint32_t)h->first[i];
     p.d = h->d;
     p.block0 = h->first[i0];
     p.nblocks = h->first[i1] - h->first[i0];
@@ -813,7 +880,8 @@ template <typename P, typename G, int BITS, int CAP>
 cudaError_t update_t(const zero1_adamw_ctx *h, const StepCall &c, uint64_t i0, uint64_t i1)
 {
     zero1::UpdateParams<CAP> p;
-    for (uint64_t i = i0; i < i1; ++i) p.grads[i - i0] = c.grads[i], p.params[i - i0] = c.params[i];
+    for (uint64_t i = i0; i < i1; ++i)
+        p.grads[i - i0] = c.grads[i], p.params[i - i0] = c.params[i], p.first[i - i0] = (uint32_t)h->first[i];
     p.d = h->d;
     p.master = c.master;
     p.m = c.m;
@@ -831,7 +899,8 @@ cudaError_t update_t(const zero1_adamw_ctx *h, const StepCall &c, uint64_t i0, u
     p.clipped = h->hp.max_norm > 0.0;
     p.decay_first = h->opt.decay_before_update;
     p.last = i1 == h->sizes.size();
-    constexpr uint64_t per = zero1::kWarps * zero1::kUpdateBlocks;
+    p.per_warp = p.nblocks < 16ull * zero1::kWarps * (uint64_t)h->num_sms ? 1 : zero1::kUpdateBlocks;
+    const uint64_t per = (uint64_t)zero1::kWarps * p.per_warp;
     uint64_t grid = (p.nblocks + per - 1) / per;
     if (grid == 0) {
         if (!p.last) return cudaSuccess;

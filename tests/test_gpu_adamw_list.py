@@ -318,6 +318,34 @@ def test_norm_with_one_extreme_entry(sizes, at, grad):
     assert abs(c.opt.grad_norm()[0] - exact) <= exact * 2.0 ** -40
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("eps", [1e-8, 0.0, 1e-30])
+def test_entries_of_every_size(bits, eps):
+    """Gradients of 1e-30 to 1e18, zeros among them: roots and quotients near
+    the ends of fp32's range and away from it round the same way."""
+    c = Case([4096, 300], "f32", "f32", bits, hp=z.Hparams(max_norm=0.0, eps=eps))
+    for turn in range(4):
+        for g in c.grads:
+            n = g.numel()
+            size = torch.exp(math.log(10) * (48 * torch.rand(n, generator=c.gen, device="cuda") - 30))
+            g.copy_(torch.randn(n, generator=c.gen, device="cuda") * size)
+            g[torch.rand(n, generator=c.gen, device="cuda") < 0.1] = 0.0
+            if turn % 2 == 0:    # rows of one size, as real ones are
+                g[:n // 2] = torch.randn(n // 2, generator=c.gen, device="cuda") * 10.0 ** (turn * 9 - 25)
+        want = c.plain()
+        c.run()
+        fine = want["w"].isfinite()          # 0 / 0 without eps is NaN on both sides
+        assert torch.equal(c.flat(c.params)[fine], (want["w"] * c.mask)[fine])
+        assert torch.equal(c.flat(c.params).isnan(), (want["w"].isnan() & c.mask))
+        for p in c.params:
+            p.nan_to_num_(0.0)
+        if bits == 32:
+            assert torch.equal(c.m[c.mask], want["m"][c.mask]) and torch.equal(c.v[c.mask], want["v"][c.mask])
+        else:
+            assert torch.equal(c.m.long()[c.mask] & 127, want["km"][c.mask] & 127)
+            assert torch.equal(c.v.long()[c.mask], want["kr"][c.mask])
+
+
 def test_zeros_and_blocks_below_the_least_scale():
     c = Case([512, 256], bits=8, hp=z.Hparams(max_norm=0.0))
     c.grads[0].zero_()

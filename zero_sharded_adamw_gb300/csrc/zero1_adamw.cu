@@ -99,6 +99,7 @@ struct NormParams {
     ListTables d;
     uint64_t block0, nblocks;
     uint32_t tensor0, before;   // partial sums of earlier launches of this step
+    float one;
     int last;
 };
 
@@ -113,9 +114,9 @@ struct UpdateParams {
     float2 *scales;
     uint64_t block0, nblocks;
     uint64_t seed;
-    float beta1, omb1, beta2, omb2, eps;
+    float beta1, omb1, beta2, omb2, eps, one;
     uint32_t tensor0, per_warp;   // blocks that a warp takes, one after another
-    int clipped, decay_first, last;
+    int clipped, decay_first, eps_easy, last;
 };
 
 constexpr uint32_t pack_block(uint32_t tensor, uint32_t count, bool decays) { return tensor | (count - 1) << 16 | (uint32_t)decays << 24; }
@@ -195,29 +196,63 @@ __device__ __forceinline__ void get8(uint32_t k[8], const uint8_t *p, uint32_t c
         for (int j = 0; j < 8; ++j) k[j] = entry_of<false>(j) < count ? p[entry_of<false>(j)] : 0u;
     }
 }
+// ... which are the top bytes of k.
+__device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
+}
 template <bool WHOLE>
-__device__ __forceinline__ void put8(uint8_t *p, const uint32_t k[8], uint32_t count)
+__device__ __forceinline__ void put8_top(uint8_t *p, const uint32_t k[8], uint32_t count)
 {
     if (WHOLE) {
         *reinterpret_cast<uint2 *>(p + entry_of<true>(0)) =
-            make_uint2(k[0] | k[1] << 8 | k[2] << 16 | k[3] << 24, k[4] | k[5] << 8 | k[6] << 16 | k[7] << 24);
+            make_uint2(top_bytes(k[0], k[1], k[2], k[3]), top_bytes(k[4], k[5], k[6], k[7]));
     } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if (entry_of<false>(j) < count) p[entry_of<false>(j)] = (uint8_t)k[j];
+            if (entry_of<false>(j) < count) p[entry_of<false>(j)] = (uint8_t)(k[j] >> 24);
     }
 }
+
+// Two fp32 numbers in one instruction, products and sums each rounded by
+// themselves: a paired product is contracted into the paired sum that takes
+// it, .rn or not, so sums are written as a + b * one with a `one` that only
+// the launch knows.
+struct Two {
+    unsigned long long v;
+};
+__device__ __forceinline__ Two two(float a, float b)
+{
+    Two r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void apart(Two x, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v)); }
+__device__ __forceinline__ Two mul(Two a, Two b)
+{
+    Two r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ Two fma(Two a, Two b, Two c)
+{
+    Two r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ Two add(Two a, Two b, Two one) { return fma(b, one, a); }
 
 // ------------------------------------------------------------------ codes
 
 // 32 well-mixed bits: two rounds of multiplication (by the first 32 bits of
 // the fractions of sqrt 2 and sqrt 3) and shifted exclusive or.
-__device__ __forceinline__ uint32_t mix(uint32_t x)
+__device__ __forceinline__ uint32_t mix_folded(uint32_t x)   // of x ^ (x >> 16)
 {
-    x = (x ^ (x >> 16)) * 0x6A09E667u;
+    x *= 0x6A09E667u;
     x = (x ^ (x >> 15)) * 0xBB67AE85u;
     return x ^ (x >> 16);
 }
+__device__ __forceinline__ uint32_t mix(uint32_t x) { return mix_folded(x ^ (x >> 16)); }
 // The key of a step's random bits; `high`: the upper half of an entry's place.
 __device__ __forceinline__ uint32_t key_of(uint64_t seed, unsigned long long t, uint32_t high)
 {
@@ -225,23 +260,73 @@ __device__ __forceinline__ uint32_t key_of(uint64_t seed, unsigned long long t, 
     return high ? mix(k + high) : k;
 }
 
-__device__ __forceinline__ float m_value(uint32_t k, float scale)
+// Correctly rounded square roots and quotients of two, without branches: from
+// the approximate (reciprocal) root or reciprocal by one Newton step, then the
+// exact remainder times the inverse added once (P. Markstein, "IA-64 and
+// elementary functions", 2000, chapters 8 and 9).  For v = 0 or in [2^-100,
+// 2^100], |m| = 0 or in [2^-60, 2^60] and d in [2^-50, 2^51], where nothing
+// leaves fp32's normal range.  Compared with the IEEE instructions: all
+// significands of two octaves at twelve exponents, and 1.7e10 quotients.
+__device__ __forceinline__ Two roots(float v0, float v1)
 {
-    const float q = __fmul_rn(__uint_as_float(((k & 127u) << 20) + (127u << 23)) - 1.f, scale);
-    return k & 128u ? -q : q;
+    float y0, y1;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y0) : "f"(v0));
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y1) : "f"(v1));
+    const float most = 1.152921504606846976e18f;   // 2^60, for v = 0
+    const Two v = two(v0, v1), y = two(fminf(y0, most), fminf(y1, most));
+    Two g = mul(v, y), h = mul(y, two(-.5f, -.5f));           // sqrt(v), -1/(2 sqrt(v))
+    const Two e = fma(g, h, two(.5f, .5f));
+    g = fma(g, e, g);
+    h = fma(h, e, h);
+    return fma(fma(g, g, mul(v, two(-1.f, -1.f))), h, g);
 }
-__device__ __forceinline__ float r_value(uint32_t k, float scale)
+__device__ __forceinline__ Two quotients(Two m, float d0, float d1)
 {
-    return __fmul_rn(__uint_as_float((k << 19) + (127u << 23)) - 1.f, scale);
+    float y0, y1;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y0) : "f"(d0));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y1) : "f"(d1));
+    Two y = two(y0, y1);
+    const Two d = mul(two(d0, d1), two(-1.f, -1.f));
+    y = fma(y, fma(d, y, two(1.f, 1.f)), y);
+    const Two q = mul(m, y);
+    return fma(fma(d, q, m), y, q);
 }
-// x / scale as a code of 4 octave bits and BITS fraction bits, rounded at random.
+constexpr float kMLow = 8.6736173798840355e-19f, kMHigh = 1.152921504606847e18f;     // 2^-60, 2^60
+constexpr float kVLow = 7.8886090522101181e-31f, kVHigh = 1.2676506002282294e30f;    // 2^-100, 2^100
+
+// f(k, b) - 1 of two codes; what their bytes stand for, times the scale.
+__device__ __forceinline__ Two units(uint32_t y0, uint32_t y1)
+{
+    return two(__uint_as_float(y0 + (127u << 23)) - 1.f, __uint_as_float(y1 + (127u << 23)) - 1.f);
+}
+__device__ __forceinline__ void m_values(float &a, float &b, uint32_t k0, uint32_t k1, float scale)
+{
+    apart(mul(units((k0 & 127u) << 20, (k1 & 127u) << 20), two(scale, scale)), a, b);
+    a = __uint_as_float(__float_as_uint(a) | (k0 & 128u) << 24);
+    b = __uint_as_float(__float_as_uint(b) | (k1 & 128u) << 24);
+}
+__device__ __forceinline__ Two r_values(uint32_t k0, uint32_t k1, float scale)
+{
+    return mul(units(k0 << 19, k1 << 19), two(scale, scale));
+}
+// y = |x| / scale + 1 (below 2^16) as a code of 4 octave bits and BITS
+// fraction bits, rounded at random, in the top bits of the result: the
+// largest y, 2^16 less one code, and a few of its last places more do not
+// carry, as a dither is 16 of them short of one code at least.
 template <int BITS>
-__device__ __forceinline__ uint32_t code_of(float x, float inv, uint32_t random16)
+__device__ __forceinline__ uint32_t code_top(float y, uint32_t random16)
 {
-    const int y = __float_as_int(__fadd_rn(__fmul_rn(x, inv), 1.f)) + (int)(random16 << (7 - BITS));
-    const int k = (y - (127 << 23)) >> (23 - BITS);
-    return (uint32_t)min(max(k, 0), (16 << BITS) - 1);
+    return (__float_as_uint(y) + (random16 << (7 - BITS)) - (127u << 23)) << (5 + BITS - 4);
 }
+__device__ __forceinline__ void most_of(float &most, float a, float b)   // NaN stays
+{
+    asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(most) : "f"(a), "f"(b));
+}
+__device__ __forceinline__ void least_of(float &least, float a, float b)
+{
+    asm("min.abs.f32 %0, %0, %1, %2;" : "+f"(least) : "f"(a), "f"(b));
+}
+
 // A block's scale and its inverse from the bits of its largest value; NaN
 // where that is not finite (its codes are then all zero, and stand for NaN).
 __device__ __forceinline__ bool scales_of(uint32_t largest, float top, float &scale, float &inv)
@@ -255,50 +340,19 @@ __device__ __forceinline__ bool scales_of(uint32_t largest, float top, float &sc
 
 // --------------------------------------------------------------- the norm
 
-// Two fp32 numbers in one instruction each, every one rounded by itself.
-struct Two {
-    unsigned long long v;
-};
-__device__ __forceinline__ Two two(float a, float b)
-{
-    Two r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void apart(Two x, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v)); }
-__device__ __forceinline__ Two add(Two a, Two b)
-{
-    Two r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ Two mul(Two a, Two b)
-{
-    Two r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ Two fma(Two a, Two b, Two c)
-{
-    Two r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
-
 // A sum of squares to twice fp32's precision.
 struct Squares {
     Two sum = two(0.f, 0.f), rest = two(0.f, 0.f);
     // Squares of two entries with the error of each addition and, where a
     // square may have one (fp32 entries: bf16's squares have 16 bits), of each square.
     template <bool EXACT>
-    __device__ __forceinline__ void add2(Two g)
+    __device__ __forceinline__ void add2(Two g, Two one, Two minus)
     {
-        const Two minus = two(-1.f, -1.f);
-        const Two p = mul(g, g), s = add(sum, p);
+        const Two p = mul(g, g), s = add(sum, p, one);
         const Two back = fma(sum, minus, s);                              // s - sum
-        Two lost = add(fma(fma(back, minus, s), minus, sum), fma(back, minus, p));
-        if (!EXACT) lost = add(lost, fma(g, g, mul(p, minus)));
-        rest = add(rest, lost);
+        Two lost = add(fma(fma(back, minus, s), minus, sum), fma(back, minus, p), one);
+        if (!EXACT) lost = add(lost, fma(g, g, mul(p, minus)), one);
+        rest = add(rest, lost, one);
         sum = s;
     }
     __device__ __forceinline__ float size() const
@@ -381,6 +435,7 @@ __global__ void __launch_bounds__(kListThreads, 4) zero1_adamw_norm_kernel(const
     constexpr bool kExact = sizeof(G) == 2;
     ptx::launch_dependents();
     Squares ss;
+    const Two one = two(p.one, p.one), minus = two(-p.one, -p.one);
     uint32_t any = 0;
     for_grads<G, CAP>(p, [&](const G *const src[kNormBlocks], const uint32_t count[kNormBlocks]) {
         bool all = true;
@@ -402,9 +457,9 @@ __global__ void __launch_bounds__(kListThreads, 4) zero1_adamw_norm_kernel(const
                     for (int k = 0; k < 4; ++k) {
                         any |= w[k];
                         if (kExact)
-                            ss.add2<kExact>(two(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u)));
+                            ss.add2<kExact>(two(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u)), one, minus);
                         else if (k % 2 == 0)
-                            ss.add2<kExact>(two(__uint_as_float(w[k]), __uint_as_float(w[k + 1])));
+                            ss.add2<kExact>(two(__uint_as_float(w[k]), __uint_as_float(w[k + 1])), one, minus);
                     }
                 }
         } else {
@@ -415,7 +470,7 @@ __global__ void __launch_bounds__(kListThreads, 4) zero1_adamw_norm_kernel(const
 #pragma unroll
                 for (int k = 0; k < 8; k += 2) {
                     any |= __float_as_uint(g[k]) | __float_as_uint(g[k + 1]);
-                    ss.add2<kExact>(two(g[k], g[k + 1]));
+                    ss.add2<kExact>(two(g[k], g[k + 1]), one, minus);
                 }
             }
         }
@@ -484,27 +539,51 @@ __device__ __forceinline__ void update_block(const UpdateParams<CAP> &p, const G
         get8<WHOLE>(km, static_cast<const uint8_t *>(p.m) + flat, count);
         get8<WHOLE>(kr, static_cast<const uint8_t *>(p.v) + flat, count);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            m[j] = m_value(km[j], s.x);
-            const float root = r_value(kr[j], s.y);
-            v[j] = __fmul_rn(root, root);
+        for (int j = 0; j < 8; j += 2) {
+            m_values(m[j], m[j + 1], km[j], km[j + 1], s.x);
+            const Two root = r_values(kr[j], kr[j + 1], s.y);
+            apart(mul(root, root), v[j], v[j + 1]);
         }
     }
-    uint32_t most_m = 0, most_r = 0;
+    // (past the block's count all are zero: they change neither maximum)
+    const Two one = two(p.one, p.one);
+    const float before = decays && p.decay_first ? decay : 1.f, after = decays && !p.decay_first ? decay : 1.f;
+    float most_m = 0.f, most_v = 0.f, least_m = kMHigh, least_v = kVHigh;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float c = __fmul_rn(g[j], clip);
-        m[j] = __fadd_rn(__fmul_rn(p.beta1, m[j]), __fmul_rn(p.omb1, c));
-        v[j] = __fadd_rn(__fmul_rn(p.beta2, v[j]), __fmul_rn(__fmul_rn(p.omb2, c), c));
-        r[j] = __fsqrt_rn(v[j]);
-        const float u = __fmul_rn(step_size, __fdiv_rn(m[j], __fadd_rn(r[j], p.eps)));
-        if (p.decay_first && decays) w[j] = __fmul_rn(w[j], decay);
-        w[j] = __fadd_rn(w[j], -u);
-        if (!p.decay_first && decays) w[j] = __fmul_rn(w[j], decay);
-        if (BITS == 8 && (WHOLE || entry_of<WHOLE>(j) < count)) {
-            most_m = max(most_m, __float_as_uint(m[j]) & 0x7FFFFFFFu);
-            most_r = max(most_r, __float_as_uint(r[j]) & 0x7FFFFFFFu);
+    for (int j = 0; j < 8; j += 2) {
+        const Two c = mul(two(g[j], g[j + 1]), two(clip, clip));
+        apart(add(mul(two(p.beta1, p.beta1), two(m[j], m[j + 1])), mul(two(p.omb1, p.omb1), c), one), m[j], m[j + 1]);
+        apart(add(mul(two(p.beta2, p.beta2), two(v[j], v[j + 1])), mul(mul(two(p.omb2, p.omb2), c), c), one), v[j], v[j + 1]);
+        most_of(most_m, m[j], m[j + 1]);
+        most_of(most_v, v[j], v[j + 1]);
+        least_of(least_m, m[j], m[j + 1]);
+        least_of(least_v, v[j], v[j + 1]);
+    }
+    // zeros throughout (a row without gradients), or nothing near the ends of fp32's range
+    const bool zeros = most_m == 0.f && most_v == 0.f;
+    const bool easy = p.eps_easy && (zeros || (least_m >= kMLow && most_m <= kMHigh && least_v >= kVLow && most_v <= kVHigh));
+    float q[8];
+    if (easy) {
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            const Two root = roots(v[j], v[j + 1]);
+            apart(root, r[j], r[j + 1]);
+            float d0, d1;
+            apart(add(root, two(p.eps, p.eps), one), d0, d1);
+            apart(quotients(two(m[j], m[j + 1]), d0, d1), q[j], q[j + 1]);
         }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            r[j] = __fsqrt_rn(v[j]);
+            q[j] = __fdiv_rn(m[j], __fadd_rn(r[j], p.eps));
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+        const Two less = mul(two(-step_size, -step_size), two(q[j], q[j + 1]));
+        const Two x = add(mul(two(w[j], w[j + 1]), two(before, before)), less, one);
+        apart(mul(x, two(after, after)), w[j], w[j + 1]);
     }
     put8<WHOLE>(param, w, count);
     if constexpr (kMaster) put8<WHOLE>(p.master + flat, w, count);
@@ -512,30 +591,50 @@ __device__ __forceinline__ void update_block(const UpdateParams<CAP> &p, const G
         put8<WHOLE>(static_cast<float *>(p.m) + flat, m, count);
         put8<WHOLE>(static_cast<float *>(p.v) + flat, v, count);
     } else {
-        most_m = __reduce_max_sync(~0u, most_m);
-        most_r = __reduce_max_sync(~0u, most_r);
         float2 s;
         float inv_m, inv_r;
-        const bool held_m = scales_of(most_m, kMTop, s.x, inv_m), held_r = scales_of(most_r, kRTop, s.y, inv_r);
-        const uint32_t key = key_of(p.seed, t, (uint32_t)(flat >> 32));
+        const bool held_m = scales_of(__reduce_max_sync(~0u, __float_as_uint(most_m)), kMTop, s.x, inv_m);
+        // the largest root is the root of the largest: a correctly rounded root does not decrease
+        const float most_r = __fsqrt_rn(__uint_as_float(__reduce_max_sync(~0u, __float_as_uint(most_v))));
+        const bool held_r = scales_of(__float_as_uint(most_r), kRTop, s.y, inv_r);
+        // an entry's place differs from its lane's first in bits below 16 only, so their first folding is shared
+        const uint32_t first = ((uint32_t)flat + entry_of<WHOLE>(0)) ^ key_of(p.seed, t, (uint32_t)(flat >> 32));
+        const uint32_t folded = first ^ (first >> 16);
         uint32_t km[8], kr[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t random = mix(((uint32_t)flat + entry_of<WHOLE>(j)) ^ key);
-            km[j] = held_m ? code_of<3>(fabsf(m[j]), inv_m, random & 0xFFFFu) : 0u;
-            if (m[j] < 0.f) km[j] |= 128u;
-            kr[j] = code_of<4>(r[j], inv_r, random >> 16);
-            if (kr[j] == 0 && r[j] > 0.f) kr[j] = 1u;
-            if (!held_r) kr[j] = 0u;
+        for (int j = 0; j < 8; j += 2) {
+            float a[2], b[2];
+            apart(mul(two(m[j], m[j + 1]), two(inv_m, inv_m)), a[0], a[1]);
+            apart(add(mul(two(r[j], r[j + 1]), two(inv_r, inv_r)), one, one), b[0], b[1]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t random = mix_folded(folded ^ (WHOLE ? j + i : (j + i) * 32));
+                km[j + i] = code_top<3>(__fadd_rn(fabsf(a[i]), 1.f), random & 0xFFFFu);
+                kr[j + i] = code_top<4>(b[i], random >> 16);
+            }
         }
-        put8<WHOLE>(static_cast<uint8_t *>(p.m) + flat, km, count);
-        put8<WHOLE>(static_cast<uint8_t *>(p.v) + flat, kr, count);
+        // a block of zeros has inverse 0 and codes 0 by itself; one that is not finite is held as codes 0
+        if (!held_m) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) km[j] = 0;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            km[j] = (km[j] & 0x7FFFFFFFu) | (__float_as_uint(m[j]) & 0x80000000u);
+            kr[j] = max(kr[j], min(__float_as_uint(r[j]), 1u) << 24);   // sqrt(v) > 0 never becomes 0
+        }
+        if (!held_r) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) kr[j] = 0;
+        }
+        put8_top<WHOLE>(static_cast<uint8_t *>(p.m) + flat, km, count);
+        put8_top<WHOLE>(static_cast<uint8_t *>(p.v) + flat, kr, count);
         if ((threadIdx.x & 31) == 0) p.scales[block] = s;
     }
 }
 
 template <typename P, typename G, int BITS, int CAP>
-__global__ void __launch_bounds__(kListThreads) zero1_adamw_update_kernel(const __grid_constant__ UpdateParams<CAP> p)
+__global__ void __launch_bounds__(kListThreads, 4) zero1_adamw_update_kernel(const __grid_constant__ UpdateParams<CAP> p)
 {
     const ListStatus *status = p.d.status;
     const float step_size = status->step_size, decay = status->decay;
@@ -584,15 +683,15 @@ __global__ void __launch_bounds__(kListThreads) zero1_adamw_moments_kernel(ListT
         if (m_out) {
             get8<WHOLE>(k, m + flat, count);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = m_value(k[j], s.x);
+            for (int j = 0; j < 8; j += 2) m_values(x[j], x[j + 1], k[j], k[j + 1], s.x);
             put8<WHOLE>(m_out + flat, x, count);
         }
         if (v_out) {
             get8<WHOLE>(k, v + flat, count);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                x[j] = r_value(k[j], s.y);
-                x[j] = __fmul_rn(x[j], x[j]);
+            for (int j = 0; j < 8; j += 2) {
+                const Two root = r_values(k[j], k[j + 1], s.y);
+                apart(mul(root, root), x[j], x[j + 1]);
             }
             put8<WHOLE>(v_out + flat, x, count);
         }
@@ -866,6 +965,7 @@ cudaError_t norm_t(const zero1_adamw_ctx *h, const StepCall &c, uint64_t i0, uin
     p.nblocks = h->first[i1] - h->first[i0];
     p.tensor0 = (uint32_t)i0;
     p.before = before;
+    p.one = 1.f;
     p.last = i1 == h->sizes.size();
     uint32_t grid = norm_grid(p.nblocks, h->num_sms);
     if (grid == 0) {
@@ -895,9 +995,11 @@ cudaError_t update_t(const zero1_adamw_ctx *h, const StepCall &c, uint64_t i0, u
     p.beta2 = (float)h->hp.beta2;
     p.omb2 = (float)(1.0 - h->hp.beta2);
     p.eps = (float)h->hp.eps;
+    p.one = 1.f;
     p.tensor0 = (uint32_t)i0;
     p.clipped = h->hp.max_norm > 0.0;
     p.decay_first = h->opt.decay_before_update;
+    p.eps_easy = p.eps >= 0x1p-50f && p.eps <= 0x1p50f;   // so that sqrt(v) + eps is never near the ends of fp32's range
     p.last = i1 == h->sizes.size();
     p.per_warp = p.nblocks < 16ull * zero1::kWarps * (uint64_t)h->num_sms ? 1 : zero1::kUpdateBlocks;
     const uint64_t per = (uint64_t)zero1::kWarps * p.per_warp;

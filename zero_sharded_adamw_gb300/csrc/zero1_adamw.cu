@@ -33,6 +33,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <cstring>
 #include <exception>
 #include <memory>
 #include <mutex>
@@ -51,7 +52,8 @@ namespace {
 constexpr uint32_t kListBlock = 256;      // entries of one block: 8 a lane of one warp
 constexpr int kListThreads = 256;
 constexpr uint32_t kWarps = kListThreads / 32;
-constexpr uint32_t kUpdateBlocks = 4;     // blocks of a warp of the update
+constexpr uint32_t kUpdateBlocks = 4;     // blocks of a warp of the update, fp32 moments (they are unrolled)
+constexpr uint32_t kStagedBlocks = 8;     // ... with 8 bits (16: 374 us in place of 366, 32: 392, all at once: 417)
 constexpr uint32_t kNormBlocks = 4;       // ... of the norm, at a time
 constexpr float kMTop = 61439.f, kRTop = 63487.f;       // f(127, 3) - 1, f(255, 4) - 1
 constexpr uint32_t kHeldLow = 27u << 23;                // 2^-100: a block whose largest value is smaller is all zeros
@@ -92,6 +94,13 @@ __global__ void zero1_adamw_set_kernel(ListTables d, unsigned long long t, doubl
     form_scalars(d, d.status->t, d.status->lr);
 }
 
+// Two fp32 numbers in one instruction, products and sums each rounded by
+// themselves: a paired product is contracted into the paired sum that takes
+// it, .rn or not, so sums are written as a + b * one with a `one` that only
+// the launch knows.
+struct Two {
+    unsigned long long v;
+};
 template <int CAP>
 struct NormParams {
     const void *grads[CAP];
@@ -114,7 +123,8 @@ struct UpdateParams {
     float2 *scales;
     uint64_t block0, nblocks;
     uint64_t seed;
-    float beta1, omb1, beta2, omb2, eps, one;
+    Two beta1, omb1, beta2, omb2, eps2, one;   // each twice
+    float eps;
     uint32_t tensor0, per_warp;   // blocks that a warp takes, one after another
     int clipped, decay_first, eps_easy, last;
 };
@@ -214,13 +224,6 @@ __device__ __forceinline__ void put8_top(uint8_t *p, const uint32_t k[8], uint32
     }
 }
 
-// Two fp32 numbers in one instruction, products and sums each rounded by
-// themselves: a paired product is contracted into the paired sum that takes
-// it, .rn or not, so sums are written as a + b * one with a `one` that only
-// the launch knows.
-struct Two {
-    unsigned long long v;
-};
 __device__ __forceinline__ Two two(float a, float b)
 {
     Two r;
@@ -308,6 +311,15 @@ __device__ __forceinline__ void m_values(float &a, float &b, uint32_t k0, uint32
 __device__ __forceinline__ Two r_values(uint32_t k0, uint32_t k1, float scale)
 {
     return mul(units(k0 << 19, k1 << 19), two(scale, scale));
+}
+__device__ __forceinline__ void decode8(float m[8], float v[8], const uint32_t km[8], const uint32_t kr[8], float2 s)
+{
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+        m_values(m[j], m[j + 1], km[j], km[j + 1], s.x);
+        const Two root = r_values(kr[j], kr[j + 1], s.y);
+        apart(mul(root, root), v[j], v[j + 1]);
+    }
 }
 // y = |x| / scale + 1 (below 2^16) as a code of 4 octave bits and BITS
 // fraction bits, rounded at random, in the top bits of the result: the
@@ -517,43 +529,48 @@ __global__ void __launch_bounds__(kListThreads, 4) zero1_adamw_norm_kernel(const
 
 // -------------------------------------------------------------- the update
 
-// One block by one warp.
+// What a lane reads of a block.
+template <int BITS>
+struct Read {
+    float g[8], w[8], m[8], v[8];
+};
 template <typename P, typename G, int BITS, bool WHOLE, int CAP>
-__device__ __forceinline__ void update_block(const UpdateParams<CAP> &p, const G *grad, P *param, uint32_t count, bool decays,
+__device__ __forceinline__ void read_block(Read<BITS> &x, const UpdateParams<CAP> &p, const G *grad, const P *param,
+                                           uint32_t count, uint64_t block)
+{
+    const uint64_t flat = block * kListBlock;
+    get8<WHOLE>(x.g, grad, count);
+    if constexpr (sizeof(P) == 2)
+        get8<WHOLE>(x.w, p.master + flat, count);
+    else
+        get8<WHOLE>(x.w, param, count);
+    if constexpr (BITS == 32) {
+        get8<WHOLE>(x.m, static_cast<const float *>(p.m) + flat, count);
+        get8<WHOLE>(x.v, static_cast<const float *>(p.v) + flat, count);
+    } else {
+        uint32_t km[8], kr[8];
+        get8<WHOLE>(km, static_cast<const uint8_t *>(p.m) + flat, count);
+        get8<WHOLE>(kr, static_cast<const uint8_t *>(p.v) + flat, count);
+        decode8(x.m, x.v, km, kr, p.scales[block]);
+    }
+}
+
+// One block by one warp.
+template <typename P, int BITS, bool WHOLE, int CAP>
+__device__ __forceinline__ void update_block(Read<BITS> &x, const UpdateParams<CAP> &p, P *param, uint32_t count, bool decays,
                                              uint64_t block, float clip, float step_size, float decay, unsigned long long t)
 {
     const uint64_t flat = block * kListBlock;
     constexpr bool kMaster = sizeof(P) == 2;
-    float g[8], w[8], m[8], v[8], r[8];
-    get8<WHOLE>(g, grad, count);
-    if constexpr (kMaster)
-        get8<WHOLE>(w, p.master + flat, count);
-    else
-        get8<WHOLE>(w, param, count);
-    if constexpr (BITS == 32) {
-        get8<WHOLE>(m, static_cast<const float *>(p.m) + flat, count);
-        get8<WHOLE>(v, static_cast<const float *>(p.v) + flat, count);
-    } else {
-        const float2 s = p.scales[block];
-        uint32_t km[8], kr[8];
-        get8<WHOLE>(km, static_cast<const uint8_t *>(p.m) + flat, count);
-        get8<WHOLE>(kr, static_cast<const uint8_t *>(p.v) + flat, count);
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-            m_values(m[j], m[j + 1], km[j], km[j + 1], s.x);
-            const Two root = r_values(kr[j], kr[j + 1], s.y);
-            apart(mul(root, root), v[j], v[j + 1]);
-        }
-    }
+    float(&g)[8] = x.g, (&w)[8] = x.w, (&m)[8] = x.m, (&v)[8] = x.v, r[8];
     // (past the block's count all are zero: they change neither maximum)
-    const Two one = two(p.one, p.one);
     const float before = decays && p.decay_first ? decay : 1.f, after = decays && !p.decay_first ? decay : 1.f;
     float most_m = 0.f, most_v = 0.f, least_m = kMHigh, least_v = kVHigh;
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
         const Two c = mul(two(g[j], g[j + 1]), two(clip, clip));
-        apart(add(mul(two(p.beta1, p.beta1), two(m[j], m[j + 1])), mul(two(p.omb1, p.omb1), c), one), m[j], m[j + 1]);
-        apart(add(mul(two(p.beta2, p.beta2), two(v[j], v[j + 1])), mul(mul(two(p.omb2, p.omb2), c), c), one), v[j], v[j + 1]);
+        apart(add(mul(p.beta1, two(m[j], m[j + 1])), mul(p.omb1, c), p.one), m[j], m[j + 1]);
+        apart(add(mul(p.beta2, two(v[j], v[j + 1])), mul(mul(p.omb2, c), c), p.one), v[j], v[j + 1]);
         most_of(most_m, m[j], m[j + 1]);
         most_of(most_v, v[j], v[j + 1]);
         least_of(least_m, m[j], m[j + 1]);
@@ -569,7 +586,7 @@ __device__ __forceinline__ void update_block(const UpdateParams<CAP> &p, const G
             const Two root = roots(v[j], v[j + 1]);
             apart(root, r[j], r[j + 1]);
             float d0, d1;
-            apart(add(root, two(p.eps, p.eps), one), d0, d1);
+            apart(add(root, p.eps2, p.one), d0, d1);
             apart(quotients(two(m[j], m[j + 1]), d0, d1), q[j], q[j + 1]);
         }
     } else {
@@ -582,8 +599,8 @@ __device__ __forceinline__ void update_block(const UpdateParams<CAP> &p, const G
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
         const Two less = mul(two(-step_size, -step_size), two(q[j], q[j + 1]));
-        const Two x = add(mul(two(w[j], w[j + 1]), two(before, before)), less, one);
-        apart(mul(x, two(after, after)), w[j], w[j + 1]);
+        const Two moved = add(mul(two(w[j], w[j + 1]), two(before, before)), less, p.one);
+        apart(mul(moved, two(after, after)), w[j], w[j + 1]);
     }
     put8<WHOLE>(param, w, count);
     if constexpr (kMaster) put8<WHOLE>(p.master + flat, w, count);
@@ -605,7 +622,7 @@ __device__ __forceinline__ void update_block(const UpdateParams<CAP> &p, const G
         for (int j = 0; j < 8; j += 2) {
             float a[2], b[2];
             apart(mul(two(m[j], m[j + 1]), two(inv_m, inv_m)), a[0], a[1]);
-            apart(add(mul(two(r[j], r[j + 1]), two(inv_r, inv_r)), one, one), b[0], b[1]);
+            apart(add(mul(two(r[j], r[j + 1]), two(inv_r, inv_r)), p.one, p.one), b[0], b[1]);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const uint32_t random = mix_folded(folded ^ (WHOLE ? j + i : (j + i) * 32));
@@ -633,31 +650,153 @@ __device__ __forceinline__ void update_block(const UpdateParams<CAP> &p, const G
     }
 }
 
+// Where a block's tensors are.
+template <typename P, typename G>
+struct Place {
+    const G *grad;
+    P *param;
+    uint32_t count;
+    bool decays;
+    __device__ __forceinline__ bool whole() const { return count == kListBlock && whole16(grad) && whole16(param); }
+};
+template <typename P, typename G, int CAP>
+__device__ __forceinline__ Place<P, G> place_of(const UpdateParams<CAP> &p, uint32_t word, uint64_t block)
+{
+    const uint32_t i = tensor_of(word) - p.tensor0;
+    const uint64_t at = (uint64_t)((uint32_t)block - p.first[i]) * kListBlock;
+    return {static_cast<const G *>(p.grads[i]) + at, static_cast<P *>(p.params[i]) + at, count_of(word), decays_of(word)};
+}
+
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async8(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// A lane's part of a block on its way through shared memory (8-bit moments):
+// every lane reads what it copied itself, so no barrier is needed.
+template <typename P, typename G>
+struct Staged {
+    static constexpr uint32_t kGrad = 8 * sizeof(G) / 16, kBytes = 32 * (8 * sizeof(G) + 32 + 16);
+    static __device__ __forceinline__ void copy(uint32_t at, const G *grad, const float *master, const void *m, const void *v, uint64_t flat)
+    {
+        const uint32_t lane = threadIdx.x & 31;
+#pragma unroll
+        for (uint32_t q = 0; q < kGrad; ++q) copy_async16(at + (q * 32 + lane) * 16, reinterpret_cast<const uint4 *>(grad) + lane * kGrad + q);
+        at += kGrad * 512;
+#pragma unroll
+        for (uint32_t q = 0; q < 2; ++q) copy_async16(at + (q * 32 + lane) * 16, reinterpret_cast<const uint4 *>(master) + lane * 2 + q);
+        at += 1024;
+        copy_async8(at + lane * 8, static_cast<const uint8_t *>(m) + flat + lane * 8);
+        copy_async8(at + 256 + lane * 8, static_cast<const uint8_t *>(v) + flat + lane * 8);
+    }
+    static __device__ __forceinline__ uint4 ld16(uint32_t at)
+    {
+        uint4 v;
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+        return v;
+    }
+    static __device__ __forceinline__ void floats(float v[8], uint4 a, uint4 b)
+    {
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(w[j]);
+    }
+    static __device__ __forceinline__ void read(Read<8> &x, uint32_t at, float2 scale)
+    {
+        const uint32_t lane = threadIdx.x & 31;
+        if constexpr (kGrad == 1)
+            ptx::set_widened(x.g, ld16(at + lane * 16));
+        else
+            floats(x.g, ld16(at + lane * 16), ld16(at + 512 + lane * 16));
+        at += kGrad * 512;
+        floats(x.w, ld16(at + lane * 16), ld16(at + 512 + lane * 16));
+        at += 1024;
+        uint32_t km[8], kr[8], a, b, c, d;
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(at + lane * 8) : "memory");
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(c), "=r"(d) : "r"(at + 256 + lane * 8) : "memory");
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            km[j] = ((j < 4 ? a : b) >> (8 * (j & 3))) & 0xFFu;
+            kr[j] = ((j < 4 ? c : d) >> (8 * (j & 3))) & 0xFFu;
+        }
+        decode8(x.m, x.v, km, kr, scale);
+    }
+};
+
+// Bound by HBM with fp32 moments; with 8-bit ones a block's arithmetic takes
+// as long as its 2 KB, so the next block's are copied meanwhile.
 template <typename P, typename G, int BITS, int CAP>
 __global__ void __launch_bounds__(kListThreads, 4) zero1_adamw_update_kernel(const __grid_constant__ UpdateParams<CAP> p)
 {
     const ListStatus *status = p.d.status;
     const float step_size = status->step_size, decay = status->decay;
     const unsigned long long t = status->t + 1;
-    const uint64_t b0 = (uint64_t)blockIdx.x * kWarps * p.per_warp + (threadIdx.x >> 5);
-    uint32_t word[kUpdateBlocks];
+    if constexpr (BITS == 8) {
+        extern __shared__ __align__(16) unsigned char raw[];
+        using S = Staged<P, G>;
+        const uint32_t mine = ptx::smem_u32(raw) + (threadIdx.x >> 5) * 2 * S::kBytes;
+        const uint64_t stride = (uint64_t)gridDim.x * kWarps;
+        uint64_t b = (uint64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+        const uint32_t *words = p.d.blocks + p.block0;
+        uint32_t word = b < p.nblocks ? __ldg(words + b) : 0u, next = b + stride < p.nblocks ? __ldg(words + b + stride) : 0u;
+        float2 scale = make_float2(0.f, 0.f), next_scale = scale;
+        const auto copy = [&](uint64_t which, uint32_t w, uint32_t buffer, float2 &s) {
+            if (which < p.nblocks) {
+                const uint64_t block = p.block0 + which;
+                const Place<P, G> at = place_of<P, G, CAP>(p, w, block);
+                s = p.scales[block];
+                if (at.whole())
+                    S::copy(mine + buffer * S::kBytes, at.grad, sizeof(P) == 2 ? p.master + block * kListBlock : reinterpret_cast<const float *>(at.param),
+                            p.m, p.v, block * kListBlock);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        copy(b, word, 0, scale);       // none of this is the norm's
+        ptx::grid_dependency_wait();   // for the norm
+        const float clip = p.clipped ? __ldcg(&status->clip) : 1.f;
+#pragma unroll 1
+        for (uint32_t i = 0; b < p.nblocks; ++i, b += stride) {
+            const uint32_t after = b + 2 * stride < p.nblocks ? __ldg(words + b + 2 * stride) : 0u;
+            copy(b + stride, next, (i + 1) & 1, next_scale);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            const uint64_t block = p.block0 + b;
+            const Place<P, G> at = place_of<P, G, CAP>(p, word, block);
+            Read<BITS> x;
+            if (at.whole()) {
+                S::read(x, mine + (i & 1) * S::kBytes, scale);
+                update_block<P, BITS, true, CAP>(x, p, at.param, kListBlock, at.decays, block, clip, step_size, decay, t);
+            } else {
+                read_block<P, G, BITS, false, CAP>(x, p, at.grad, at.param, at.count, block);
+                update_block<P, BITS, false, CAP>(x, p, at.param, at.count, at.decays, block, clip, step_size, decay, t);
+            }
+            word = next, next = after, scale = next_scale;
+        }
+    } else {
+        const uint64_t b0 = (uint64_t)blockIdx.x * kWarps * p.per_warp + (threadIdx.x >> 5);
+        uint32_t word[kUpdateBlocks];
 #pragma unroll
-    for (uint32_t u = 0; u < kUpdateBlocks; ++u)
-        word[u] = u < p.per_warp && b0 + u * kWarps < p.nblocks ? __ldg(p.d.blocks + p.block0 + b0 + u * kWarps) : 0u;
-    ptx::grid_dependency_wait();   // for the norm
-    const float clip = p.clipped ? __ldcg(&status->clip) : 1.f;
+        for (uint32_t u = 0; u < kUpdateBlocks; ++u)
+            word[u] = u < p.per_warp && b0 + u * kWarps < p.nblocks ? __ldg(p.d.blocks + p.block0 + b0 + u * kWarps) : 0u;
+        ptx::grid_dependency_wait();   // for the norm
+        const float clip = p.clipped ? __ldcg(&status->clip) : 1.f;
 #pragma unroll
-    for (uint32_t u = 0; u < kUpdateBlocks; ++u) {
-        if (u >= p.per_warp || b0 + u * kWarps >= p.nblocks) break;
-        const uint64_t block = p.block0 + b0 + u * kWarps;
-        const uint32_t i = tensor_of(word[u]) - p.tensor0, count = count_of(word[u]);
-        const uint64_t at = (uint64_t)((uint32_t)block - p.first[i]) * kListBlock;
-        const G *grad = static_cast<const G *>(p.grads[i]) + at;
-        P *param = static_cast<P *>(p.params[i]) + at;
-        if (count == kListBlock && whole16(grad) && whole16(param))
-            update_block<P, G, BITS, true, CAP>(p, grad, param, kListBlock, decays_of(word[u]), block, clip, step_size, decay, t);
-        else
-            update_block<P, G, BITS, false, CAP>(p, grad, param, count, decays_of(word[u]), block, clip, step_size, decay, t);
+        for (uint32_t u = 0; u < kUpdateBlocks; ++u) {
+            if (u >= p.per_warp || b0 + u * kWarps >= p.nblocks) break;
+            const uint64_t block = p.block0 + b0 + u * kWarps;
+            const Place<P, G> at = place_of<P, G, CAP>(p, word[u], block);
+            Read<BITS> x;
+            if (at.whole()) {
+                read_block<P, G, BITS, true, CAP>(x, p, at.grad, at.param, kListBlock, block);
+                update_block<P, BITS, true, CAP>(x, p, at.param, kListBlock, at.decays, block, clip, step_size, decay, t);
+            } else {
+                read_block<P, G, BITS, false, CAP>(x, p, at.grad, at.param, at.count, block);
+                update_block<P, BITS, false, CAP>(x, p, at.param, at.count, at.decays, block, clip, step_size, decay, t);
+            }
+        }
     }
     __syncthreads();   // every warp has read the scalars
     if (last_block(&p.d.status->ticket[1]) && p.last && threadIdx.x == 0) {
@@ -990,12 +1129,19 @@ cudaError_t update_t(const zero1_adamw_ctx *h, const StepCall &c, uint64_t i0, u
     p.block0 = h->first[i0];
     p.nblocks = h->first[i1] - h->first[i0];
     p.seed = h->opt.seed;
-    p.beta1 = (float)h->hp.beta1;
-    p.omb1 = (float)(1.0 - h->hp.beta1);
-    p.beta2 = (float)h->hp.beta2;
-    p.omb2 = (float)(1.0 - h->hp.beta2);
+    const auto twice = [](double v) {
+        const float f = (float)v;
+        uint32_t bits;
+        std::memcpy(&bits, &f, sizeof bits);
+        return zero1::Two{(unsigned long long)bits << 32 | bits};
+    };
+    p.beta1 = twice(h->hp.beta1);
+    p.omb1 = twice(1.0 - h->hp.beta1);
+    p.beta2 = twice(h->hp.beta2);
+    p.omb2 = twice(1.0 - h->hp.beta2);
+    p.eps2 = twice(h->hp.eps);
+    p.one = twice(1.0);
     p.eps = (float)h->hp.eps;
-    p.one = 1.f;
     p.tensor0 = (uint32_t)i0;
     p.clipped = h->hp.max_norm > 0.0;
     p.decay_first = h->opt.decay_before_update;
@@ -1004,13 +1150,19 @@ cudaError_t update_t(const zero1_adamw_ctx *h, const StepCall &c, uint64_t i0, u
     p.per_warp = p.nblocks < 16ull * zero1::kWarps * (uint64_t)h->num_sms ? 1 : zero1::kUpdateBlocks;
     const uint64_t per = (uint64_t)zero1::kWarps * p.per_warp;
     uint64_t grid = (p.nblocks + per - 1) / per;
+    uint32_t smem = 0;
+    if (BITS == 8) {
+        smem = zero1::kWarps * 2 * zero1::Staged<P, G>::kBytes;   // 32 or 40 KB
+        p.per_warp = p.nblocks < 64ull * zero1::kWarps * (uint64_t)h->num_sms ? 1 : zero1::kStagedBlocks;
+        grid = (p.nblocks + zero1::kWarps * p.per_warp - 1) / (zero1::kWarps * p.per_warp);
+    }
     if (grid == 0) {
         if (!p.last) return cudaSuccess;
         grid = 1;
     }
     const auto kernel = zero1::zero1_adamw_update_kernel<P, G, BITS, CAP>;
-    return p.clipped && i0 == 0 ? zero1::launch_early(kernel, dim3((unsigned)grid), zero1::kListThreads, 0, c.stream, p)
-                                : zero1::launch(kernel, dim3((unsigned)grid), zero1::kListThreads, 0, c.stream, p);
+    return p.clipped && i0 == 0 ? zero1::launch_early(kernel, dim3((unsigned)grid), zero1::kListThreads, smem, c.stream, p)
+                                : zero1::launch(kernel, dim3((unsigned)grid), zero1::kListThreads, smem, c.stream, p);
 }
 
 template <typename P, typename G, int BITS, int CAP>

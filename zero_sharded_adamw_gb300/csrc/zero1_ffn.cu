@@ -151,13 +151,28 @@ uint64_t workspace_of(const zero1_ffn_shape &s, bool backward)
 
 // ---------------------------------------------------------------- copies
 
-// Rows that start off a 16-byte boundary, copied to rows that start on one.
-__global__ void __launch_bounds__(256) zero1_ffn_copy_kernel(const uint16_t *src, uint64_t ld, uint16_t *dst, uint64_t ld_to,
-                                                             uint64_t rows, uint32_t cols)
+// Matrices whose rows start off a 16-byte boundary, copied to rows that start
+// on one: all operands of a call in one launch, 8 entries a thread.
+constexpr int kMostCopies = 6;
+struct CopyParams {
+    const uint16_t *src[kMostCopies];
+    uint4 *dst[kMostCopies];
+    uint64_t ld[kMostCopies], pieces[kMostCopies];   // pieces: of 8 entries, rows times those of a row
+    uint32_t cols[kMostCopies], row_pieces[kMostCopies];
+};
+__global__ void __launch_bounds__(256) zero1_ffn_copy_kernel(const __grid_constant__ CopyParams p)
 {
-    const uint32_t c = blockIdx.x * 256 + threadIdx.x;
-    if (c >= cols) return;
-    for (uint64_t r = blockIdx.y; r < rows; r += gridDim.y) dst[r * ld_to + c] = src[r * ld + c];
+    const int m = blockIdx.y;
+    const uint32_t per = p.row_pieces[m], cols = p.cols[m];
+    for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < p.pieces[m]; i += (uint64_t)gridDim.x * 256) {
+        const uint64_t r = i / per;
+        const uint32_t c = (uint32_t)(i - r * per) * 8;
+        const uint16_t *src = p.src[m] + r * p.ld[m] + c;
+        uint32_t w[8];
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k) w[k] = c + k < cols ? src[k] : 0u;
+        p.dst[m][i] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+    }
 }
 
 typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
@@ -184,6 +199,10 @@ struct Call {
     unsigned *errors;
     EncodeFn fn = nullptr;
     int rc = ZERO1_OK;
+    CopyParams copies{};
+    int count = 0;           // of them
+    uint64_t most = 0;       // pieces of the largest
+    bool launched = false;   // a kernel of this call
 
     Call(const zero1_ffn_shape &shape, void *workspace, unsigned *err, void *st)
         : s(shape), space(static_cast<unsigned char *>(workspace)), stream(static_cast<cudaStream_t>(st)), errors(err)
@@ -206,21 +225,31 @@ struct Call {
         at += round_up(bytes, 256);
         return here;
     }
-    // The matrix itself, or a copy that TMA can address.
+    // The matrix itself, or its copy that TMA can address (made by copy_all).
     Mat addressable(Mat m)
     {
         if (m.aligned()) return m;
         const uint64_t ld = round_up(m.cols, 8);
-        uint16_t *to = static_cast<uint16_t *>(take(copy_bytes(m.rows, m.cols)));
-        if (rc == ZERO1_OK) {
-            const dim3 grid((unsigned)((m.cols + 255) / 256), (unsigned)(m.rows < 8192 ? m.rows : 8192));
-            check(launch(zero1_ffn_copy_kernel, grid, 256, 0, stream, static_cast<const uint16_t *>(m.p), m.ld, to, ld, m.rows,
-                         (uint32_t)m.cols),
-                  "kernel launch");
-        }
+        void *to = take(copy_bytes(m.rows, m.cols));
+        copies.src[count] = static_cast<const uint16_t *>(m.p);
+        copies.dst[count] = static_cast<uint4 *>(to);
+        copies.ld[count] = m.ld;
+        copies.cols[count] = (uint32_t)m.cols;
+        copies.row_pieces[count] = (uint32_t)(ld / 8);
+        copies.pieces[count] = m.rows * (ld / 8);
+        if (copies.pieces[count] > most) most = copies.pieces[count];
+        ++count;
         m.p = to;
         m.ld = ld;
         return m;
+    }
+    void copy_all()
+    {
+        if (!count || rc != ZERO1_OK) return;
+        const uint64_t need = (most + 255) / 256, cap = 16ull * (uint64_t)sms;
+        check(launch(zero1_ffn_copy_kernel, dim3((unsigned)(need < cap ? need : cap), (unsigned)count), 256, 0, stream, copies),
+              "kernel launch");
+        launched = true;
     }
     // Boxes of 64 columns and `box_rows` rows; `planes` matrices `plane` entries apart.
     void map(CUtensorMap *to, const Mat &m, uint32_t box_rows = 64, uint64_t planes = 1, uint64_t plane = 0)
@@ -264,6 +293,16 @@ FfnParams params_of(const Call &c, uint64_t k, uint32_t segments)
     p.stall = c.s.inject_wait_timeout;
     p.errors = c.errors;
     return p;
+}
+
+// Launch a product of this call.
+template <typename F>
+void run(Call &c, FfnParams &p, F f)
+{
+    if (c.rc != ZERO1_OK) return;
+    p.follows = c.launched;
+    c.check(f(p), "kernel launch");
+    c.launched = true;
 }
 
 void slice(FfnParams &p, void *partials)
@@ -321,6 +360,7 @@ int zero1_ffn_forward(const zero1_ffn_shape *shape, const void *x, const void *w
     if (c.rc) return c.rc;
 
     const Mat ax = c.addressable(mats[0]), ag = c.addressable(mats[1]), au = c.addressable(mats[2]), ad = c.addressable(mats[3]);
+    c.copy_all();
     if (thin_rows(s, false)) {
         const uint32_t box = ffn_thin_box(s.rows);
         const uint64_t plane = copy_bytes(s.rows, s.hidden) / 2;
@@ -360,16 +400,22 @@ int zero1_ffn_forward(const zero1_ffn_shape *shape, const void *x, const void *w
     c.out(p.job[0], 0, mats[4]);
     c.out(p.job[0], 1, mats[6]);
     c.out(p.job[0], 2, mats[7]);
-    if (c.rc == ZERO1_OK) c.check(launch_ffn_gated(p, c.sms, c.stream), "kernel launch");
+    Mat ah = mats[4];
+    if (!ah.aligned()) {   // written twice: TMA cannot address the caller's
+        ah.ld = round_up(s.hidden, 8);
+        ah.p = c.take(copy_bytes(s.rows, s.hidden));
+        p.job[0].copy = static_cast<uint16_t *>(const_cast<void *>(ah.p));
+        p.job[0].ld_copy = ah.ld;
+    }
+    run(c, p, [&](const FfnParams &x) { return launch_ffn_gated(x, c.sms, c.stream); });
 
-    const Mat ah = c.addressable(mats[4]);
     FfnParams q = params_of(c, s.hidden, 1);
     c.map(&q.job[0].a[0], ah);
     c.map(&q.job[0].b[0], ad);
     size_job(q, 0, s.rows, s.width, kFfnTile);
     c.out(q.job[0], 0, mats[5]);
     slice(q, c.space + c.at);
-    if (c.rc == ZERO1_OK) c.check(launch_ffn_plain(q, false, true, c.sms, c.stream), "kernel launch");
+    run(c, q, [&](const FfnParams &x) { return launch_ffn_plain(x, false, true, c.sms, c.stream); });
     return c.rc;
 }
 
@@ -414,6 +460,7 @@ int zero1_ffn_backward(const zero1_ffn_shape *shape, const void *dy, const void 
     const Mat dup{c.take(copy_bytes(s.rows, s.hidden)), s.rows, s.hidden, ldw, "dup", true};
     const Mat ady = c.addressable(mats[4]), ax = c.addressable(mats[5]), ah = c.addressable(mats[8]);
     const Mat ag = c.addressable(mats[9]), au = c.addressable(mats[10]), ad = c.addressable(mats[11]);
+    c.copy_all();
     void *partials = c.space + c.at;
 
     FfnParams p = params_of(c, s.width, 1);          // dh, and from it dgate and dup
@@ -426,7 +473,7 @@ int zero1_ffn_backward(const zero1_ffn_shape *shape, const void *dy, const void 
     p.job[0].in[1] = static_cast<const uint16_t *>(up);
     p.job[0].ld_in = s.ldh;
     p.job[0].vec_in = mats[6].aligned() && mats[7].aligned();
-    if (c.rc == ZERO1_OK) c.check(launch_ffn_slope(p, c.sms, c.stream), "kernel launch");
+    run(c, p, [&](const FfnParams &x) { return launch_ffn_slope(x, c.sms, c.stream); });
 
     FfnParams w = params_of(c, s.rows, 1);           // the weights' gradients
     const Mat a[3] = {ax, ax, ah}, b[3] = {dgate, dup, ady};
@@ -437,7 +484,7 @@ int zero1_ffn_backward(const zero1_ffn_shape *shape, const void *dy, const void 
         c.out(w.job[i], 0, mats[i]);
     }
     slice(w, partials);
-    if (c.rc == ZERO1_OK) c.check(launch_ffn_plain(w, true, true, c.sms, c.stream), "kernel launch");
+    run(c, w, [&](const FfnParams &x) { return launch_ffn_plain(x, true, true, c.sms, c.stream); });
 
     if (dx) {
         FfnParams q = params_of(c, s.hidden, 2);
@@ -448,7 +495,7 @@ int zero1_ffn_backward(const zero1_ffn_shape *shape, const void *dy, const void 
         size_job(q, 0, s.rows, s.width, kFfnTile);
         c.out(q.job[0], 0, mats[3]);
         slice(q, partials);
-        if (c.rc == ZERO1_OK) c.check(launch_ffn_plain(q, false, false, c.sms, c.stream), "kernel launch");
+        run(c, q, [&](const FfnParams &x) { return launch_ffn_plain(x, false, false, c.sms, c.stream); });
     }
     return c.rc;
 }

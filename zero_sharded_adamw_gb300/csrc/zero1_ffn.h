@@ -28,7 +28,8 @@ struct FfnJob {
     CUtensorMap a[2], b[2];       // gated: b = gate's and up's weights; plain: one a segment
     uint16_t *out[3];             // gated: h, gate, up (the last two may be null); plain: out; slope: dgate, dup
     const uint16_t *in[2];        // slope: gate, up
-    uint64_t ld_out, ld_in;
+    uint16_t *copy;               // gated: h once more, where TMA cannot address the caller's (or null)
+    uint64_t ld_out, ld_in, ld_copy;
     uint32_t m, n;                // rows, columns of the result
     uint32_t tiles_m, tiles_n;
     uint32_t first;               // its first tile in the launch
@@ -40,6 +41,7 @@ struct FfnParams {
     uint32_t jobs, tiles, slices;
     uint32_t steps, segments;     // of 64 of K in a segment
     int act, stall;
+    int follows;                  // not the first launch of its call
     float *partials;              // of slices > 1
     unsigned *errors;             // may be null
 };

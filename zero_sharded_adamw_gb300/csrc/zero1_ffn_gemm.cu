@@ -26,8 +26,8 @@ namespace {
 
 constexpr uint32_t kBox = 8192;                     // 64 x 64 bf16
 constexpr uint32_t kStageBytes = 4 * kBox;          // one block's 128 rows of A and 128 of B
-constexpr int kStages = 6;
-constexpr int kEpilogueWarps = 8;
+constexpr int kStages = 5;
+constexpr int kEpilogueWarps = 16;
 constexpr int kGemmThreads = 64 + 32 * kEpilogueWarps;
 constexpr uint32_t kWarpTurn = 4096;                // 32 rows x 32 fp32 of an epilogue warp
 constexpr int kGemmSmem = kStages * kStageBytes + kEpilogueWarps * kWarpTurn + 1024;
@@ -74,15 +74,18 @@ __device__ __forceinline__ Item item_of(const FfnParams &p, uint32_t i)
 
 // --------------------------------------------------------------- epilogue
 
-// 32 x 32 fp32 of a warp, from one row a lane to 4 rows of 8 columns a lane:
-// lane l gets rows 8 i + l / 4, columns 8 (l % 4) on, so that a warp's
-// accesses to global memory are of 64 bytes a row.  Row r keeps its 16-byte
-// pieces exchanged by r % 8: no bank conflicts either way.
+// 32 x 32 fp32 of a warp go through shared memory, from one row a lane to a
+// mapping that global memory likes, 8 values at a time (q = 0..3):
+//   VEC:  row 8 q + lane / 4, columns 8 (lane % 4) on: 16-byte accesses, 64
+//         bytes of a row side by side;
+//   else: column `lane` of rows 8 q on: single entries, 32 of a row side by
+//         side, for rows that start off a 16-byte boundary.
+// Row r keeps its 16-byte pieces exchanged by r % 8: no bank conflicts.
 __device__ __forceinline__ uint32_t piece_at(uint32_t mem, uint32_t row, uint32_t piece)
 {
     return mem + row * 128 + ((piece ^ (row & 7u)) * 16);
 }
-__device__ __forceinline__ void turn(uint32_t mem, const float x[32], float y[4][8])
+__device__ __forceinline__ void put_rows(uint32_t mem, const float x[32])
 {
     const uint32_t lane = threadIdx.x & 31;
 #pragma unroll
@@ -90,48 +93,97 @@ __device__ __forceinline__ void turn(uint32_t mem, const float x[32], float y[4]
         tc::st_shared(piece_at(mem, lane, j), make_uint4(__float_as_uint(x[4 * j]), __float_as_uint(x[4 * j + 1]),
                                                          __float_as_uint(x[4 * j + 2]), __float_as_uint(x[4 * j + 3])));
     __syncwarp();
-#pragma unroll
-    for (uint32_t i = 0; i < 4; ++i) {
+}
+template <bool VEC>
+__device__ __forceinline__ void get8(float v[8], uint32_t mem, uint32_t q)
+{
+    const uint32_t lane = threadIdx.x & 31;
+    if (VEC) {
 #pragma unroll
         for (uint32_t j = 0; j < 2; ++j) {
-            const uint4 v = tc::ld_shared(piece_at(mem, 8 * i + (lane >> 2), 2 * (lane & 3) + j));
-            y[i][4 * j] = __uint_as_float(v.x);
-            y[i][4 * j + 1] = __uint_as_float(v.y);
-            y[i][4 * j + 2] = __uint_as_float(v.z);
-            y[i][4 * j + 3] = __uint_as_float(v.w);
+            const uint4 w = tc::ld_shared(piece_at(mem, 8 * q + (lane >> 2), 2 * (lane & 3) + j));
+            v[4 * j] = __uint_as_float(w.x);
+            v[4 * j + 1] = __uint_as_float(w.y);
+            v[4 * j + 2] = __uint_as_float(w.z);
+            v[4 * j + 3] = __uint_as_float(w.w);
         }
-    }
-    __syncwarp();
-}
-__device__ __forceinline__ void tmem_load32(float x[32], uint32_t addr)
-{
-    tc::tmem_load16(x, addr);
-    tc::tmem_load16(x + 16, addr + 16);
-}
-
-// Eight entries of a row, of which `left` are inside the matrix.
-__device__ __forceinline__ void store_row8(uint16_t *p, const float v[8], uint32_t left, bool vec)
-{
-    if (vec && left >= 8) {
-        *reinterpret_cast<uint4 *>(p) =
-            make_uint4(ptx::pack2(v[0], v[1]), ptx::pack2(v[2], v[3]), ptx::pack2(v[4], v[5]), ptx::pack2(v[6], v[7]));
     } else {
 #pragma unroll
         for (uint32_t k = 0; k < 8; ++k)
-            if (k < left) p[k] = __bfloat16_as_ushort(__float2bfloat16_rn(v[k]));
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[k]) : "r"(piece_at(mem, 8 * q + k, lane >> 2) + (lane & 3) * 4) : "memory");
     }
 }
-__device__ __forceinline__ uint4 load_row8(const uint16_t *p, uint32_t left, bool vec)
+
+// 32 lanes x 32 fp32 columns of tensor memory, one row a lane.
+__device__ __forceinline__ void tmem_load32(float v[32], uint32_t addr)
 {
-    if (vec && left >= 8) return *reinterpret_cast<const uint4 *>(p);
-    uint32_t w[8];
+    uint32_t *r = reinterpret_cast<uint32_t *>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+          "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
+          "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr)
+        : "memory");
+}
+
+// The 32 x 32 that a warp stands before: its first entry, and how much of it
+// lies inside the matrix.
+struct Patch {
+    uint64_t at;               // of entry (0, 0), in the matrix's entries
+    uint64_t ld;
+    uint32_t rows, cols;
+};
+template <bool VEC>
+__device__ __forceinline__ void store8(uint16_t *base, const Patch &p, const float v[8], uint32_t q)
+{
+    const uint32_t lane = threadIdx.x & 31;
+    if (VEC) {
+        const uint32_t r = 8 * q + (lane >> 2), c = (lane & 3) * 8;
+        if (r >= p.rows || c >= p.cols) return;
+        uint16_t *to = base + p.at + r * p.ld + c;
+        if (p.cols - c >= 8) {
+            *reinterpret_cast<uint4 *>(to) =
+                make_uint4(ptx::pack2(v[0], v[1]), ptx::pack2(v[2], v[3]), ptx::pack2(v[4], v[5]), ptx::pack2(v[6], v[7]));
+        } else {
 #pragma unroll
-    for (uint32_t k = 0; k < 8; ++k) w[k] = k < left ? p[k] : 0u;
+            for (uint32_t k = 0; k < 8; ++k)
+                if (k < p.cols - c) to[k] = __bfloat16_as_ushort(__float2bfloat16_rn(v[k]));
+        }
+    } else if (lane < p.cols) {
+        uint16_t *to = base + p.at + 8 * q * p.ld + lane;
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k)
+            if (8 * q + k < p.rows) to[k * p.ld] = __bfloat16_as_ushort(__float2bfloat16_rn(v[k]));
+    }
+}
+// The same entries read, as packed bf16 (zeros outside).
+template <bool VEC>
+__device__ __forceinline__ uint4 load8(const uint16_t *base, const Patch &p, uint32_t q)
+{
+    const uint32_t lane = threadIdx.x & 31;
+    uint32_t w[8];
+    if (VEC) {
+        const uint32_t r = 8 * q + (lane >> 2), c = (lane & 3) * 8;
+        if (r >= p.rows || c >= p.cols) return make_uint4(0, 0, 0, 0);
+        const uint16_t *from = base + p.at + r * p.ld + c;
+        if (p.cols - c >= 8) return *reinterpret_cast<const uint4 *>(from);
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k) w[k] = k < p.cols - c ? from[k] : 0u;
+    } else {
+        const uint16_t *from = base + p.at + 8 * q * p.ld + lane;
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k) w[k] = lane < p.cols && 8 * q + k < p.rows ? from[k * p.ld] : 0u;
+    }
     return make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
 }
 
 // Per pair: one thread of each block loads operands (TMA), one thread of the
-// first issues the products, eight warps of each block take its 128 rows of a
+// first issues the products, sixteen warps of each block take its 128 rows of a
 // finished tile out of one accumulator while the other fills.
 template <bool A_MN, bool B_MN, int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
@@ -162,6 +214,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     ptx::cluster_sync();
     tc::fence_after_sync();
     const uint32_t tmem = sh.tmem;
+    ptx::launch_dependents();
+    ptx::grid_dependency_wait();   // what the launch before wrote, and what it still reads
     const uint32_t items = p.tiles * p.slices, pairs = gridDim.x / 2, pair = blockIdx.x / 2;
 
     if (threadIdx.x == 0) {
@@ -227,92 +281,115 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
             }
         }
     } else if (warp >= 2) {
-        // ---- finished tiles: this block's 128 rows; each group of four warps half of the columns
+        // ---- finished tiles: this block's 128 rows; each group of four warps a fourth of the columns
         const uint32_t group = (uint32_t)(warp - 2) >> 2, quarter = (uint32_t)warp & 3, lane = threadIdx.x & 31;
         const uint32_t mem = ring + kStages * kStageBytes + (uint32_t)(warp - 2) * kWarpTurn;
-        constexpr uint32_t kHalf = MODE == kFfnGated ? 64 : 128;      // columns of a group
-        const uint32_t at = tmem + (quarter << 21) + group * kHalf;
-        const uint32_t own_row = rank * 128 + quarter * 32 + (lane >> 2), own_col = group * kHalf + (lane & 3) * 8;
+        constexpr uint32_t kCols = (MODE == kFfnGated ? 128 : 256) / (kEpilogueWarps / 4);   // columns of a group
+        const uint32_t at = tmem + (quarter << 21) + group * kCols;
         uint32_t used = 0;
         for (uint32_t i = pair; i < items; i += pairs, ++used) {
             const Item t = item_of<MODE>(p, i);
             const FfnJob &j = p.job[t.job];
-            const uint32_t acc = used & 1, row = t.row + own_row, col = t.col + own_col, m = j.m, n = j.n;
-            const bool vec_out = j.vec_out, vec_in = j.vec_in;
+            const uint32_t acc = used & 1, row = t.row + rank * 128 + quarter * 32, col = t.col + group * kCols;
+            const bool vec = j.vec_out && (MODE != kFfnSlope || j.vec_in);
+            const auto patch = [&](uint32_t c, uint64_t ld) {
+                return Patch{(uint64_t)row * ld + col + c, ld, row < j.m ? min(32u, j.m - row) : 0,
+                             col + c < j.n ? min(32u, j.n - col - c) : 0};
+            };
             uint4 in[2][4];
-            const auto fetch = [&](uint32_t c) {   // gate and up of 32 columns, while the product is still being formed
-                const uint32_t left = col + c < n ? n - col - c : 0;
+            const auto fetch = [&](uint32_t c) {   // gate and up, while the product is still being formed
+                const Patch from = patch(c, j.ld_in);
 #pragma unroll
                 for (uint32_t q = 0; q < 4; ++q) {
-                    const uint64_t o = (uint64_t)(row + 8 * q) * j.ld_in + col + c;
-                    const uint32_t here = row + 8 * q < m ? left : 0;
-                    in[0][q] = here ? load_row8(j.in[0] + o, here, vec_in) : make_uint4(0, 0, 0, 0);
-                    in[1][q] = here ? load_row8(j.in[1] + o, here, vec_in) : make_uint4(0, 0, 0, 0);
+                    in[0][q] = vec ? load8<true>(j.in[0], from, q) : load8<false>(j.in[0], from, q);
+                    in[1][q] = vec ? load8<true>(j.in[1], from, q) : load8<false>(j.in[1], from, q);
                 }
             };
             if (MODE == kFfnSlope) fetch(0);
             if (!__all_sync(~0u, tc::pair_wait(&sh.acc_full[acc], (used >> 1) & 1u, abort, errors))) break;
             tc::fence_after_sync();
 #pragma unroll 1
-            for (uint32_t c = 0; c < kHalf; c += 32) {
-                float x[32], y[4][8];
+            for (uint32_t c = 0; c < kCols; c += 32) {
+                float x[32];
                 tmem_load32(x, at + acc * kFfnTile + c);
-                turn(mem, x, y);
-                float z[4][8];
-                if (MODE == kFfnGated) {
-                    tmem_load32(x, at + acc * kFfnTile + 128 + c);
-                    turn(mem, x, z);
+                put_rows(mem, x);
+                if (MODE == kFfnGated) {   // the gate's entries to registers, up's to shared memory
+#pragma unroll
+                    for (uint32_t q = 0; q < 4; ++q) vec ? get8<true>(x + 8 * q, mem, q) : get8<false>(x + 8 * q, mem, q);
+                    __syncwarp();
+                    float y[32];
+                    tmem_load32(y, at + acc * kFfnTile + 128 + c);
+                    put_rows(mem, y);
                 }
-                if (c + 32 == kHalf) {   // the accumulator may be written again
+                if (c + 32 == kCols) {   // the accumulator may be written again
                     tc::fence_before_sync();
                     __syncwarp();
                     if (lane == 0) tc::arrive_cluster_relaxed(tc::map_to(tc::smem_u32(&sh.acc_empty[acc]), 0));
                 }
                 if (MODE == kFfnPlain && p.slices > 1) {
-                    float *to = p.partials + (uint64_t)i * (kFfnTile * kFfnTile) + own_row * kFfnTile + own_col + c;
+                    float *to = p.partials + (uint64_t)i * (kFfnTile * kFfnTile) + (row - t.row) * kFfnTile + (col - t.col) + c +
+                                (lane >> 2) * kFfnTile + (lane & 3) * 8;
 #pragma unroll
                     for (uint32_t q = 0; q < 4; ++q) {
-                        *reinterpret_cast<float4 *>(to + 8 * q * kFfnTile) = make_float4(y[q][0], y[q][1], y[q][2], y[q][3]);
-                        *reinterpret_cast<float4 *>(to + 8 * q * kFfnTile + 4) = make_float4(y[q][4], y[q][5], y[q][6], y[q][7]);
+                        float v[8];
+                        get8<true>(v, mem, q);
+                        *reinterpret_cast<float4 *>(to + 8 * q * kFfnTile) = make_float4(v[0], v[1], v[2], v[3]);
+                        *reinterpret_cast<float4 *>(to + 8 * q * kFfnTile + 4) = make_float4(v[4], v[5], v[6], v[7]);
                     }
+                    __syncwarp();
                     continue;
                 }
-                const uint32_t left = col + c < n ? n - col - c : 0;
-                if (MODE == kFfnSlope) {
+                const Patch to = patch(c, j.ld_out);
+                const auto finish = [&](auto is_vec, auto act) {
+                    constexpr bool VEC = decltype(is_vec)::value;
+                    constexpr int ACT = decltype(act)::value;
 #pragma unroll
                     for (uint32_t q = 0; q < 4; ++q) {
-                        float g[8], u[8];
-                        ptx::set_widened(g, in[0][q]);
-                        ptx::set_widened(u, in[1][q]);
+                        float v[8];
+                        get8<VEC>(v, mem, q);
+                        if (MODE == kFfnPlain) {
+                            store8<VEC>(j.out[0], to, v, q);
+                        } else if (MODE == kFfnGated) {
+                            if (j.out[1]) {
+                                store8<VEC>(j.out[1], to, x + 8 * q, q);
+                                store8<VEC>(j.out[2], to, v, q);
+                            }
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            float a, slope;
-                            activate<true>(p.act, g[k], a, slope);
-                            z[q][k] = y[q][k] * a;
-                            y[q][k] = y[q][k] * u[k] * slope;
+                            for (int k = 0; k < 8; ++k) {
+                                float a, none;
+                                activate<ACT, false>(x[8 * q + k], a, none);
+                                v[k] *= a;
+                            }
+                            store8<VEC>(j.out[0], to, v, q);
+                            if (j.copy) store8<VEC>(j.copy, patch(c, j.ld_copy), v, q);
+                        } else {
+                            float g[8], u[8];
+                            ptx::set_widened(g, in[0][q]);
+                            ptx::set_widened(u, in[1][q]);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                float a, slope;
+                                activate<ACT, true>(g[k], a, slope);
+                                g[k] = v[k] * u[k] * slope;
+                                u[k] = v[k] * a;
+                            }
+                            store8<VEC>(j.out[0], to, g, q);
+                            store8<VEC>(j.out[1], to, u, q);
                         }
                     }
-                    if (c + 32 < kHalf) fetch(c + 32);
-                }
-#pragma unroll
-                for (uint32_t q = 0; q < 4; ++q) {
-                    if (row + 8 * q >= m || left == 0) continue;
-                    const uint64_t o = (uint64_t)(row + 8 * q) * j.ld_out + col + c;
-                    if (MODE == kFfnGated) {
-                        if (j.out[1]) {
-                            store_row8(j.out[1] + o, y[q], left, vec_out);
-                            store_row8(j.out[2] + o, z[q], left, vec_out);
-                        }
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            float a, none;
-                            activate<false>(p.act, y[q][k], a, none);
-                            y[q][k] = a * z[q][k];
-                        }
-                    }
-                    store_row8(j.out[0] + o, y[q], left, vec_out);
-                    if (MODE == kFfnSlope) store_row8(j.out[1] + o, z[q], left, vec_out);
-                }
+                };
+                const auto by_act = [&](auto is_vec) {
+                    if (MODE == kFfnPlain)
+                        finish(is_vec, ActOf<0>{});
+                    else
+                        with_activation(p.act, [&](auto act) { finish(is_vec, act); });
+                };
+                if (vec)
+                    by_act(ActOf<1>{});
+                else
+                    by_act(ActOf<0>{});
+                if (MODE == kFfnSlope && c + 32 < kCols) fetch(c + 32);
+                __syncwarp();
             }
         }
     }
@@ -334,6 +411,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 // The slices' partial sums, added in order: one warp a row of a tile.
 __global__ void __launch_bounds__(256) zero1_ffn_join_kernel(const __grid_constant__ FfnParams p)
 {
+    ptx::launch_dependents();
+    ptx::grid_dependency_wait();
     const uint32_t tile = blockIdx.x / (kFfnTile / 8), lane = threadIdx.x & 31;
     const Item t = item_of<kFfnPlain>(p, tile * p.slices);
     const FfnJob &j = p.job[t.job];
@@ -348,7 +427,15 @@ __global__ void __launch_bounds__(256) zero1_ffn_join_kernel(const __grid_consta
         const float4 a = reinterpret_cast<const float4 *>(src)[0], b = reinterpret_cast<const float4 *>(src)[1];
         v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w, v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
     }
-    store_row8(j.out[0] + (uint64_t)row * j.ld_out + col, v, j.n - col, j.vec_out);
+    uint16_t *to = j.out[0] + (uint64_t)row * j.ld_out + col;
+    if (j.vec_out && j.n - col >= 8) {
+        *reinterpret_cast<uint4 *>(to) =
+            make_uint4(ptx::pack2(v[0], v[1]), ptx::pack2(v[2], v[3]), ptx::pack2(v[4], v[5]), ptx::pack2(v[6], v[7]));
+    } else {
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k)
+            if (k < j.n - col) to[k] = __bfloat16_as_ushort(__float2bfloat16_rn(v[k]));
+    }
 }
 
 template <bool A_MN, bool B_MN, int MODE>
@@ -358,9 +445,12 @@ cudaError_t gemm(const FfnParams &p, int sms, cudaStream_t stream)
     cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), kGemmSmem);
     if (e != cudaSuccess) return e;
     const uint32_t pairs = (uint32_t)sms / 2, items = p.tiles * p.slices;
-    e = launch(kernel, dim3(2 * (items < pairs ? items : pairs)), kGemmThreads, kGemmSmem, stream, p);
+    const dim3 grid(2 * (items < pairs ? items : pairs));
+    // after another kernel of the same call it may begin while that one ends
+    e = p.follows ? launch_early(kernel, grid, kGemmThreads, kGemmSmem, stream, p)
+                  : launch(kernel, grid, kGemmThreads, kGemmSmem, stream, p);
     if (e == cudaSuccess && p.slices > 1)
-        e = launch(zero1_ffn_join_kernel, dim3(p.tiles * (kFfnTile / 8)), 256, 0, stream, p);
+        e = launch_early(zero1_ffn_join_kernel, dim3(p.tiles * (kFfnTile / 8)), 256, 0, stream, p);
     return e;
 }
 

@@ -224,14 +224,16 @@ __global__ void __launch_bounds__(kThinThreads) zero1_ffn_thin_kernel(const __gr
                 store4(p.out[2] + at, b, left, p.vec);
             }
             float rest[4];
+            with_activation(p.act, [&](auto act) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                float v, none;
-                activate<false>(p.act, a[k], v, none);
-                a[k] = v * b[k];
-                rest[k] = a[k] - __bfloat162float(__float2bfloat16_rn(a[k]));
-                if (!isfinite(rest[k])) rest[k] = 0.f;   // an infinite h has no low part
-            }
+                for (int k = 0; k < 4; ++k) {
+                    float v, none;
+                    activate<decltype(act)::value, false>(a[k], v, none);
+                    a[k] = v * b[k];
+                    rest[k] = a[k] - __bfloat162float(__float2bfloat16_rn(a[k]));
+                    if (!isfinite(rest[k])) rest[k] = 0.f;   // an infinite h has no low part
+                }
+            });
             uint16_t *to = p.part + (uint64_t)r * p.ld_part + c;   // padded to 8 entries
             store4(to, a, left, true);
             if (N == 16) store4(to + p.plane, rest, left, true);

@@ -74,12 +74,16 @@ __device__ __forceinline__ Item item_of(const FfnParams &p, uint32_t i)
 
 // --------------------------------------------------------------- epilogue
 
+// How a warp's patch meets global memory: 16-byte pieces of a patch wholly
+// inside the matrix, the same near an edge, or single entries.
+enum Access : int { kWholePatch, kEdgePatch, kSingles };
+
 // 32 x 32 fp32 of a warp go through shared memory, from one row a lane to a
 // mapping that global memory likes, 8 values at a time (q = 0..3):
-//   VEC:  row 8 q + lane / 4, columns 8 (lane % 4) on: 16-byte accesses, 64
-//         bytes of a row side by side;
-//   else: column `lane` of rows 8 q on: single entries, 32 of a row side by
-//         side, for rows that start off a 16-byte boundary.
+//   pieces:  row 8 q + lane / 4, columns 8 (lane % 4) on: 16-byte accesses,
+//            64 bytes of a row side by side;
+//   singles: column `lane` of rows 8 q on: 32 entries of a row side by side,
+//            for rows that start off a 16-byte boundary.
 // Row r keeps its 16-byte pieces exchanged by r % 8: no bank conflicts.
 __device__ __forceinline__ uint32_t piece_at(uint32_t mem, uint32_t row, uint32_t piece)
 {
@@ -94,11 +98,11 @@ __device__ __forceinline__ void put_rows(uint32_t mem, const float x[32])
                                                          __float_as_uint(x[4 * j + 2]), __float_as_uint(x[4 * j + 3])));
     __syncwarp();
 }
-template <bool VEC>
+template <int HOW>
 __device__ __forceinline__ void get8(float v[8], uint32_t mem, uint32_t q)
 {
     const uint32_t lane = threadIdx.x & 31;
-    if (VEC) {
+    if (HOW != kSingles) {
 #pragma unroll
         for (uint32_t j = 0; j < 2; ++j) {
             const uint4 w = tc::ld_shared(piece_at(mem, 8 * q + (lane >> 2), 2 * (lane & 3) + j));
@@ -138,48 +142,89 @@ struct Patch {
     uint64_t ld;
     uint32_t rows, cols;
 };
-template <bool VEC>
-__device__ __forceinline__ void store8(uint16_t *base, const Patch &p, const float v[8], uint32_t q)
-{
-    const uint32_t lane = threadIdx.x & 31;
-    if (VEC) {
-        const uint32_t r = 8 * q + (lane >> 2), c = (lane & 3) * 8;
-        if (r >= p.rows || c >= p.cols) return;
-        uint16_t *to = base + p.at + r * p.ld + c;
-        if (p.cols - c >= 8) {
-            *reinterpret_cast<uint4 *>(to) =
-                make_uint4(ptx::pack2(v[0], v[1]), ptx::pack2(v[2], v[3]), ptx::pack2(v[4], v[5]), ptx::pack2(v[6], v[7]));
-        } else {
-#pragma unroll
-            for (uint32_t k = 0; k < 8; ++k)
-                if (k < p.cols - c) to[k] = __bfloat16_as_ushort(__float2bfloat16_rn(v[k]));
-        }
-    } else if (lane < p.cols) {
-        uint16_t *to = base + p.at + 8 * q * p.ld + lane;
-#pragma unroll
-        for (uint32_t k = 0; k < 8; ++k)
-            if (8 * q + k < p.rows) to[k * p.ld] = __bfloat16_as_ushort(__float2bfloat16_rn(v[k]));
-    }
-}
-// The same entries read, as packed bf16 (zeros outside).
-template <bool VEC>
+// 8 values of the mapping above, as packed bf16; zeros outside the matrix.
+template <int HOW>
 __device__ __forceinline__ uint4 load8(const uint16_t *base, const Patch &p, uint32_t q)
 {
     const uint32_t lane = threadIdx.x & 31;
     uint32_t w[8];
-    if (VEC) {
-        const uint32_t r = 8 * q + (lane >> 2), c = (lane & 3) * 8;
-        if (r >= p.rows || c >= p.cols) return make_uint4(0, 0, 0, 0);
-        const uint16_t *from = base + p.at + r * p.ld + c;
-        if (p.cols - c >= 8) return *reinterpret_cast<const uint4 *>(from);
-#pragma unroll
-        for (uint32_t k = 0; k < 8; ++k) w[k] = k < p.cols - c ? from[k] : 0u;
-    } else {
+    if (HOW == kSingles) {
         const uint16_t *from = base + p.at + 8 * q * p.ld + lane;
 #pragma unroll
         for (uint32_t k = 0; k < 8; ++k) w[k] = lane < p.cols && 8 * q + k < p.rows ? from[k * p.ld] : 0u;
+    } else {
+        const uint32_t r = 8 * q + (lane >> 2), c = (lane & 3) * 8;
+        const uint16_t *from = base + p.at + r * p.ld + c;
+        if (HOW == kWholePatch) return *reinterpret_cast<const uint4 *>(from);
+        if (r >= p.rows || c >= p.cols) return make_uint4(0, 0, 0, 0);
+        if (p.cols - c >= 8) return *reinterpret_cast<const uint4 *>(from);
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k) w[k] = k < p.cols - c ? from[k] : 0u;
     }
     return make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+}
+template <int HOW>
+__device__ __forceinline__ void store8(uint16_t *base, const Patch &p, uint4 v, uint32_t q)
+{
+    const uint32_t lane = threadIdx.x & 31;
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if (HOW == kSingles) {
+        if (lane >= p.cols) return;
+        uint16_t *to = base + p.at + 8 * q * p.ld + lane;
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k)
+            if (8 * q + k < p.rows) to[k * p.ld] = (uint16_t)(w[k / 2] >> (k & 1 ? 16 : 0));
+    } else {
+        const uint32_t r = 8 * q + (lane >> 2), c = (lane & 3) * 8;
+        uint16_t *to = base + p.at + r * p.ld + c;
+        if (HOW == kEdgePatch) {
+            if (r >= p.rows || c >= p.cols) return;
+            if (p.cols - c < 8) {
+#pragma unroll
+                for (uint32_t k = 0; k < 8; ++k)
+                    if (k < p.cols - c) to[k] = (uint16_t)(w[k / 2] >> (k & 1 ? 16 : 0));
+                return;
+            }
+        }
+        *reinterpret_cast<uint4 *>(to) = v;
+    }
+}
+__device__ __forceinline__ uint4 pack8(const float v[8])
+{
+    return make_uint4(ptx::pack2(v[0], v[1]), ptx::pack2(v[2], v[3]), ptx::pack2(v[4], v[5]), ptx::pack2(v[6], v[7]));
+}
+
+// Results that are bf16 already when they leave their row: 32 rows of 64
+// bytes, in 2 KB.  Row r keeps its pieces exchanged by (r / 2) % 4.
+__device__ __forceinline__ uint32_t narrow_at(uint32_t mem, uint32_t row, uint32_t piece)
+{
+    return mem + row * 64 + ((piece ^ ((row >> 1) & 3u)) * 16);
+}
+__device__ __forceinline__ void put_narrow(uint32_t mem, const float x[32])
+{
+    const uint32_t lane = threadIdx.x & 31;
+#pragma unroll
+    for (uint32_t j = 0; j < 4; ++j) tc::st_shared(narrow_at(mem, lane, j), pack8(x + 8 * j));
+}
+template <int HOW>
+__device__ __forceinline__ uint4 get_narrow(uint32_t mem, uint32_t q)
+{
+    const uint32_t lane = threadIdx.x & 31;
+    if (HOW != kSingles) return tc::ld_shared(narrow_at(mem, 8 * q + (lane >> 2), lane & 3));
+    uint32_t w[8];
+#pragma unroll
+    for (uint32_t k = 0; k < 8; ++k) {
+        uint16_t e;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(e) : "r"(narrow_at(mem, 8 * q + k, lane >> 3) + (lane & 7) * 2) : "memory");
+        w[k] = e;
+    }
+    return make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+}
+template <int HOW>
+__device__ __forceinline__ void write_narrow(uint16_t *base, const Patch &p, uint32_t mem)
+{
+#pragma unroll
+    for (uint32_t q = 0; q < 4; ++q) store8<HOW>(base, p, get_narrow<HOW>(mem, q), q);
 }
 
 // Per pair: one thread of each block loads operands (TMA), one thread of the
@@ -287,6 +332,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         constexpr uint32_t kCols = (MODE == kFfnGated ? 128 : 256) / (kEpilogueWarps / 4);   // columns of a group
         const uint32_t at = tmem + (quarter << 21) + group * kCols;
         uint32_t used = 0;
+        uint4 in[2][MODE == kFfnSlope ? 4 : 1];   // slope: gate and up of the 32 columns to come
         for (uint32_t i = pair; i < items; i += pairs, ++used) {
             const Item t = item_of<MODE>(p, i);
             const FfnJob &j = p.job[t.job];
@@ -296,99 +342,120 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
                 return Patch{(uint64_t)row * ld + col + c, ld, row < j.m ? min(32u, j.m - row) : 0,
                              col + c < j.n ? min(32u, j.n - col - c) : 0};
             };
-            uint4 in[2][4];
-            const auto fetch = [&](uint32_t c) {   // gate and up, while the product is still being formed
-                const Patch from = patch(c, j.ld_in);
+            if (MODE == kFfnSlope && used == 0) {
+                const Patch from = patch(0, j.ld_in);
 #pragma unroll
                 for (uint32_t q = 0; q < 4; ++q) {
-                    in[0][q] = vec ? load8<true>(j.in[0], from, q) : load8<false>(j.in[0], from, q);
-                    in[1][q] = vec ? load8<true>(j.in[1], from, q) : load8<false>(j.in[1], from, q);
+                    in[0][q] = vec ? load8<kEdgePatch>(j.in[0], from, q) : load8<kSingles>(j.in[0], from, q);
+                    in[1][q] = vec ? load8<kEdgePatch>(j.in[1], from, q) : load8<kSingles>(j.in[1], from, q);
                 }
-            };
-            if (MODE == kFfnSlope) fetch(0);
+            }
             if (!__all_sync(~0u, tc::pair_wait(&sh.acc_full[acc], (used >> 1) & 1u, abort, errors))) break;
             tc::fence_after_sync();
 #pragma unroll 1
             for (uint32_t c = 0; c < kCols; c += 32) {
-                float x[32];
+                float x[32], y[MODE == kFfnGated ? 32 : 1];
                 tmem_load32(x, at + acc * kFfnTile + c);
-                put_rows(mem, x);
-                if (MODE == kFfnGated) {   // the gate's entries to registers, up's to shared memory
-#pragma unroll
-                    for (uint32_t q = 0; q < 4; ++q) vec ? get8<true>(x + 8 * q, mem, q) : get8<false>(x + 8 * q, mem, q);
-                    __syncwarp();
-                    float y[32];
-                    tmem_load32(y, at + acc * kFfnTile + 128 + c);
-                    put_rows(mem, y);
-                }
+                if constexpr (MODE == kFfnGated) tmem_load32(y, at + acc * kFfnTile + 128 + c);
                 if (c + 32 == kCols) {   // the accumulator may be written again
                     tc::fence_before_sync();
                     __syncwarp();
                     if (lane == 0) tc::arrive_cluster_relaxed(tc::map_to(tc::smem_u32(&sh.acc_empty[acc]), 0));
                 }
-                if (MODE == kFfnPlain && p.slices > 1) {
-                    float *to = p.partials + (uint64_t)i * (kFfnTile * kFfnTile) + (row - t.row) * kFfnTile + (col - t.col) + c +
-                                (lane >> 2) * kFfnTile + (lane & 3) * 8;
-#pragma unroll
-                    for (uint32_t q = 0; q < 4; ++q) {
-                        float v[8];
-                        get8<true>(v, mem, q);
-                        *reinterpret_cast<float4 *>(to + 8 * q * kFfnTile) = make_float4(v[0], v[1], v[2], v[3]);
-                        *reinterpret_cast<float4 *>(to + 8 * q * kFfnTile + 4) = make_float4(v[4], v[5], v[6], v[7]);
-                    }
-                    __syncwarp();
-                    continue;
-                }
                 const Patch to = patch(c, j.ld_out);
-                const auto finish = [&](auto is_vec, auto act) {
-                    constexpr bool VEC = decltype(is_vec)::value;
-                    constexpr int ACT = decltype(act)::value;
+                const int how = !vec ? kSingles : to.rows == 32 && to.cols == 32 ? kWholePatch : kEdgePatch;
+                const auto by_access = [&](auto f) {
+                    if (how == kWholePatch) f(ActOf<kWholePatch>{});
+                    else if (how == kEdgePatch) f(ActOf<kEdgePatch>{});
+                    else f(ActOf<kSingles>{});
+                };
+                if constexpr (MODE == kFfnPlain) {
+                    if (p.slices > 1) {
+                        put_rows(mem, x);
+                        float *sums = p.partials + (uint64_t)i * (kFfnTile * kFfnTile) + (row - t.row) * kFfnTile + (col - t.col) + c +
+                                      (lane >> 2) * kFfnTile + (lane & 3) * 8;
 #pragma unroll
-                    for (uint32_t q = 0; q < 4; ++q) {
-                        float v[8];
-                        get8<VEC>(v, mem, q);
-                        if (MODE == kFfnPlain) {
-                            store8<VEC>(j.out[0], to, v, q);
-                        } else if (MODE == kFfnGated) {
-                            if (j.out[1]) {
-                                store8<VEC>(j.out[1], to, x + 8 * q, q);
-                                store8<VEC>(j.out[2], to, v, q);
-                            }
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                float a, none;
-                                activate<ACT, false>(x[8 * q + k], a, none);
-                                v[k] *= a;
-                            }
-                            store8<VEC>(j.out[0], to, v, q);
-                            if (j.copy) store8<VEC>(j.copy, patch(c, j.ld_copy), v, q);
-                        } else {
-                            float g[8], u[8];
-                            ptx::set_widened(g, in[0][q]);
-                            ptx::set_widened(u, in[1][q]);
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                float a, slope;
-                                activate<ACT, true>(g[k], a, slope);
-                                g[k] = v[k] * u[k] * slope;
-                                u[k] = v[k] * a;
-                            }
-                            store8<VEC>(j.out[0], to, g, q);
-                            store8<VEC>(j.out[1], to, u, q);
+                        for (uint32_t q = 0; q < 4; ++q) {
+                            float v[8];
+                            get8<kWholePatch>(v, mem, q);
+                            *reinterpret_cast<float4 *>(sums + 8 * q * kFfnTile) = make_float4(v[0], v[1], v[2], v[3]);
+                            *reinterpret_cast<float4 *>(sums + 8 * q * kFfnTile + 4) = make_float4(v[4], v[5], v[6], v[7]);
                         }
+                    } else {
+                        put_narrow(mem, x);
+                        __syncwarp();
+                        by_access([&](auto h) { write_narrow<decltype(h)::value>(j.out[0], to, mem); });
                     }
-                };
-                const auto by_act = [&](auto is_vec) {
-                    if (MODE == kFfnPlain)
-                        finish(is_vec, ActOf<0>{});
-                    else
-                        with_activation(p.act, [&](auto act) { finish(is_vec, act); });
-                };
-                if (vec)
-                    by_act(ActOf<1>{});
-                else
-                    by_act(ActOf<0>{});
-                if (MODE == kFfnSlope && c + 32 < kCols) fetch(c + 32);
+                } else if constexpr (MODE == kFfnGated) {
+                    const uint32_t second = mem + kWarpTurn / 2;
+                    if (j.out[1]) {
+                        put_narrow(mem, x);
+                        put_narrow(second, y);
+                        __syncwarp();
+                        by_access([&](auto h) {
+                            write_narrow<decltype(h)::value>(j.out[1], to, mem);
+                            write_narrow<decltype(h)::value>(j.out[2], to, second);
+                        });
+                        __syncwarp();
+                    }
+                    with_activation(p.act, [&](auto act) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) {
+                            float a, none;
+                            activate<decltype(act)::value, false>(x[k], a, none);
+                            x[k] = a * y[k];
+                        }
+                    });
+                    put_narrow(mem, x);
+                    __syncwarp();
+                    by_access([&](auto h) { write_narrow<decltype(h)::value>(j.out[0], to, mem); });
+                    if (j.copy) {   // of aligned rows
+                        const Patch again = patch(c, j.ld_copy);
+                        write_narrow<kEdgePatch>(j.copy, again, mem);
+                    }
+                } else {
+                    // gate and up of the warp's next 32 columns are fetched as these are used
+                    put_rows(mem, x);
+                    Patch next = patch(c + 32, j.ld_in);
+                    bool more = c + 32 < kCols;
+                    if (!more && i + pairs < items) {
+                        const Item then = item_of<MODE>(p, i + pairs);
+                        const uint32_t r = then.row + rank * 128 + quarter * 32, cc = then.col + group * kCols;
+                        next = Patch{(uint64_t)r * j.ld_in + cc, j.ld_in, r < j.m ? min(32u, j.m - r) : 0, cc < j.n ? min(32u, j.n - cc) : 0};
+                        more = true;
+                    }
+                    const bool next_whole = next.rows == 32 && next.cols == 32;
+                    by_access([&](auto h) {
+                        constexpr int HOW = decltype(h)::value;
+                        with_activation(p.act, [&](auto act) {
+#pragma unroll
+                            for (uint32_t q = 0; q < 4; ++q) {
+                                float v[8], g[8], u[8];
+                                get8<HOW>(v, mem, q);
+                                ptx::set_widened(g, in[0][q]);
+                                ptx::set_widened(u, in[1][q]);
+                                if (more) {
+                                    if (HOW != kSingles && next_whole) {
+                                        in[0][q] = load8<kWholePatch>(j.in[0], next, q);
+                                        in[1][q] = load8<kWholePatch>(j.in[1], next, q);
+                                    } else {
+                                        in[0][q] = load8<HOW == kSingles ? kSingles : kEdgePatch>(j.in[0], next, q);
+                                        in[1][q] = load8<HOW == kSingles ? kSingles : kEdgePatch>(j.in[1], next, q);
+                                    }
+                                }
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) {
+                                    float a, slope;
+                                    activate<decltype(act)::value, true>(g[k], a, slope);
+                                    g[k] = v[k] * u[k] * slope;
+                                    u[k] = v[k] * a;
+                                }
+                                store8<HOW>(j.out[0], to, pack8(g), q);
+                                store8<HOW>(j.out[1], to, pack8(u), q);
+                            }
+                        });
+                    });
+                }
                 __syncwarp();
             }
         }

@@ -801,32 +801,35 @@ class FfnShape:
                        self.ldh, self.ld_gate, self.ld_up, self.ld_down, int(self.unaligned),
                        int(self.inject_wait_timeout))
         r, w, h = self.rows, self.width, self.hidden
-        # (rows, columns, stride) of the buffers, for the checks of every call
-        mats = {"x": (r, w, self.ldx or w), "y": (r, w, self.ldy or w), "h": (r, h, self.ldh or h),
-                "w_gate": (w, h, self.ld_gate or h), "w_up": (w, h, self.ld_up or h), "w_down": (h, w, self.ld_down or w)}
+        # (rows, columns, stride, shape, strides) of x, y, h, w_gate, w_up and w_down, for the checks of every call
+        mats = [(r, w, self.ldx or w), (r, w, self.ldy or w), (r, h, self.ldh or h), (w, h, self.ld_gate or h),
+                (w, h, self.ld_up or h), (h, w, self.ld_down or w)]
         object.__setattr__(self, "_c", c)
-        object.__setattr__(self, "_mats", mats)
+        object.__setattr__(self, "_ref", C.byref(c))
+        object.__setattr__(self, "_mats", [(a, b, ld, (a, b), (ld, 1)) for a, b, ld in mats])
 
 
-def _ffn_mats(shape: FfnShape, **buffers):
-    """Addresses of a call's buffers, each checked as the matrix it is (dx as
-    x, dw_gate as w_gate, ...)."""
-    return [_take_matrix(x, *shape._mats[_FFN_KINDS.get(k, k)], k) for k, x in buffers.items()]
-
-
-_FFN_KINDS = {"dx": "x", "dy": "y", "gate": "h", "up": "h", "dw_gate": "w_gate", "dw_up": "w_up", "dw_down": "w_down"}
-
-
-def _take_matrix(x, rows: int, cols: int, ld: int, what: str) -> int | None:
-    """_take_rows of bf16, a two-dimensional tensor having to be this matrix."""
-    if x is not None and hasattr(x, "data_ptr") and x.dim() == 2 and x.shape != (rows, cols):
-        raise Zero1ArgumentError(f"{what}: expected {rows} x {cols}, got {tuple(x.shape)}")
-    return _take_rows(x, rows, cols, ld, "bf16", what)
+def _take_matrix(x, matrix: tuple, what: str) -> int | None:
+    """Address of the bf16 buffer `x` of a call, as _take_rows; a two-dimensional
+    tensor has to be this matrix (rows, columns, stride, shape, strides)."""
+    try:
+        if x.dtype is _TORCH_DTYPES["bf16"] and x.is_cuda and x.shape == matrix[3] and x.stride() == matrix[4]:
+            return x.data_ptr()
+    except (AttributeError, KeyError):
+        pass
+    if x is not None and hasattr(x, "data_ptr") and x.dim() == 2 and x.shape != matrix[3]:
+        raise Zero1ArgumentError(f"{what}: expected {matrix[0]} x {matrix[1]}, got {tuple(x.shape)}")
+    return _take_rows(x, *matrix[:3], "bf16", what)
 
 
 def _ffn_workspace(workspace) -> tuple[int | None, int]:
     if workspace is None:
         return None, 0
+    try:
+        if workspace.is_cuda and workspace.is_contiguous():
+            return workspace.data_ptr() or None, workspace.nbytes
+    except AttributeError:
+        pass
     if not hasattr(workspace, "numel") or not workspace.is_cuda or not workspace.is_contiguous():
         raise Zero1ArgumentError("workspace: expected a contiguous CUDA tensor")
     return workspace.data_ptr() or None, workspace.numel() * workspace.element_size()
@@ -844,17 +847,28 @@ def zero1_ffn_forward(shape: FfnShape, x, w_gate, w_up, w_down, gate, up, h, y, 
     """y = (act(x w_gate) * (x w_up)) w_down, keeping h and, unless both are
     None, gate and up; `workspace` is a CUDA tensor of at least
     zero1_ffn_workspace bytes, `errors` an optional CUDA word."""
-    mats = _ffn_mats(shape, x=x, w_gate=w_gate, w_up=w_up, w_down=w_down, gate=gate, up=up, h=h, y=y)
-    _check(_load().zero1_ffn_forward(C.byref(shape._c), *mats, *_ffn_workspace(workspace), _addr(errors), _stream(stream)))
+    mx, my, mh, mg, mu, md = shape._mats
+    rc = _load().zero1_ffn_forward(
+        shape._ref, _take_matrix(x, mx, "x"), _take_matrix(w_gate, mg, "w_gate"), _take_matrix(w_up, mu, "w_up"),
+        _take_matrix(w_down, md, "w_down"), None if gate is None else _take_matrix(gate, mh, "gate"),
+        None if up is None else _take_matrix(up, mh, "up"), _take_matrix(h, mh, "h"), _take_matrix(y, my, "y"),
+        *_ffn_workspace(workspace), _addr(errors), _stream(stream))
+    if rc:
+        _check(rc)
 
 
 def zero1_ffn_backward(shape: FfnShape, dy, x, w_gate, w_up, w_down, gate, up, h, dx, dw_gate, dw_up, dw_down,
                        workspace=None, stream=None, errors=None) -> None:
     """The gradients of x (None: not wanted) and of the three matrices, from the forward pass's gate, up and h."""
-    mats = _ffn_mats(shape, dy=dy, x=x, w_gate=w_gate, w_up=w_up, w_down=w_down, gate=gate, up=up, h=h, dx=dx,
-                     dw_gate=dw_gate, dw_up=dw_up, dw_down=dw_down)
-    _check(_load().zero1_ffn_backward(C.byref(shape._c), *mats, *_ffn_workspace(workspace), _addr(errors),
-                                      _stream(stream)))
+    mx, my, mh, mg, mu, md = shape._mats
+    rc = _load().zero1_ffn_backward(
+        shape._ref, _take_matrix(dy, my, "dy"), _take_matrix(x, mx, "x"), _take_matrix(w_gate, mg, "w_gate"),
+        _take_matrix(w_up, mu, "w_up"), _take_matrix(w_down, md, "w_down"), _take_matrix(gate, mh, "gate"),
+        _take_matrix(up, mh, "up"), _take_matrix(h, mh, "h"), None if dx is None else _take_matrix(dx, mx, "dx"),
+        _take_matrix(dw_gate, mg, "dw_gate"), _take_matrix(dw_up, mu, "dw_up"), _take_matrix(dw_down, md, "dw_down"),
+        *_ffn_workspace(workspace), _addr(errors), _stream(stream))
+    if rc:
+        _check(rc)
 
 
 # --------------------------------------------------------- AdamW over many tensors

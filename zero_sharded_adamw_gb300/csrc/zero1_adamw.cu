@@ -387,17 +387,33 @@ struct Squares {
 constexpr float kSumHigh = 1.3292279957849159e36f, kSumLow = 8.0779356694631609e-28f;   // 2^120, 2^-90
 
 // Sum over the block in a fixed order; valid on thread 0.
+template <uint32_t WARPS = kWarps>
 __device__ __forceinline__ double sum_block(double v)
 {
-    __shared__ double part[kWarps];
+    __shared__ double part[WARPS];
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
     double s = 0.0;
     if (threadIdx.x == 0)
-        for (uint32_t i = 0; i < kWarps; ++i) s += part[i];
+        for (uint32_t i = 0; i < WARPS; ++i) s += part[i];
     __syncthreads();
     return s;
+}
+
+// The norm of a sum of squares, and the clip coefficient it gives.
+__device__ __forceinline__ float finish_norm(const ListTables &d, double squares)
+{
+    const double norm = sqrt(squares);
+    float c = 1.f;
+    if (isnan(norm))
+        c = __int_as_float(0x7FC00000);
+    else if (d.max_norm / norm < 1.0)
+        c = (float)(d.max_norm / norm);
+    d.status->nsq = squares;
+    d.status->norm = norm;
+    d.status->clip = c;
+    return c;
 }
 
 // Whether this block is the last of its grid to get here (all threads).
@@ -514,17 +530,7 @@ __global__ void __launch_bounds__(kListThreads, 4) zero1_adamw_norm_kernel(const
     double v = 0.0;
     for (uint32_t i = threadIdx.x; i < p.before + gridDim.x; i += kListThreads) v += __ldcg(p.d.partials + i);
     v = sum_block(v);
-    if (threadIdx.x == 0) {
-        const double norm = sqrt(v);
-        float c = 1.f;
-        if (isnan(norm))
-            c = __int_as_float(0x7FC00000);
-        else if (p.d.max_norm / norm < 1.0)
-            c = (float)(p.d.max_norm / norm);
-        p.d.status->nsq = v;
-        p.d.status->norm = norm;
-        p.d.status->clip = c;
-    }
+    if (threadIdx.x == 0) finish_norm(p.d, v);
 }
 
 // -------------------------------------------------------------- the update
@@ -800,6 +806,73 @@ __global__ void __launch_bounds__(kListThreads, 4) zero1_adamw_update_kernel(con
     }
     __syncthreads();   // every warp has read the scalars
     if (last_block(&p.d.status->ticket[1]) && p.last && threadIdx.x == 0) {
+        p.d.status->t = t;
+        form_scalars(p.d, t, p.d.status->lr);
+    }
+}
+
+// A clipped step of a short list in one launch: one block keeps all gradients
+// in registers between the norm and the update (4,096 bf16 entries in two
+// tensors: 7 us, 10 with two launches).
+constexpr uint32_t kSmallWarps = 32, kSmallPer = 2;
+template <typename P, typename G, int BITS>
+__global__ void __launch_bounds__(32 * kSmallWarps) zero1_adamw_small_kernel(const __grid_constant__ UpdateParams<32> p)
+{
+    constexpr bool kExact = sizeof(G) == 2;
+    __shared__ float clip_of_all;
+    const ListStatus *status = p.d.status;
+    const float step_size = status->step_size, decay = status->decay;
+    const unsigned long long t = status->t + 1;
+    const uint32_t warp = threadIdx.x >> 5;
+    const Two one = p.one, minus = mul(p.one, two(-1.f, -1.f));
+    Squares ss;
+    float kept[8 * kSmallPer] = {};
+    uint32_t any = 0;
+#pragma unroll
+    for (uint32_t u = 0; u < kSmallPer; ++u) {
+        const uint32_t b = warp + u * kSmallWarps;
+        if (b >= p.nblocks) break;
+        const Place<P, G> at = place_of<P, G, 32>(p, __ldg(p.d.blocks + b), b);
+        float g[8];
+        if (at.whole())
+            get8<true>(g, at.grad, kListBlock);
+        else
+            get8<false>(g, at.grad, at.count);
+#pragma unroll
+        for (int k = 0; k < 8; k += 2) {
+            any |= __float_as_uint(g[k]) | __float_as_uint(g[k + 1]);
+            ss.add2<kExact>(two(g[k], g[k + 1]), one, minus);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) kept[u * 8 + k] = g[k];
+    }
+    const float size = ss.size();
+    double mine = ss.total();
+    if (!(size < kSumHigh) || (size < kSumLow && any != 0)) {
+        mine = 0.0;
+#pragma unroll
+        for (uint32_t k = 0; k < 8 * kSmallPer; ++k) mine += (double)kept[k] * (double)kept[k];
+    }
+    const double sum = sum_block<kSmallWarps>(mine);
+    if (threadIdx.x == 0) clip_of_all = finish_norm(p.d, sum);
+    __syncthreads();
+    const float clip = clip_of_all;
+#pragma unroll
+    for (uint32_t u = 0; u < kSmallPer; ++u) {
+        const uint32_t b = warp + u * kSmallWarps;
+        if (b >= p.nblocks) break;
+        const Place<P, G> at = place_of<P, G, 32>(p, __ldg(p.d.blocks + b), b);
+        Read<BITS> x;
+        if (at.whole()) {
+            read_block<P, G, BITS, true, 32>(x, p, at.grad, at.param, kListBlock, b);
+            update_block<P, BITS, true, 32>(x, p, at.param, kListBlock, at.decays, b, clip, step_size, decay, t);
+        } else {
+            read_block<P, G, BITS, false, 32>(x, p, at.grad, at.param, at.count, b);
+            update_block<P, BITS, false, 32>(x, p, at.param, at.count, at.decays, b, clip, step_size, decay, t);
+        }
+    }
+    __syncthreads();   // every warp has read the scalars
+    if (threadIdx.x == 0) {
         p.d.status->t = t;
         form_scalars(p.d, t, p.d.status->lr);
     }
@@ -1115,10 +1188,9 @@ cudaError_t norm_t(const zero1_adamw_ctx *h, const StepCall &c, uint64_t i0, uin
     return zero1::launch(zero1::zero1_adamw_norm_kernel<G, CAP>, dim3(grid), zero1::kListThreads, 0, c.stream, p);
 }
 
-template <typename P, typename G, int BITS, int CAP>
-cudaError_t update_t(const zero1_adamw_ctx *h, const StepCall &c, uint64_t i0, uint64_t i1)
+template <int CAP>
+void fill(zero1::UpdateParams<CAP> &p, const zero1_adamw_ctx *h, const StepCall &c, uint64_t i0, uint64_t i1)
 {
-    zero1::UpdateParams<CAP> p;
     for (uint64_t i = i0; i < i1; ++i)
         p.grads[i - i0] = c.grads[i], p.params[i - i0] = c.params[i], p.first[i - i0] = (uint32_t)h->first[i];
     p.d = h->d;
@@ -1147,6 +1219,13 @@ cudaError_t update_t(const zero1_adamw_ctx *h, const StepCall &c, uint64_t i0, u
     p.decay_first = h->opt.decay_before_update;
     p.eps_easy = p.eps >= 0x1p-50f && p.eps <= 0x1p50f;   // so that sqrt(v) + eps is never near the ends of fp32's range
     p.last = i1 == h->sizes.size();
+}
+
+template <typename P, typename G, int BITS, int CAP>
+cudaError_t update_t(const zero1_adamw_ctx *h, const StepCall &c, uint64_t i0, uint64_t i1)
+{
+    zero1::UpdateParams<CAP> p;
+    fill(p, h, c, i0, i1);
     p.per_warp = p.nblocks < 16ull * zero1::kWarps * (uint64_t)h->num_sms ? 1 : zero1::kUpdateBlocks;
     const uint64_t per = (uint64_t)zero1::kWarps * p.per_warp;
     uint64_t grid = (p.nblocks + per - 1) / per;
@@ -1171,6 +1250,11 @@ cudaError_t step_t(const zero1_adamw_ctx *h, const StepCall &c)
     const uint64_t count = h->sizes.size();
     cudaError_t e = cudaSuccess;
     uint32_t before = 0;
+    if (CAP == kCaps[0] && h->hp.max_norm > 0.0 && h->first.back() <= zero1::kSmallWarps * zero1::kSmallPer) {
+        zero1::UpdateParams<kCaps[0]> p;
+        fill(p, h, c, 0, count);
+        return zero1::launch(zero1::zero1_adamw_small_kernel<P, G, BITS>, dim3(1), 32 * zero1::kSmallWarps, 0, c.stream, p);
+    }
     if (h->hp.max_norm > 0.0)
         for (uint64_t i = 0; e == cudaSuccess && i < count; i += CAP)
             e = norm_t<G, CAP>(h, c, i, std::min<uint64_t>(i + CAP, count), before);

@@ -68,9 +68,9 @@ int check_shape(const zero1_ffn_shape *in, zero1_ffn_shape &s)
         if (*l.ld < l.cols || *l.ld >= (1ull << 38) || *l.ld > (1ull << 50) / (l.rows ? l.rows : 1))
             return ffail(ZERO1_EINVAL, "%s must be at least its matrix's columns, below 2^38, and times the rows at most 2^50", l.name);
     }
-    // tiles of 256 x 256 (gated: of 128 columns) in one launch
+    // tiles of 256 x 256 (gated: of 128 columns) and their slices in one launch
     const uint64_t m = (s.rows + kFfnTile - 1) / kFfnTile, h = (s.hidden + 127) / 128, w = (s.width + kFfnTile - 1) / kFfnTile;
-    if (m * h >= (1ull << 26) || m * w >= (1ull << 26)) return ffail(ZERO1_EINVAL, "rows times hidden or width is too large");
+    if (m * h >= (1ull << 26) || m * w * ((s.hidden + 32767) / 32768) + 2 * w * h * ((s.rows + 65535) / 65536) >= (1ull << 26)) return ffail(ZERO1_EINVAL, "rows times hidden or width is too large");
     return ZERO1_OK;
 }
 
@@ -117,11 +117,7 @@ uint64_t steps_of(uint64_t k) { return (k + kFfnStep - 1) / kFfnStep; }
 // A matrix's copy in the workspace, rows padded to 16 bytes.
 uint64_t copy_bytes(uint64_t rows, uint64_t cols) { return round_up(rows * round_up(cols, 8) * 2, 256); }
 
-uint64_t partial_bytes(uint64_t tiles, uint64_t steps)
-{
-    const uint64_t s = ffn_slices(tiles, steps);
-    return s > 1 ? tiles * s * kFfnPartial : 0;
-}
+uint64_t partial_bytes(uint64_t tiles, uint32_t slices) { return slices > 1 ? tiles * slices * kFfnPartial : 0; }
 
 // Tiles of the three weight gradients, which one launch takes.
 uint64_t weight_tiles(const zero1_ffn_shape &s) { return 2 * tiles_of(s.width, s.hidden) + tiles_of(s.hidden, s.width); }
@@ -139,14 +135,14 @@ uint64_t workspace_of(const zero1_ffn_shape &s, bool backward)
                  copy(s.hidden, s.width, s.ld_down);
     if (thin_rows(s, backward)) return b + 2 * copy_bytes(s.rows, s.hidden);   // h in two parts
     b += copy(s.rows, s.hidden, s.ldh);
-    uint64_t partials = partial_bytes(tiles_of(s.rows, s.width), steps_of(s.hidden));
-    if (backward) {
-        b += copy(s.rows, s.width, s.ldy) + 2 * copy_bytes(s.rows, s.hidden);
-        const uint64_t dx = partial_bytes(tiles_of(s.rows, s.width), 2 * steps_of(s.hidden));
-        const uint64_t dw = partial_bytes(weight_tiles(s), steps_of(s.rows));
-        partials = dx > dw ? dx : dw;
-    }
-    return b + partials;
+    const uint64_t out_tiles = tiles_of(s.rows, s.width);
+    if (!backward) return b + partial_bytes(out_tiles, ffn_slices(out_tiles, steps_of(s.hidden)).a);
+    b += copy(s.rows, s.width, s.ldy) + 2 * copy_bytes(s.rows, s.hidden);
+    const FfnSlices n = ffn_slices(weight_tiles(s), steps_of(s.rows), out_tiles, 2 * steps_of(s.hidden));
+    const FfnSlices without = ffn_slices(weight_tiles(s), steps_of(s.rows));   // dx not wanted
+    const uint64_t with_dx = partial_bytes(weight_tiles(s), n.a) + partial_bytes(out_tiles, n.b);
+    const uint64_t only = partial_bytes(weight_tiles(s), without.a);
+    return b + (with_dx > only ? with_dx : only);
 }
 
 // ---------------------------------------------------------------- copies
@@ -270,25 +266,44 @@ struct Call {
     }
 };
 
-void size_job(FfnParams &p, int i, uint64_t m, uint64_t n, uint64_t tile_n)
+// The next job of a launch: out (m x n, in tiles of 256 x tile_n) over `segments` times k.
+FfnJob &add_job(FfnParams &p, uint64_t m, uint64_t n, uint64_t tile_n, uint64_t k, uint32_t segments, uint32_t slices, bool a_mn,
+                bool b_mn)
 {
-    FfnJob &j = p.job[i];
+    FfnJob &j = p.job[p.jobs++];
     j.m = (uint32_t)m;
     j.n = (uint32_t)n;
     j.tiles_m = (uint32_t)((m + kFfnTile - 1) / kFfnTile);
     j.tiles_n = (uint32_t)((n + tile_n - 1) / tile_n);
-    j.first = p.tiles;
-    p.tiles += j.tiles_m * j.tiles_n;
-    p.jobs = (uint32_t)i + 1;
+    j.steps = (uint32_t)steps_of(k);
+    j.segments = segments;
+    j.slices = slices;
+    j.a_mn = a_mn;
+    j.b_mn = b_mn;
+    j.first = p.items;
+    j.joins = p.joins;
+    const uint32_t tiles = j.tiles_m * j.tiles_n;
+    p.items += tiles * slices;
+    if (slices > 1) p.joins += tiles;
+    return j;
 }
 
-FfnParams params_of(const Call &c, uint64_t k, uint32_t segments)
+// Where the partial tiles of the jobs that have some lie, one job's after another's.
+void place_partials(FfnParams &p, void *partials)
+{
+    uint32_t at = 0;
+    for (uint32_t i = 0; i < p.jobs; ++i) {
+        FfnJob &j = p.job[i];
+        j.partial = at;
+        if (j.slices > 1) at += j.tiles_m * j.tiles_n * j.slices;
+    }
+    p.partials = static_cast<float *>(partials);
+}
+
+FfnParams params_of(const Call &c)
 {
     FfnParams p;
     memset(&p, 0, sizeof p);
-    p.steps = (uint32_t)steps_of(k);
-    p.segments = segments;
-    p.slices = 1;
     p.act = c.s.activation;
     p.stall = c.s.inject_wait_timeout;
     p.errors = c.errors;
@@ -303,12 +318,6 @@ void run(Call &c, FfnParams &p, F f)
     p.follows = c.launched;
     c.check(f(p), "kernel launch");
     c.launched = true;
-}
-
-void slice(FfnParams &p, void *partials)
-{
-    p.slices = ffn_slices(p.tiles, (uint64_t)p.steps * p.segments);
-    p.partials = static_cast<float *>(partials);
 }
 
 int check_workspace(const zero1_ffn_shape &s, bool backward, const void *workspace, uint64_t bytes)
@@ -392,30 +401,31 @@ int zero1_ffn_forward(const zero1_ffn_shape *shape, const void *x, const void *w
         if (c.rc == ZERO1_OK) c.check(launch_ffn_thin(f, c.sms, c.stream), "kernel launch");
         return c.rc;
     }
-    FfnParams p = params_of(c, s.width, 1);
-    c.map(&p.job[0].a[0], ax);
-    c.map(&p.job[0].b[0], ag);
-    c.map(&p.job[0].b[1], au);
-    size_job(p, 0, s.rows, s.hidden, kFfnTile / 2);
-    c.out(p.job[0], 0, mats[4]);
-    c.out(p.job[0], 1, mats[6]);
-    c.out(p.job[0], 2, mats[7]);
+    FfnParams p = params_of(c);
+    FfnJob &first = add_job(p, s.rows, s.hidden, kFfnTile / 2, s.width, 1, 1, false, true);
+    c.map(&first.a[0], ax);
+    c.map(&first.b[0], ag);
+    c.map(&first.b[1], au);
+    c.out(first, 0, mats[4]);
+    c.out(first, 1, mats[6]);
+    c.out(first, 2, mats[7]);
     Mat ah = mats[4];
     if (!ah.aligned()) {   // written twice: TMA cannot address the caller's
         ah.ld = round_up(s.hidden, 8);
         ah.p = c.take(copy_bytes(s.rows, s.hidden));
-        p.job[0].copy = static_cast<uint16_t *>(const_cast<void *>(ah.p));
-        p.job[0].ld_copy = ah.ld;
+        first.copy = static_cast<uint16_t *>(const_cast<void *>(ah.p));
+        first.ld_copy = ah.ld;
     }
     run(c, p, [&](const FfnParams &x) { return launch_ffn_gated(x, c.sms, c.stream); });
 
-    FfnParams q = params_of(c, s.hidden, 1);
-    c.map(&q.job[0].a[0], ah);
-    c.map(&q.job[0].b[0], ad);
-    size_job(q, 0, s.rows, s.width, kFfnTile);
-    c.out(q.job[0], 0, mats[5]);
-    slice(q, c.space + c.at);
-    run(c, q, [&](const FfnParams &x) { return launch_ffn_plain(x, false, true, c.sms, c.stream); });
+    FfnParams q = params_of(c);
+    FfnJob &second = add_job(q, s.rows, s.width, kFfnTile, s.hidden, 1, ffn_slices(tiles_of(s.rows, s.width), steps_of(s.hidden)).a,
+                             false, true);
+    c.map(&second.a[0], ah);
+    c.map(&second.b[0], ad);
+    c.out(second, 0, mats[5]);
+    place_partials(q, c.space + c.at);
+    run(c, q, [&](const FfnParams &x) { return launch_ffn_plain(x, c.sms, c.stream); });
     return c.rc;
 }
 
@@ -463,40 +473,46 @@ int zero1_ffn_backward(const zero1_ffn_shape *shape, const void *dy, const void 
     c.copy_all();
     void *partials = c.space + c.at;
 
-    FfnParams p = params_of(c, s.width, 1);          // dh, and from it dgate and dup
-    c.map(&p.job[0].a[0], ady);
-    c.map(&p.job[0].b[0], ad);
-    size_job(p, 0, s.rows, s.hidden, kFfnTile);
-    c.out(p.job[0], 0, dgate);
-    c.out(p.job[0], 1, dup);
-    p.job[0].in[0] = static_cast<const uint16_t *>(gate);
-    p.job[0].in[1] = static_cast<const uint16_t *>(up);
-    p.job[0].ld_in = s.ldh;
-    p.job[0].vec_in = mats[6].aligned() && mats[7].aligned();
+    FfnParams p = params_of(c);                      // dh, and from it dgate and dup
+    FfnJob &first = add_job(p, s.rows, s.hidden, kFfnTile, s.width, 1, 1, false, false);
+    c.map(&first.a[0], ady);
+    c.map(&first.b[0], ad);
+    c.out(first, 0, dgate);
+    c.out(first, 1, dup);
+    first.in[0] = static_cast<const uint16_t *>(gate);
+    first.in[1] = static_cast<const uint16_t *>(up);
+    first.ld_in = s.ldh;
+    first.vec_in = mats[6].aligned() && mats[7].aligned();
     run(c, p, [&](const FfnParams &x) { return launch_ffn_slope(x, c.sms, c.stream); });
 
-    FfnParams w = params_of(c, s.rows, 1);           // the weights' gradients
-    const Mat a[3] = {ax, ax, ah}, b[3] = {dgate, dup, ady};
-    for (int i = 0; i < 3; ++i) {
-        c.map(&w.job[i].a[0], a[i]);
-        c.map(&w.job[i].b[0], b[i]);
-        size_job(w, i, mats[i].rows, mats[i].cols, kFfnTile);
-        c.out(w.job[i], 0, mats[i]);
-    }
-    slice(w, partials);
-    run(c, w, [&](const FfnParams &x) { return launch_ffn_plain(x, true, true, c.sms, c.stream); });
-
-    if (dx) {
-        FfnParams q = params_of(c, s.hidden, 2);
-        c.map(&q.job[0].a[0], dgate);
-        c.map(&q.job[0].b[0], ag);
-        c.map(&q.job[0].a[1], dup);
-        c.map(&q.job[0].b[1], au);
-        size_job(q, 0, s.rows, s.width, kFfnTile);
-        c.out(q.job[0], 0, mats[3]);
-        slice(q, partials);
-        run(c, q, [&](const FfnParams &x) { return launch_ffn_plain(x, false, false, c.sms, c.stream); });
-    }
+    // the gradients of the weights and of x, the longer sums first
+    FfnParams w = params_of(c);
+    const uint64_t out_tiles = tiles_of(s.rows, s.width), w_steps = steps_of(s.rows), x_steps = 2 * steps_of(s.hidden);
+    const FfnSlices n = dx ? ffn_slices(weight_tiles(s), w_steps, out_tiles, x_steps) : ffn_slices(weight_tiles(s), w_steps);
+    const auto weights = [&]() {
+        const Mat a[3] = {ax, ax, ah}, b[3] = {dgate, dup, ady};
+        for (int i = 0; i < 3; ++i) {
+            FfnJob &j = add_job(w, mats[i].rows, mats[i].cols, kFfnTile, s.rows, 1, n.a, true, true);
+            c.map(&j.a[0], a[i]);
+            c.map(&j.b[0], b[i]);
+            c.out(j, 0, mats[i]);
+        }
+    };
+    const auto input = [&]() {
+        if (!dx) return;
+        FfnJob &j = add_job(w, s.rows, s.width, kFfnTile, s.hidden, 2, n.b, false, false);
+        c.map(&j.a[0], dgate);
+        c.map(&j.b[0], ag);
+        c.map(&j.a[1], dup);
+        c.map(&j.b[1], au);
+        c.out(j, 0, mats[3]);
+    };
+    const bool input_first = x_steps / n.b > w_steps / n.a;
+    if (input_first) input();
+    weights();
+    if (!input_first) input();
+    place_partials(w, partials);
+    run(c, w, [&](const FfnParams &x) { return launch_ffn_plain(x, c.sms, c.stream); });
     return c.rc;
 }
 

@@ -12,7 +12,7 @@ namespace zero1 {
 // Tiles of 256 x 256 accumulators by pairs of blocks, 64 of K a step.
 constexpr uint32_t kFfnTile = 256;
 constexpr uint32_t kFfnStep = 64;
-constexpr uint32_t kFfnJobs = 3;
+constexpr uint32_t kFfnJobs = 4;
 constexpr uint32_t kFfnPairs = 76;            // pairs of SMs the rules below count on; results do not depend on it
 constexpr uint64_t kFfnPartial = (uint64_t)kFfnTile * kFfnTile * sizeof(float);   // bytes of one tile's partial sums
 
@@ -32,32 +32,46 @@ struct FfnJob {
     uint64_t ld_out, ld_in, ld_copy;
     uint32_t m, n;                // rows, columns of the result
     uint32_t tiles_m, tiles_n;
-    uint32_t first;               // its first tile in the launch
+    uint32_t steps, segments;     // of 64 of K in a segment; segments
+    uint32_t slices;              // parts of K that are summed apart
+    uint32_t first;               // its first item (a tile's slice) in the launch
+    uint32_t partial, joins;      // slices > 1: its first partial tile, and how many tiles earlier jobs have to join
+    uint32_t a_mn, b_mn;          // plain: rows of the operand in memory are K, its columns the result's
     uint32_t vec_out, vec_in;     // 16-byte aligned rows
 };
 
 struct FfnParams {
     FfnJob job[kFfnJobs];
-    uint32_t jobs, tiles, slices;
-    uint32_t steps, segments;     // of 64 of K in a segment
+    uint32_t jobs, items, joins;
     int act, stall;
     int follows;                  // not the first launch of its call
     float *partials;              // of slices > 1
     unsigned *errors;             // may be null
 };
 
-// In how many slices K is taken, so that few tiles still fill the pairs: as
-// many as leave every slice 8 steps (512 of K), fewer than make a second
-// round.  A long sum is taken in slices of 65,536 in any case: the tensor
-// cores cut every addition of 16 products off below the sum's last place, so
-// a sum of one sign falls short by 8e-8 of itself for each, 3.3e-4 there, an
-// eighth of a bf16 rounding.
-inline uint32_t ffn_slices(uint64_t tiles, uint64_t steps)
+// In how many slices the K of up to two kinds of tiles (`tiles` of `steps`
+// each) is taken, so that few tiles still fill the pairs: the shortest slices,
+// of at least 8 steps (512 of K), that make no second round.  A long sum is taken in
+// slices of 65,536 in any case: the tensor cores cut every addition of 16
+// products off below the sum's last place, so a sum of one sign falls short by
+// 8e-8 of itself for each, 3.3e-4 there, an eighth of a bf16 rounding.
+struct FfnSlices {
+    uint32_t a, b;
+};
+inline FfnSlices ffn_slices(uint64_t tiles_a, uint64_t steps_a, uint64_t tiles_b = 0, uint64_t steps_b = 1)
 {
-    uint64_t s = tiles ? kFfnPairs / tiles : 1;
-    if (s > steps / 8) s = steps / 8;
-    const uint64_t least = (steps * kFfnStep + 65535) / 65536;
-    return (uint32_t)(s < least ? least : s < 1 ? 1 : s);
+    const uint64_t least_a = (steps_a * kFfnStep + 65535) / 65536, least_b = (steps_b * kFfnStep + 65535) / 65536;
+    FfnSlices s{(uint32_t)least_a, (uint32_t)least_b};
+    if (tiles_a + tiles_b >= kFfnPairs) return s;
+    const uint64_t most = steps_a > steps_b ? steps_a : steps_b;
+    for (uint64_t length = 8; length < most; length += 2) {
+        const uint64_t a = (steps_a + length - 1) / length, b = (steps_b + length - 1) / length;
+        if (tiles_a * a + tiles_b * b > kFfnPairs) continue;
+        if (a > least_a) s.a = (uint32_t)a;
+        if (b > least_b) s.b = (uint32_t)b;
+        return s;
+    }
+    return s;
 }
 
 // The forward pass of at most kFfnThinRows rows (zero1_ffn_thin.cu).
@@ -80,7 +94,6 @@ cudaError_t launch_ffn_thin(const FfnThin &f, int sms, cudaStream_t stream);
 
 cudaError_t launch_ffn_gated(const FfnParams &p, int sms, cudaStream_t stream);
 cudaError_t launch_ffn_slope(const FfnParams &p, int sms, cudaStream_t stream);
-// a_cols, b_cols: the operand's rows in memory are K (and its columns those of the result).
-cudaError_t launch_ffn_plain(const FfnParams &p, bool a_cols, bool b_cols, int sms, cudaStream_t stream);
+cudaError_t launch_ffn_plain(const FfnParams &p, int sms, cudaStream_t stream);
 
 }  // namespace zero1

@@ -6,7 +6,7 @@
 //             y = h Wd
 //   backward: dh = dy Wd^T, dup = dh act(gate),
 //             dgate = dh up act'(gate)                       (one launch)
-//             dWg = x^T dgate, dWu = x^T dup, dWd = h^T dy   (one launch)
+//             dWg = x^T dgate, dWu = x^T dup, dWd = h^T dy,
 //             dx = dgate Wg^T + dup Wu^T                     (one launch)
 //
 // Operands are bf16 as they lie in memory (K- or MN-major, no transposed
@@ -48,31 +48,30 @@ __device__ __forceinline__ uint32_t bf16_desc(bool a_mn, bool b_mn)
     return tc::instr_desc(kFfnTile, kFfnTile, a_mn, b_mn) | (1u << 7) | (1u << 10);
 }
 
-// Where an item's tile lies: items are tiles, `slices` of K of each one after
-// another, in groups of 8 tile rows (all columns of a group before the next),
-// so that the pairs at work share operands in L2.
+// Where an item's tile lies: items are tiles, the slices of K of each one
+// after another, in groups of 8 tile rows (all columns of a group before the
+// next), so that the pairs at work share operands in L2.
 struct Item {
-    uint32_t job, row, col, begin, end;             // k steps [begin, end) over all segments
+    uint32_t job, row, col, begin, end, partial;    // k steps [begin, end) over all segments
 };
 template <int MODE>
 __device__ __forceinline__ Item item_of(const FfnParams &p, uint32_t i)
 {
     Item t;
-    const uint32_t slice = i % p.slices, tile = i / p.slices;
     t.job = 0;
-    while (t.job + 1 < p.jobs && tile >= p.job[t.job + 1].first) ++t.job;
+    while (MODE == kFfnPlain && t.job + 1 < p.jobs && i >= p.job[t.job + 1].first) ++t.job;
     const FfnJob &j = p.job[t.job];
-    const uint32_t at = tile - j.first, span = 8 * j.tiles_n, group = at / span;
+    const uint32_t local = i - j.first, slice = local % j.slices, at = local / j.slices;
+    const uint32_t span = 8 * j.tiles_n, group = at / span;
     const uint32_t height = min(8u, j.tiles_m - group * 8), in = at - group * span;
     t.row = (group * 8 + in % height) * kFfnTile;
     t.col = in / height * (MODE == kFfnGated ? kFfnTile / 2 : kFfnTile);
-    const uint32_t steps = p.steps * p.segments;
-    t.begin = (uint32_t)((uint64_t)steps * slice / p.slices);
-    t.end = (uint32_t)((uint64_t)steps * (slice + 1) / p.slices);
+    const uint32_t steps = j.steps * j.segments;
+    t.begin = (uint32_t)((uint64_t)steps * slice / j.slices);
+    t.end = (uint32_t)((uint64_t)steps * (slice + 1) / j.slices);
+    t.partial = j.partial + local;
     return t;
 }
-
-// --------------------------------------------------------------- epilogue
 
 // How a warp's patch meets global memory: 16-byte pieces of a patch wholly
 // inside the matrix, the same near an edge, or single entries.
@@ -230,7 +229,7 @@ __device__ __forceinline__ void write_narrow(uint16_t *base, const Patch &p, uin
 // Per pair: one thread of each block loads operands (TMA), one thread of the
 // first issues the products, sixteen warps of each block take its 128 rows of a
 // finished tile out of one accumulator while the other fills.
-template <bool A_MN, bool B_MN, int MODE>
+template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     zero1_ffn_gemm_kernel(const __grid_constant__ FfnParams p)
 {
@@ -261,7 +260,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     const uint32_t tmem = sh.tmem;
     ptx::launch_dependents();
     ptx::grid_dependency_wait();   // what the launch before wrote, and what it still reads
-    const uint32_t items = p.tiles * p.slices, pairs = gridDim.x / 2, pair = blockIdx.x / 2;
+    const uint32_t items = p.items, pairs = gridDim.x / 2, pair = blockIdx.x / 2;
 
     if (threadIdx.x == 0) {
         // ---- loads
@@ -270,22 +269,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         for (uint32_t i = pair; ok && i < items; i += pairs) {
             const Item t = item_of<MODE>(p, i);
             const FfnJob &j = p.job[t.job];
+            const bool a_mn = MODE == kFfnPlain && j.a_mn, b_mn = MODE == kFfnGated || (MODE == kFfnPlain && j.b_mn);
             const int row = (int)(t.row + rank * 128);
             const int col = (int)(t.col + (MODE == kFfnGated ? 0 : rank * 128));
             for (uint32_t s = t.begin; s < t.end; ++s) {
                 const uint32_t stage = issued % kStages;
                 if (issued >= kStages) ok = tc::pair_wait(&sh.empty[stage], (issued / kStages - 1) & 1u, abort, errors);
                 if (!ok) break;
-                const uint32_t seg = s >= p.steps;
-                const int k = (int)((s - seg * p.steps) * kFfnStep);
+                const uint32_t seg = s >= j.steps;
+                const int k = (int)((s - seg * j.steps) * kFfnStep);
                 const CUtensorMap *ma = &j.a[seg], *mb = &j.b[MODE == kFfnGated ? rank : seg];
                 if (rank == 0) ptx::mbar_arrive_expect_tx(&sh.full[stage], 2 * kStageBytes);
                 const uint32_t bar = tc::map_to(tc::smem_u32(&sh.full[stage]), 0), dst = ring + stage * kStageBytes;
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     const int r = row + 64 * b, c = col + 64 * b;
-                    tc::tma_box_pair(dst + b * kBox, ma, A_MN ? r : k, A_MN ? k : r, 0, bar);
-                    tc::tma_box_pair(dst + (2 + b) * kBox, mb, B_MN ? c : k, B_MN ? k : c, 0, bar);
+                    tc::tma_box_pair(dst + b * kBox, ma, a_mn ? r : k, a_mn ? k : r, 0, bar);
+                    tc::tma_box_pair(dst + (2 + b) * kBox, mb, b_mn ? c : k, b_mn ? k : c, 0, bar);
                 }
                 ++issued;
             }
@@ -295,10 +295,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         // ---- products
         uint32_t taken = 0, used = 0;   // stages, accumulators
         bool ok = true;
-        constexpr uint32_t kAStep = A_MN ? 2048 >> 4 : 32 >> 4, kBStep = B_MN ? 2048 >> 4 : 32 >> 4;   // 16 of K
-        const uint32_t idesc = bf16_desc(A_MN, B_MN);
         for (uint32_t i = pair; ok && i < items; i += pairs, ++used) {
             const Item t = item_of<MODE>(p, i);
+            const FfnJob &j = p.job[t.job];
+            const bool a_mn = MODE == kFfnPlain && j.a_mn, b_mn = MODE == kFfnGated || (MODE == kFfnPlain && j.b_mn);
+            const uint64_t a_step = tc::k16_step(a_mn), b_step = tc::k16_step(b_mn);
+            const uint32_t idesc = bf16_desc(a_mn, b_mn);
             const uint32_t acc = used & 1, d = tmem + acc * kFfnTile;
             if (used >= 2) {
                 if (!(ok = tc::pair_wait(&sh.acc_empty[acc], (used / 2 - 1) & 1u, abort, errors))) break;
@@ -309,10 +311,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
                 if (!(ok = tc::pair_wait(&sh.full[stage], (taken / kStages) & 1u, abort, errors))) break;
                 tc::fence_after_sync();
                 const uint32_t src = ring + stage * kStageBytes;
-                const uint64_t a = tc::smem_desc(src, A_MN), b = tc::smem_desc(src + 2 * kBox, B_MN);
+                const uint64_t a = tc::smem_desc(src, a_mn), b = tc::smem_desc(src + 2 * kBox, b_mn);
 #pragma unroll
                 for (uint32_t q = 0; q < kFfnStep / 16; ++q)
-                    tc::mma_f16(d, a + q * kAStep, b + q * kBStep, idesc, s > t.begin || q > 0);
+                    tc::mma_f16(d, a + q * a_step, b + q * b_step, idesc, s > t.begin || q > 0);
                 tc::mma_commit(&sh.empty[stage]);
                 ++taken;
             }
@@ -370,9 +372,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
                     else f(ActOf<kSingles>{});
                 };
                 if constexpr (MODE == kFfnPlain) {
-                    if (p.slices > 1) {
+                    if (j.slices > 1) {
                         put_rows(mem, x);
-                        float *sums = p.partials + (uint64_t)i * (kFfnTile * kFfnTile) + (row - t.row) * kFfnTile + (col - t.col) + c +
+                        float *sums = p.partials + (uint64_t)t.partial * (kFfnTile * kFfnTile) + (row - t.row) * kFfnTile + (col - t.col) + c +
                                       (lane >> 2) * kFfnTile + (lane & 3) * 8;
 #pragma unroll
                         for (uint32_t q = 0; q < 4; ++q) {
@@ -481,16 +483,19 @@ __global__ void __launch_bounds__(256) zero1_ffn_join_kernel(const __grid_consta
     ptx::launch_dependents();
     ptx::grid_dependency_wait();
     const uint32_t tile = blockIdx.x / (kFfnTile / 8), lane = threadIdx.x & 31;
-    const Item t = item_of<kFfnPlain>(p, tile * p.slices);
-    const FfnJob &j = p.job[t.job];
+    uint32_t job = 0;   // the last that begins here and has something to join
+    for (uint32_t k = 1; k < p.jobs; ++k)
+        if (p.job[k].slices > 1 && (tile >= p.job[k].joins || p.job[job].slices == 1)) job = k;
+    const FfnJob &j = p.job[job];
+    const Item t = item_of<kFfnPlain>(p, j.first + (tile - j.joins) * j.slices);
     const uint32_t r = blockIdx.x % (kFfnTile / 8) * 8 + (threadIdx.x >> 5), row = t.row + r, col = t.col + lane * 8;
     if (row >= j.m || col >= j.n) return;
     float v[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = 0.f;
-    const float *src = p.partials + (uint64_t)tile * p.slices * (kFfnTile * kFfnTile) + r * kFfnTile + lane * 8;
+    const float *src = p.partials + (uint64_t)t.partial * (kFfnTile * kFfnTile) + r * kFfnTile + lane * 8;
 #pragma unroll 4
-    for (uint32_t s = 0; s < p.slices; ++s, src += kFfnTile * kFfnTile) {
+    for (uint32_t s = 0; s < j.slices; ++s, src += kFfnTile * kFfnTile) {
         const float4 a = reinterpret_cast<const float4 *>(src)[0], b = reinterpret_cast<const float4 *>(src)[1];
         v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w, v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
     }
@@ -505,38 +510,28 @@ __global__ void __launch_bounds__(256) zero1_ffn_join_kernel(const __grid_consta
     }
 }
 
-template <bool A_MN, bool B_MN, int MODE>
+template <int MODE>
 cudaError_t gemm(const FfnParams &p, int sms, cudaStream_t stream)
 {
-    const auto kernel = zero1_ffn_gemm_kernel<A_MN, B_MN, MODE>;
+    const auto kernel = zero1_ffn_gemm_kernel<MODE>;
     cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), kGemmSmem);
     if (e != cudaSuccess) return e;
-    const uint32_t pairs = (uint32_t)sms / 2, items = p.tiles * p.slices;
-    const dim3 grid(2 * (items < pairs ? items : pairs));
+    const uint32_t pairs = (uint32_t)sms / 2;
+    const dim3 grid(2 * (p.items < pairs ? p.items : pairs));
     // after another kernel of the same call it may begin while that one ends
     e = p.follows ? launch_early(kernel, grid, kGemmThreads, kGemmSmem, stream, p)
                   : launch(kernel, grid, kGemmThreads, kGemmSmem, stream, p);
-    if (e == cudaSuccess && p.slices > 1)
-        e = launch_early(zero1_ffn_join_kernel, dim3(p.tiles * (kFfnTile / 8)), 256, 0, stream, p);
+    if (e == cudaSuccess && p.joins)
+        e = launch_early(zero1_ffn_join_kernel, dim3(p.joins * (kFfnTile / 8)), 256, 0, stream, p);
     return e;
 }
 
 }  // namespace
 
-cudaError_t launch_ffn_gated(const FfnParams &p, int sms, cudaStream_t stream)
-{
-    return gemm<false, true, kFfnGated>(p, sms, stream);
-}
+cudaError_t launch_ffn_gated(const FfnParams &p, int sms, cudaStream_t stream) { return gemm<kFfnGated>(p, sms, stream); }
 
-cudaError_t launch_ffn_slope(const FfnParams &p, int sms, cudaStream_t stream)
-{
-    return gemm<false, false, kFfnSlope>(p, sms, stream);
-}
+cudaError_t launch_ffn_slope(const FfnParams &p, int sms, cudaStream_t stream) { return gemm<kFfnSlope>(p, sms, stream); }
 
-cudaError_t launch_ffn_plain(const FfnParams &p, bool a_cols, bool b_cols, int sms, cudaStream_t stream)
-{
-    if (a_cols) return gemm<true, true, kFfnPlain>(p, sms, stream);
-    return b_cols ? gemm<false, true, kFfnPlain>(p, sms, stream) : gemm<false, false, kFfnPlain>(p, sms, stream);
-}
+cudaError_t launch_ffn_plain(const FfnParams &p, int sms, cudaStream_t stream) { return gemm<kFfnPlain>(p, sms, stream); }
 
 }  // namespace zero1

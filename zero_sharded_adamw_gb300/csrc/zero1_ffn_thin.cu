@@ -260,8 +260,25 @@ uint32_t ranks_of(uint32_t tiles, uint32_t steps, uint32_t slots, uint32_t extra
     return best;
 }
 
+// Whether a stream may use a part of the SMs only (zero1_sm_partition): then a
+// cluster has to be asked for, which takes 2 us of a call that takes 10.
+bool partitioned(cudaStream_t stream)
+{
+    typedef CUresult (*Fn)(CUstream, CUgreenCtx *);
+    static const Fn fn = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuStreamGetGreenCtx", &f, 12040, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<Fn>(f);
+    }();
+    CUgreenCtx part = nullptr;
+    return !fn || fn(reinterpret_cast<CUstream>(stream), &part) != CUDA_SUCCESS || part != nullptr;
+}
+
 template <int N, bool GATED>
-cudaError_t thin_t(ThinParams &p, int sms, cudaStream_t stream)
+cudaError_t thin_t(ThinParams &p, int sms, bool part, cudaStream_t stream)
 {
     using S = Thin<N, GATED>;
     const auto kernel = zero1_ffn_thin_kernel<N, GATED>;
@@ -282,7 +299,7 @@ cudaError_t thin_t(ThinParams &p, int sms, cudaStream_t stream)
         attr[0].val.clusterDim.x = ranks;
         cfg.gridDim = dim3(tiles * ranks);
         cfg.numAttrs = 1;
-        if (ranks == 1) break;
+        if (ranks == 1 || !part) break;
         int fit = 0;   // an SM partition may hold no cluster of this size
         e = cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg);
         if (e != cudaSuccess) return e;
@@ -293,12 +310,12 @@ cudaError_t thin_t(ThinParams &p, int sms, cudaStream_t stream)
 }
 
 template <bool GATED>
-cudaError_t thin(ThinParams &p, int sms, cudaStream_t stream)
+cudaError_t thin(ThinParams &p, int sms, bool part, cudaStream_t stream)
 {
-    if (p.rows <= 16) return thin_t<16, GATED>(p, sms, stream);
-    if (p.rows <= 32) return thin_t<32, GATED>(p, sms, stream);
-    if (p.rows <= 64) return thin_t<64, GATED>(p, sms, stream);
-    return thin_t<128, GATED>(p, sms, stream);
+    if (p.rows <= 16) return thin_t<16, GATED>(p, sms, part, stream);
+    if (p.rows <= 32) return thin_t<32, GATED>(p, sms, part, stream);
+    if (p.rows <= 64) return thin_t<64, GATED>(p, sms, part, stream);
+    return thin_t<128, GATED>(p, sms, part, stream);
 }
 
 }  // namespace
@@ -321,7 +338,8 @@ cudaError_t launch_ffn_thin(const FfnThin &f, int sms, cudaStream_t stream)
     p.vec = f.vec[0];
     p.stall = f.stall;
     p.errors = f.errors;
-    cudaError_t e = thin<true>(p, sms, stream);
+    const bool part = partitioned(stream);
+    cudaError_t e = thin<true>(p, sms, part, stream);
     if (e != cudaSuccess) return e;
     p.wide[0] = f.w_down;
     p.narrow = f.h;
@@ -330,7 +348,7 @@ cudaError_t launch_ffn_thin(const FfnThin &f, int sms, cudaStream_t stream)
     p.vec = f.vec[1];
     p.n = f.width;
     p.steps = (f.hidden + 63) / 64;
-    return thin<false>(p, sms, stream);
+    return thin<false>(p, sms, part, stream);
 }
 
 }  // namespace zero1

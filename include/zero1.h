@@ -794,7 +794,7 @@ int zero1_ffn_backward(const zero1_ffn_shape *shape, const void *dy, const void 
  * The AdamW step for a model whose parameters are a list of tensors rather
  * than one flat buffer over W ranks: one call steps them all, in two launches
  * (the gradients' norm and the update; one without clipping, or for at most
- * 16,384 entries, rounded up to 256 a tensor, in 32 tensors), whatever their
+ * 8,192 entries, rounded up to 256 a tensor, in 32 tensors), whatever their
  * number up to 1,600 (and two more for each 1,600 beyond).
  *
  * Moments are fp32 or 8 bits.  The caller owns all state, in buffers that

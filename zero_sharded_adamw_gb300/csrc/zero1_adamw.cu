@@ -54,7 +54,7 @@ constexpr int kListThreads = 256;
 constexpr uint32_t kWarps = kListThreads / 32;
 constexpr uint32_t kUpdateBlocks = 4;     // blocks of a warp of the update, fp32 moments (they are unrolled)
 constexpr uint32_t kStagedBlocks = 8;     // ... with 8 bits (16: 374 us in place of 366, 32: 392, all at once: 417)
-constexpr uint32_t kNormBlocks = 4;       // ... of the norm, at a time
+constexpr uint32_t kNormBlocks = 8;       // ... of the norm, at a time
 constexpr float kMTop = 61439.f, kRTop = 63487.f;       // f(127, 3) - 1, f(255, 4) - 1
 constexpr uint32_t kHeldLow = 27u << 23;                // 2^-100: a block whose largest value is smaller is all zeros
 constexpr uint32_t kInf = 0x7F800000u;
@@ -387,16 +387,15 @@ struct Squares {
 constexpr float kSumHigh = 1.3292279957849159e36f, kSumLow = 8.0779356694631609e-28f;   // 2^120, 2^-90
 
 // Sum over the block in a fixed order; valid on thread 0.
-template <uint32_t WARPS = kWarps>
 __device__ __forceinline__ double sum_block(double v)
 {
-    __shared__ double part[WARPS];
+    __shared__ double part[kWarps];
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
     double s = 0.0;
     if (threadIdx.x == 0)
-        for (uint32_t i = 0; i < WARPS; ++i) s += part[i];
+        for (uint32_t i = 0; i < kWarps; ++i) s += part[i];
     __syncthreads();
     return s;
 }
@@ -741,18 +740,21 @@ __global__ void __launch_bounds__(kListThreads, 4) zero1_adamw_update_kernel(con
     const ListStatus *status = p.d.status;
     const float step_size = status->step_size, decay = status->decay;
     const unsigned long long t = status->t + 1;
+    // After a norm the last blocks come first: their gradients are still in L2 (the GPT-2-small list 577 to 569 us;
+    // with 8-bit moments, whose update waits for its arithmetic as much, 610 to 616).
+    const auto place = [&](uint64_t b) { return p.block0 + (BITS == 32 && p.clipped ? p.nblocks - 1 - b : b); };
     if constexpr (BITS == 8) {
         extern __shared__ __align__(16) unsigned char raw[];
         using S = Staged<P, G>;
         const uint32_t mine = ptx::smem_u32(raw) + (threadIdx.x >> 5) * 2 * S::kBytes;
         const uint64_t stride = (uint64_t)gridDim.x * kWarps;
         uint64_t b = (uint64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-        const uint32_t *words = p.d.blocks + p.block0;
-        uint32_t word = b < p.nblocks ? __ldg(words + b) : 0u, next = b + stride < p.nblocks ? __ldg(words + b + stride) : 0u;
+        const uint32_t *words = p.d.blocks;
+        uint32_t word = b < p.nblocks ? __ldg(words + place(b)) : 0u, next = b + stride < p.nblocks ? __ldg(words + place(b + stride)) : 0u;
         float2 scale = make_float2(0.f, 0.f), next_scale = scale;
         const auto copy = [&](uint64_t which, uint32_t w, uint32_t buffer, float2 &s) {
             if (which < p.nblocks) {
-                const uint64_t block = p.block0 + which;
+                const uint64_t block = place(which);
                 const Place<P, G> at = place_of<P, G, CAP>(p, w, block);
                 s = p.scales[block];
                 if (at.whole())
@@ -766,10 +768,10 @@ __global__ void __launch_bounds__(kListThreads, 4) zero1_adamw_update_kernel(con
         const float clip = p.clipped ? __ldcg(&status->clip) : 1.f;
 #pragma unroll 1
         for (uint32_t i = 0; b < p.nblocks; ++i, b += stride) {
-            const uint32_t after = b + 2 * stride < p.nblocks ? __ldg(words + b + 2 * stride) : 0u;
+            const uint32_t after = b + 2 * stride < p.nblocks ? __ldg(words + place(b + 2 * stride)) : 0u;
             copy(b + stride, next, (i + 1) & 1, next_scale);
             asm volatile("cp.async.wait_group 1;" ::: "memory");
-            const uint64_t block = p.block0 + b;
+            const uint64_t block = place(b);
             const Place<P, G> at = place_of<P, G, CAP>(p, word, block);
             Read<BITS> x;
             if (at.whole()) {
@@ -786,13 +788,13 @@ __global__ void __launch_bounds__(kListThreads, 4) zero1_adamw_update_kernel(con
         uint32_t word[kUpdateBlocks];
 #pragma unroll
         for (uint32_t u = 0; u < kUpdateBlocks; ++u)
-            word[u] = u < p.per_warp && b0 + u * kWarps < p.nblocks ? __ldg(p.d.blocks + p.block0 + b0 + u * kWarps) : 0u;
+            word[u] = u < p.per_warp && b0 + u * kWarps < p.nblocks ? __ldg(p.d.blocks + place(b0 + u * kWarps)) : 0u;
         ptx::grid_dependency_wait();   // for the norm
         const float clip = p.clipped ? __ldcg(&status->clip) : 1.f;
 #pragma unroll
         for (uint32_t u = 0; u < kUpdateBlocks; ++u) {
             if (u >= p.per_warp || b0 + u * kWarps >= p.nblocks) break;
-            const uint64_t block = p.block0 + b0 + u * kWarps;
+            const uint64_t block = place(b0 + u * kWarps);
             const Place<P, G> at = place_of<P, G, CAP>(p, word[u], block);
             Read<BITS> x;
             if (at.whole()) {
@@ -811,67 +813,62 @@ __global__ void __launch_bounds__(kListThreads, 4) zero1_adamw_update_kernel(con
     }
 }
 
-// A clipped step of a short list in one launch: one block keeps all gradients
-// in registers between the norm and the update (4,096 bf16 entries in two
-// tensors: 7 us, 10 with two launches).
-constexpr uint32_t kSmallWarps = 32, kSmallPer = 2;
+// A clipped step of a short list in one launch: a block of 256 entries to a
+// warp, which reads all of it before the norm is formed.
+constexpr uint32_t kSmallWarps = 32;
 template <typename P, typename G, int BITS>
 __global__ void __launch_bounds__(32 * kSmallWarps) zero1_adamw_small_kernel(const __grid_constant__ UpdateParams<32> p)
 {
     constexpr bool kExact = sizeof(G) == 2;
+    __shared__ double sums[kSmallWarps];
     __shared__ float clip_of_all;
     const ListStatus *status = p.d.status;
     const float step_size = status->step_size, decay = status->decay;
     const unsigned long long t = status->t + 1;
-    const uint32_t warp = threadIdx.x >> 5;
-    const Two one = p.one, minus = mul(p.one, two(-1.f, -1.f));
+    const uint32_t b = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool here = b < p.nblocks;
+    Place<P, G> at{};
+    Read<BITS> x;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x.g[k] = 0.f;
+    if (here) {
+        at = place_of<P, G, 32>(p, __ldg(p.d.blocks + b), b);
+        if (at.whole())
+            read_block<P, G, BITS, true, 32>(x, p, at.grad, at.param, kListBlock, b);
+        else
+            read_block<P, G, BITS, false, 32>(x, p, at.grad, at.param, at.count, b);
+    }
+    const Two minus = mul(p.one, two(-1.f, -1.f));
     Squares ss;
-    float kept[8 * kSmallPer] = {};
     uint32_t any = 0;
 #pragma unroll
-    for (uint32_t u = 0; u < kSmallPer; ++u) {
-        const uint32_t b = warp + u * kSmallWarps;
-        if (b >= p.nblocks) break;
-        const Place<P, G> at = place_of<P, G, 32>(p, __ldg(p.d.blocks + b), b);
-        float g[8];
-        if (at.whole())
-            get8<true>(g, at.grad, kListBlock);
-        else
-            get8<false>(g, at.grad, at.count);
-#pragma unroll
-        for (int k = 0; k < 8; k += 2) {
-            any |= __float_as_uint(g[k]) | __float_as_uint(g[k + 1]);
-            ss.add2<kExact>(two(g[k], g[k + 1]), one, minus);
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) kept[u * 8 + k] = g[k];
+    for (int k = 0; k < 8; k += 2) {
+        any |= __float_as_uint(x.g[k]) | __float_as_uint(x.g[k + 1]);
+        ss.add2<kExact>(two(x.g[k], x.g[k + 1]), p.one, minus);
     }
     const float size = ss.size();
-    double mine = ss.total();
+    double sum = ss.total();
     if (!(size < kSumHigh) || (size < kSumLow && any != 0)) {
-        mine = 0.0;
+        sum = 0.0;
 #pragma unroll
-        for (uint32_t k = 0; k < 8 * kSmallPer; ++k) mine += (double)kept[k] * (double)kept[k];
+        for (int k = 0; k < 8; ++k) sum += (double)x.g[k] * (double)x.g[k];
     }
-    const double sum = sum_block<kSmallWarps>(mine);
-    if (threadIdx.x == 0) clip_of_all = finish_norm(p.d, sum);
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+    if (lane == 0) sums[b] = sum;
     __syncthreads();
-    const float clip = clip_of_all;
-#pragma unroll
-    for (uint32_t u = 0; u < kSmallPer; ++u) {
-        const uint32_t b = warp + u * kSmallWarps;
-        if (b >= p.nblocks) break;
-        const Place<P, G> at = place_of<P, G, 32>(p, __ldg(p.d.blocks + b), b);
-        Read<BITS> x;
-        if (at.whole()) {
-            read_block<P, G, BITS, true, 32>(x, p, at.grad, at.param, kListBlock, b);
-            update_block<P, BITS, true, 32>(x, p, at.param, kListBlock, at.decays, b, clip, step_size, decay, t);
-        } else {
-            read_block<P, G, BITS, false, 32>(x, p, at.grad, at.param, at.count, b);
-            update_block<P, BITS, false, 32>(x, p, at.param, at.count, at.decays, b, clip, step_size, decay, t);
-        }
+    if (b == 0) {
+        sum = sums[lane];
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+        if (lane == 0) clip_of_all = finish_norm(p.d, sum);
     }
-    __syncthreads();   // every warp has read the scalars
+    __syncthreads();   // (every warp has read the scalars, too)
+    const float clip = clip_of_all;
+    if (here) {
+        if (at.whole())
+            update_block<P, BITS, true, 32>(x, p, at.param, kListBlock, at.decays, b, clip, step_size, decay, t);
+        else
+            update_block<P, BITS, false, 32>(x, p, at.param, at.count, at.decays, b, clip, step_size, decay, t);
+    }
     if (threadIdx.x == 0) {
         p.d.status->t = t;
         form_scalars(p.d, t, p.d.status->lr);
@@ -986,11 +983,11 @@ struct FreeAdamw {
     }
 };
 
-// Blocks of a norm launch: eight of 256 threads an SM, or one for each 32 blocks of the list.
+// Blocks of a norm launch: the four an SM that run at once, or one for each 64 blocks of the list.
 uint32_t norm_grid(uint64_t nblocks, int sms)
 {
     const uint64_t need = (nblocks + zero1::kWarps * zero1::kNormBlocks - 1) / (zero1::kWarps * zero1::kNormBlocks);
-    return (uint32_t)std::min<uint64_t>(need, 8ull * (uint64_t)sms);
+    return (uint32_t)std::min<uint64_t>(need, 4ull * (uint64_t)sms);
 }
 
 // Tensors whose pointers one launch holds: kernel arguments are 32,764 bytes
@@ -1250,7 +1247,7 @@ cudaError_t step_t(const zero1_adamw_ctx *h, const StepCall &c)
     const uint64_t count = h->sizes.size();
     cudaError_t e = cudaSuccess;
     uint32_t before = 0;
-    if (CAP == kCaps[0] && h->hp.max_norm > 0.0 && h->first.back() <= zero1::kSmallWarps * zero1::kSmallPer) {
+    if (CAP == kCaps[0] && h->hp.max_norm > 0.0 && h->first.back() <= zero1::kSmallWarps) {
         zero1::UpdateParams<kCaps[0]> p;
         fill(p, h, c, 0, count);
         return zero1::launch(zero1::zero1_adamw_small_kernel<P, G, BITS>, dim3(1), 32 * zero1::kSmallWarps, 0, c.stream, p);

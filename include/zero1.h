@@ -754,8 +754,8 @@ typedef struct zero1_ffn_shape {
 } zero1_ffn_shape;
 
 /* Host-only: the bytes of workspace a forward (backward = 0) or backward call
- * of this shape needs: copies of operands (see above), h (forward, at most 128
- * rows) or partial sums where few tiles share a long sum, and in the backward
+ * of this shape needs: copies of operands (see above), h in parts (forward, at
+ * most 128 rows) or partial sums where few tiles share a long sum, and in the backward
  * pass dgate and dup.
  * Errors: ZERO1_EINVAL. */
 int zero1_ffn_workspace(const zero1_ffn_shape *shape, int backward, uint64_t *bytes);
@@ -768,7 +768,8 @@ int zero1_ffn_workspace(const zero1_ffn_shape *shape, int backward, uint64_t *by
  *     be kept;
  *   errors: optional device word (NULL = none); bit 0 is set if a kernel
  *     wait gave up (1 s limit), in which case the outputs are not valid.
- * No output may share an entry with another buffer of the call.  rows = 0
+ * No output may share an entry with another buffer of the call, and none may lie
+ * in the workspace.  rows = 0
  * does nothing.  Asynchronous on `stream`; allocates nothing; may be captured.
  * Errors: ZERO1_EINVAL, ZERO1_EALIGN, ZERO1_ECUDA. */
 int zero1_ffn_forward(const zero1_ffn_shape *shape, const void *x, const void *w_gate, const void *w_up,

@@ -416,6 +416,7 @@ def test_refusals():
                       (args(param_ptrs=[None, c.params[1]]), "NULL"),
                       (args(master=None), "master"), (args(scales=None), "scales"), (args(m=None), "NULL"),
                       (args(m=c.m.float()), "uint8"), (args(scales=c.scales[:-1]), "elements"),
+                      (args(v=c.m), "share memory"), (args(scales=c.master[:c.scales.numel()]), "share memory"),
                       (args(master=c.master.data_ptr() + 4), "aligned"),
                       (args(grad_ptrs=[c.grads[0].data_ptr() + 1, c.grads[1]]), "aligned")):
         with pytest.raises(z.Zero1Error, match=word):
@@ -425,6 +426,10 @@ def test_refusals():
         c.opt.step(z.PtrTable([c.grads[0][:299], c.grads[1]]), c.params, c.master, c.m, c.v, c.scales)
     with pytest.raises(z.Zero1Error, match="elements"):
         c.opt.moments(c.m, c.v, c.scales, torch.empty(10, device="cuda"))
+    big = torch.zeros(2 * c.n, device="cuda")
+    for outs in ((big[:c.n], big[256:]), (c.scales.data_ptr(), None)):
+        with pytest.raises(z.Zero1Error, match="share"):
+            c.opt.moments(c.m, c.v, c.scales, *outs)
     with pytest.raises(z.Zero1Error, match="lr"):
         c.opt.set_lr(-1.0)
     f = Case([10], "f32", "f32", hp=z.Hparams(max_norm=0.0))

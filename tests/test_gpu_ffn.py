@@ -150,9 +150,19 @@ def test_long_sums():
     b.check_backward()
 
 
-def test_wide_hidden_sums():
+@pytest.mark.parametrize("rows", [5, 130])
+def test_wide_hidden_sums(rows):
     """A hidden size past 65,536: y and dx in slices."""
-    b = Block(130, 24, 70000)
+    b = Block(rows, 24, 70000)
+    b.forward()
+    b.check_forward()
+    b.backward()
+    b.check_backward()
+
+
+@pytest.mark.parametrize("rows,width,hidden", [(7, 65536, 40), (40, 65000, 16), (130, 65536, 8), (7, 24, 65536)])
+def test_widest(rows, width, hidden):
+    b = Block(rows, width, hidden)
     b.forward()
     b.check_forward()
     b.backward()
@@ -309,9 +319,10 @@ def test_gradient_against_differences():
         assert abs(diff - float((g * d).sum())) <= 6 * 2 * NORM * float(g.norm()), key
 
 
-def test_a_wait_that_runs_out_is_reported():
-    b = Block(300, 64, 64)
-    s = z.FfnShape(300, 64, 64, inject_wait_timeout=True)
+@pytest.mark.parametrize("rows", [5, 300])
+def test_a_wait_that_runs_out_is_reported(rows):
+    b = Block(rows, 64, 64)
+    s = z.FfnShape(rows, 64, 64, inject_wait_timeout=True)
     z.zero1_ffn_forward(s, b.x.t, b.w_gate.t, b.w_up.t, b.w_down.t, b.gate.t, b.up.t, b.h.t, b.y.t, b.space(False), None,
                         b.errors)
     assert int(b.errors) == 1
@@ -333,6 +344,9 @@ def test_refusals():
         with pytest.raises(z.Zero1Error, match=word):
             z.zero1_ffn_forward(**{**args, **kw})
     assert bool(b.y.t.isnan().all())
+    space = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    with pytest.raises(z.Zero1Error, match="lies in the workspace"):
+        z.zero1_ffn_forward(**{**args, "y": space[4096:4096 + 40 * 64 * 2].view(BF).view(40, 64), "workspace": space})
     odd = Block(40, 65, 72)
     with pytest.raises(z.Zero1Error, match="workspace holds"):
         z.zero1_ffn_forward(odd.shape, odd.x.t, odd.w_gate.t, odd.w_up.t, odd.w_down.t, None, None, odd.h.t, odd.y.t,

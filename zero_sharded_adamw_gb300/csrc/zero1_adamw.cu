@@ -1275,6 +1275,16 @@ cudaError_t step_bits(const zero1_adamw_ctx *h, const StepCall &c)
     return h->opt.state_bits == 8 ? step_cap<P, G, 8>(h, c) : step_cap<P, G, 32>(h, c);
 }
 
+struct Bytes {
+    const void *p;
+    uint64_t n;
+};
+bool apart(Bytes a, Bytes b)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return !a.p || !b.p || x + a.n <= y || y + b.n <= x;
+}
+
 int check_state(const zero1_adamw_ctx *h, const void *master, const void *m, const void *v, const void *scales)
 {
     if ((master != nullptr) != (h->opt.param_dtype == ZERO1_DTYPE_BF16))
@@ -1283,7 +1293,11 @@ int check_state(const zero1_adamw_ctx *h, const void *master, const void *m, con
     if ((scales != nullptr) != (h->opt.state_bits == 8)) return afail(ZERO1_EINVAL, "scales go with moments in 8 bits, and only with them");
     if (!on16(master) || !on16(m) || !on16(v) || !on16(scales))
         return afail(ZERO1_EALIGN, "master, m, v and scales must be 16-byte aligned");
-    return ZERO1_OK;
+    const uint64_t n = h->first.back() * kListBlock, each = h->opt.state_bits == 8 ? n : 4 * n;
+    if (apart({master, 4 * n}, {m, each}) && apart({master, 4 * n}, {v, each}) && apart({m, each}, {v, each}) &&
+        apart({scales, n / 32}, {m, each}) && apart({scales, n / 32}, {v, each}) && apart({scales, n / 32}, {master, 4 * n}))
+        return ZERO1_OK;
+    return afail(ZERO1_EINVAL, "two of master, m, v and scales share memory");
 }
 
 }  // namespace
@@ -1353,8 +1367,12 @@ int zero1_adamw_moments(zero1_adamw_handle h, const void *m, const void *v, cons
     if (!m || !v || !scales) return afail(ZERO1_EINVAL, "NULL buffer");
     if (!on16(m) || !on16(v) || !on16(scales) || !on16(m_out) || !on16(v_out))
         return afail(ZERO1_EALIGN, "buffers must be 16-byte aligned");
+    const uint64_t blocks = h->first.back(), n = blocks * kListBlock;
+    for (const Bytes out : {Bytes{m_out, 4 * n}, Bytes{v_out, 4 * n}})
+        if (!apart(out, {m, n}) || !apart(out, {v, n}) || !apart(out, {scales, n / 32}))
+            return afail(ZERO1_EINVAL, "m_out or v_out shares memory with the moments");
+    if (!apart({m_out, 4 * n}, {v_out, 4 * n})) return afail(ZERO1_EINVAL, "m_out and v_out share memory");
     AdamwDeviceGuard g(h->device);
-    const uint64_t blocks = h->first.back();
     const cudaError_t e = zero1::launch(zero1::zero1_adamw_moments_kernel, dim3((unsigned)((blocks + zero1::kWarps - 1) / zero1::kWarps)),
                                         zero1::kListThreads, 0, static_cast<cudaStream_t>(stream), h->d, blocks,
                                         static_cast<const uint8_t *>(m), static_cast<const uint8_t *>(v),

@@ -123,7 +123,10 @@ uint64_t partial_bytes(uint64_t tiles, uint32_t slices) { return slices > 1 ? ti
 uint64_t weight_tiles(const zero1_ffn_shape &s) { return 2 * tiles_of(s.width, s.hidden) + tiles_of(s.hidden, s.width); }
 
 // The forward pass of few rows has kernels of its own.
-bool thin_rows(const zero1_ffn_shape &s, bool backward) { return !backward && s.rows <= kFfnThinRows; }
+bool thin_rows(const zero1_ffn_shape &s, bool backward)
+{
+    return !backward && s.rows <= kFfnThinRows && s.hidden <= kFfnThinHidden;
+}
 
 uint64_t workspace_of(const zero1_ffn_shape &s, bool backward)
 {
@@ -320,12 +323,18 @@ void run(Call &c, FfnParams &p, F f)
     c.launched = true;
 }
 
-int check_workspace(const zero1_ffn_shape &s, bool backward, const void *workspace, uint64_t bytes)
+int check_workspace(const zero1_ffn_shape &s, bool backward, const void *workspace, uint64_t bytes, const Mat *m, int count)
 {
     const uint64_t need = workspace_of(s, backward);
     if (bytes < need) return ffail(ZERO1_EINVAL, "the workspace holds %llu bytes, the call needs %llu", (unsigned long long)bytes, (unsigned long long)need);
     if (need && !workspace) return ffail(ZERO1_EINVAL, "workspace is NULL");
     if (reinterpret_cast<uintptr_t>(workspace) % 256) return ffail(ZERO1_EALIGN, "the workspace is not 256-byte aligned");
+    const uintptr_t from = reinterpret_cast<uintptr_t>(workspace);
+    for (int i = 0; i < count; ++i) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(m[i].p);
+        if (need && m[i].p && at < from + need && from < at + 2 * m[i].extent())
+            return ffail(ZERO1_EINVAL, "%s lies in the workspace", m[i].name);
+    }
     return ZERO1_OK;
 }
 
@@ -364,7 +373,7 @@ int zero1_ffn_forward(const zero1_ffn_shape *shape, const void *x, const void *w
                          {gate, s.rows, s.hidden, s.ldh, "gate", true},
                          {up, s.rows, s.hidden, s.ldh, "up", true}};
     if (const int rc = check_mats(s, mats, 8)) return rc;
-    if (const int rc = check_workspace(s, false, workspace, workspace_bytes)) return rc;
+    if (const int rc = check_workspace(s, false, workspace, workspace_bytes, mats, 8)) return rc;
     Call c(s, workspace, errors, stream);
     if (c.rc) return c.rc;
 
@@ -461,7 +470,7 @@ int zero1_ffn_backward(const zero1_ffn_shape *shape, const void *dy, const void 
     if (!dy || !x || !w_gate || !w_up || !w_down || !gate || !up || !h) return ffail(ZERO1_EINVAL, "NULL pointer argument");
     if (reinterpret_cast<uintptr_t>(errors) % 4) return ffail(ZERO1_EALIGN, "errors is not 4-byte aligned");
     if (const int rc = check_mats(s, mats, 12)) return rc;
-    if (const int rc = check_workspace(s, true, workspace, workspace_bytes)) return rc;
+    if (const int rc = check_workspace(s, true, workspace, workspace_bytes, mats, 12)) return rc;
     Call c(s, workspace, errors, stream);
     if (c.rc) return c.rc;
 

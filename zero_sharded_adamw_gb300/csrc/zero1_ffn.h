@@ -74,8 +74,10 @@ inline FfnSlices ffn_slices(uint64_t tiles_a, uint64_t steps_a, uint64_t tiles_b
     return s;
 }
 
-// The forward pass of at most kFfnThinRows rows (zero1_ffn_thin.cu).
-constexpr uint64_t kFfnThinRows = 128;
+// The forward pass of at most kFfnThinRows rows (zero1_ffn_thin.cu; at 128
+// rows, 4096 x 11008, 69 us to the tiles' 79), unless a sum over the hidden
+// size has to be taken in slices (ffn_slices).
+constexpr uint64_t kFfnThinRows = 128, kFfnThinHidden = 65536;
 
 // Rows of x and of h that one box of the narrow operand holds.
 inline uint32_t ffn_thin_box(uint64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }

@@ -133,7 +133,9 @@ __global__ void __launch_bounds__(kThinThreads) zero1_ffn_thin_kernel(const __gr
     const uint32_t tmem = sh.tmem, col0 = blockIdx.x / ranks * 128;
     const uint32_t begin = (uint32_t)((uint64_t)p.steps * rank / ranks), end = (uint32_t)((uint64_t)p.steps * (rank + 1) / ranks);
 
-    if (threadIdx.x == 0 && !p.stall) {
+    if (threadIdx.x == 0 && p.stall) {
+        ptx::grid_dependency_wait();   // a launch does not end before the one it began beside
+    } else if (threadIdx.x == 0) {
         // ---- loads
         const auto wide = [&](uint32_t s, uint32_t stage) {
             ptx::mbar_arrive_expect_tx(&sh.full[stage], S::kStageBytes);

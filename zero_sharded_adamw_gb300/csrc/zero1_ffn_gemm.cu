@@ -26,15 +26,21 @@ namespace {
 
 constexpr uint32_t kBox = 8192;                     // 64 x 64 bf16
 constexpr uint32_t kStageBytes = 4 * kBox;          // one block's 128 rows of A and 128 of B
-constexpr int kStages = 5;
-constexpr int kEpilogueWarps = 16;
-constexpr int kGemmThreads = 64 + 32 * kEpilogueWarps;
 constexpr uint32_t kWarpTurn = 4096;                // 32 rows x 32 fp32 of an epilogue warp
-constexpr int kGemmSmem = kStages * kStageBytes + kEpilogueWarps * kWarpTurn + 1024;
-static_assert(kGemmSmem >= kAloneSmem, "two pairs could wait for each other's tensor memory");
+// Eight epilogue warps have registers for what is in flight (16,384 x 768 x
+// 2048: dh's product in 67 us, 76 with sixteen; 8,192 x 4096 x 11008 backward
+// 2.77 ms, 2.86).  Sixteen finish one tile sooner, where no pair has another
+// to go on with (2,000 x 256 x 688 backward in 37 us, 41 with eight).
+template <int WARPS>
+struct Gemm {
+    static constexpr int kThreads = 64 + 32 * WARPS;
+    static constexpr int kStages = WARPS == 16 ? 5 : 6;
+    static constexpr int kSmem = kStages * kStageBytes + WARPS * kWarpTurn + 1024;
+    static_assert(kSmem >= kAloneSmem, "two pairs could wait for each other's tensor memory");
+};
 
 struct GemmShared {
-    uint64_t full[kStages], empty[kStages];
+    uint64_t full[6], empty[6];
     uint64_t acc_full[2], acc_empty[2];
     uint64_t drain;
     uint32_t tmem;
@@ -227,12 +233,13 @@ __device__ __forceinline__ void write_narrow(uint16_t *base, const Patch &p, uin
 }
 
 // Per pair: one thread of each block loads operands (TMA), one thread of the
-// first issues the products, sixteen warps of each block take its 128 rows of a
+// first issues the products, eight or sixteen warps of each block take its 128 rows of a
 // finished tile out of one accumulator while the other fills.
-template <int MODE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
+template <int MODE, int WARPS>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Gemm<WARPS>::kThreads, 1)
     zero1_ffn_gemm_kernel(const __grid_constant__ FfnParams p)
 {
+    constexpr int kStages = Gemm<WARPS>::kStages;
     extern __shared__ unsigned char raw[];
     __shared__ GemmShared sh;
     const uint32_t ring = (tc::smem_u32(raw) + 1023u) & ~1023u;
@@ -243,7 +250,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) ptx::mbar_init(&sh.full[i], 1), ptx::mbar_init(&sh.empty[i], 1);
-        for (int i = 0; i < 2; ++i) ptx::mbar_init(&sh.acc_full[i], 1), ptx::mbar_init(&sh.acc_empty[i], 2 * kEpilogueWarps);
+        for (int i = 0; i < 2; ++i) ptx::mbar_init(&sh.acc_full[i], 1), ptx::mbar_init(&sh.acc_empty[i], 2 * WARPS);
         ptx::mbar_init(&sh.drain, 1);
         sh.abort = 0;
         sh.errors = 0;
@@ -328,10 +335,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
             }
         }
     } else if (warp >= 2) {
-        // ---- finished tiles: this block's 128 rows; each group of four warps a fourth of the columns
+        // ---- finished tiles: this block's 128 rows; each group of four warps its part of the columns
         const uint32_t group = (uint32_t)(warp - 2) >> 2, quarter = (uint32_t)warp & 3, lane = threadIdx.x & 31;
         const uint32_t mem = ring + kStages * kStageBytes + (uint32_t)(warp - 2) * kWarpTurn;
-        constexpr uint32_t kCols = (MODE == kFfnGated ? 128 : 256) / (kEpilogueWarps / 4);   // columns of a group
+        constexpr uint32_t kCols = (MODE == kFfnGated ? 128 : 256) / (WARPS / 4);   // columns of a group
         const uint32_t at = tmem + (quarter << 21) + group * kCols;
         uint32_t used = 0;
         uint4 in[2][MODE == kFfnSlope ? 4 : 1];   // slope: gate and up of the 32 columns to come
@@ -510,20 +517,27 @@ __global__ void __launch_bounds__(256) zero1_ffn_join_kernel(const __grid_consta
     }
 }
 
-template <int MODE>
-cudaError_t gemm(const FfnParams &p, int sms, cudaStream_t stream)
+template <int MODE, int WARPS>
+cudaError_t gemm_t(const FfnParams &p, uint32_t pairs, cudaStream_t stream)
 {
-    const auto kernel = zero1_ffn_gemm_kernel<MODE>;
-    cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), kGemmSmem);
+    using S = Gemm<WARPS>;
+    const auto kernel = zero1_ffn_gemm_kernel<MODE, WARPS>;
+    cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), S::kSmem);
     if (e != cudaSuccess) return e;
-    const uint32_t pairs = (uint32_t)sms / 2;
     const dim3 grid(2 * (p.items < pairs ? p.items : pairs));
     // after another kernel of the same call it may begin while that one ends
-    e = p.follows ? launch_early(kernel, grid, kGemmThreads, kGemmSmem, stream, p)
-                  : launch(kernel, grid, kGemmThreads, kGemmSmem, stream, p);
+    e = p.follows ? launch_early(kernel, grid, S::kThreads, S::kSmem, stream, p)
+                  : launch(kernel, grid, S::kThreads, S::kSmem, stream, p);
     if (e == cudaSuccess && p.joins)
         e = launch_early(zero1_ffn_join_kernel, dim3(p.joins * (kFfnTile / 8)), 256, 0, stream, p);
     return e;
+}
+
+template <int MODE>
+cudaError_t gemm(const FfnParams &p, int sms, cudaStream_t stream)
+{
+    const uint32_t pairs = (uint32_t)sms / 2;
+    return p.items <= pairs ? gemm_t<MODE, 16>(p, pairs, stream) : gemm_t<MODE, 8>(p, pairs, stream);
 }
 
 }  // namespace

@@ -12,6 +12,12 @@
 // until it needs h.  Of 16 rows and fewer, h goes on as two bf16 parts, high
 // and low, whose products are added: y then has no rounding of h in it.  (The
 // narrow operand is free: one more product of the same weights.)
+//
+// Measured at 4096 x 11008 (271 MB of weights): one row 45 us (6.0 TB/s), 8 rows
+// 47, 16 49, 32 57, 128 69 (the narrow operand is read again by every block);
+// at 8192 x 28672 one row 215 us (6.5 TB/s).  768 x 2048: 10 us, all latency.
+// Multiplying on the CUDA cores, weights from registers, took 69 us for one
+// row and 169 for eight.
 #include "zero1_ffn.h"
 #include "zero1_ffn_device.cuh"
 #include "zero1_internal.h"

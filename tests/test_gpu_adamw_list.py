@@ -384,6 +384,41 @@ def test_a_captured_step_replays_as_the_next_one():
         assert torch.equal(x, y)
 
 
+def test_places_past_32_bits():
+    """A tensor of 2^32 + 1,000 entries with 8-bit moments: the entries around
+    and past 2^32, whose random bits take the upper half of their place."""
+    n, hp = (1 << 32) + 1000, z.Hparams(max_norm=0.0)
+    entries = -(-n // 256) * 256
+    first = (1 << 32) - 512
+    grad = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    param = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    master = torch.zeros(entries, device="cuda")
+    m, v = (torch.zeros(entries, dtype=torch.uint8, device="cuda") for _ in range(2))
+    scales = torch.zeros(entries // 128, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    grad[first:] = torch.randn(n - first, generator=gen, device="cuda").bfloat16()
+    with z.AdamW([n], hp, z.AdamWOptions(state_bits=8, seed=5)) as opt:
+        opt.step([grad], [param], master, m, v, scales)
+        torch.cuda.synchronize()
+    tail = entries - first
+    g = torch.zeros(tail, device="cuda")
+    g[:n - first] = grad[first:].float()
+    zero = torch.zeros(tail, device="cuda")
+    w, wm, wv = ap.step(g, zero, zero, zero, hp, 1, torch.ones(tail, dtype=torch.bool, device="cuda"), None)
+    place = torch.arange(first, entries, device="cuda")
+    key = ap.mix(ap.mix(ap.mix(5) ^ 0) ^ 1)
+    high = ap.mix((key + 1) & 0xFFFFFFFF)
+    h = ap.mix((place & 0xFFFFFFFF) ^ torch.where(place >> 32 > 0, high, key))
+    km, sm = ap.encode(wm, ap.M_TOP, 3, h & 0xFFFF, False)
+    kr, sr = ap.encode(wv.sqrt(), ap.R_TOP, 4, h >> 16, True)
+    live = slice(0, n - first)
+    assert torch.equal(master[first:n], w[live]) and torch.equal(param[first:], w[live].bfloat16())
+    assert torch.equal(m[first:n].long(), torch.where(wm < 0, km + 128, km)[live])
+    assert torch.equal(v[first:n].long(), kr[live])
+    assert torch.equal(scales.view(-1, 2)[first // 256:], torch.stack([sm, sr], 1))
+    assert not bool(master[:1 << 20].any()) and not bool(m[1 << 31:(1 << 31) + (1 << 20)].any())
+
+
 def test_two_handles_on_two_streams():
     cases = [Case([70000, 33], bits=bits, seed=9) for bits in (8, 32)]
     twins = [Case([70000, 33], bits=bits, seed=9) for bits in (8, 32)]

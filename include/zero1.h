@@ -755,8 +755,8 @@ typedef struct zero1_ffn_shape {
 
 /* Host-only: the bytes of workspace a forward (backward = 0) or backward call
  * of this shape needs: copies of operands (see above), h in parts (forward, at
- * most 128 rows) or partial sums where few tiles share a long sum, and in the backward
- * pass dgate and dup.
+ * most 128 rows) or partial sums where few tiles share a long sum, and in the
+ * backward pass dgate and dup.
  * Errors: ZERO1_EINVAL. */
 int zero1_ffn_workspace(const zero1_ffn_shape *shape, int backward, uint64_t *bytes);
 
@@ -768,9 +768,9 @@ int zero1_ffn_workspace(const zero1_ffn_shape *shape, int backward, uint64_t *by
  *     be kept;
  *   errors: optional device word (NULL = none); bit 0 is set if a kernel
  *     wait gave up (1 s limit), in which case the outputs are not valid.
- * No output may share an entry with another buffer of the call, and none may lie
- * in the workspace.  rows = 0
- * does nothing.  Asynchronous on `stream`; allocates nothing; may be captured.
+ * No output may share an entry with another buffer of the call, and no buffer
+ * may lie in the workspace.  rows = 0 does nothing.  Asynchronous on `stream`;
+ * allocates nothing; may be captured.
  * Errors: ZERO1_EINVAL, ZERO1_EALIGN, ZERO1_ECUDA. */
 int zero1_ffn_forward(const zero1_ffn_shape *shape, const void *x, const void *w_gate, const void *w_up,
                       const void *w_down, void *gate, void *up, void *h, void *y, void *workspace,
@@ -813,8 +813,8 @@ int zero1_ffn_backward(const zero1_ffn_shape *shape, const void *dy, const void 
  * value is below 2^-100: it is held as zeros).  Codes are rounded up or down
  * at random with the exact value as their mean, by a hash of `seed`, the step
  * and the entry's place: the same inputs give the same bits.  A block with an
- * infinity or a NaN among its new moments has a NaN scale and stands for NaN;
- * other blocks are not touched by it (clipping, whose norm is then infinite
+ * infinity or a NaN among its new m (or v) has a NaN scale, and its m (or v)
+ * stand for NaN; other blocks are not touched by it (clipping, whose norm is then infinite
  * or NaN, turns the whole list NaN or holds it, as zero1_step does).
  *   state_bits: 8 or 32;
  *   param_dtype, grad_dtype: ZERO1_DTYPE_BF16 or ZERO1_DTYPE_F32;

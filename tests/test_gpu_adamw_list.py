@@ -456,6 +456,20 @@ def test_refusals():
                       (args(grad_ptrs=[c.grads[0].data_ptr() + 1, c.grads[1]]), "aligned")):
         with pytest.raises(z.Zero1Error, match=word):
             z.zero1_adamw_step(h, **bad)
+    # in any order of addresses, and gradients between parameters
+    pool = torch.zeros(4096, dtype=torch.bfloat16, device="cuda")
+    for p0, p1, g0, g1, fine in ((0, 512, 1024, 2048, True), (512, 0, 2048, 1024, True), (0, 1024, 512, 2048, True),
+                                 (1024, 2048, 0, 512, True), (0, 292, 1024, 2048, False), (292, 260, 1024, 2048, False),
+                                 (0, 512, 292, 2048, False), (0, 512, 2048, 544, False), (1000, 0, 700, 36, False)):
+        call = dict(param_ptrs=[pool[p0:p0 + 300], pool[p1:p1 + 40]], grad_ptrs=[pool[g0:g0 + 300], pool[g1:g1 + 40]])
+        if fine:
+            z.zero1_adamw_step(h, **args(**call))
+        else:
+            with pytest.raises(z.Zero1Error, match="shares memory"):
+                z.zero1_adamw_step(h, **args(**call))
+    c = Case([300, 40], bits=8)    # one that has not stepped
+    c.draw()
+    args = lambda **k: {**dict(grad_ptrs=c.grads, param_ptrs=c.params, master=c.master, m=c.m, v=c.v, scales=c.scales), **k}  # noqa: E731
     # a table of pointers is refused the same way
     with pytest.raises(z.Zero1Error, match="elements"):
         c.opt.step(z.PtrTable([c.grads[0][:299], c.grads[1]]), c.params, c.master, c.m, c.v, c.scales)

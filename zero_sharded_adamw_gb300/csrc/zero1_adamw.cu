@@ -932,7 +932,6 @@ struct zero1_adamw_ctx {
     void *block = nullptr;                    // one cudaMalloc: tables, status, partial sums
     uint64_t block_bytes = 0;
     zero1::ListTables d{};
-    std::vector<const void *> checked;        // the pointers last found not to overlap
 };
 
 namespace {
@@ -1125,15 +1124,24 @@ int create(const uint64_t *sizes, const uint8_t *decays, uint64_t count, const z
 }
 
 // No parameter tensor may share memory with another, or with a gradient: each
-// is written by blocks that run in any order.  Looked at again only when a
-// pointer has changed.
-int check_overlap(zero1_adamw_ctx *h, const void *const *grads, void *const *params)
+// is written by blocks that run in any order.
+int check_overlap(const zero1_adamw_ctx *h, const void *const *grads, void *const *params)
 {
     const size_t count = h->sizes.size();
-    if (h->checked.size() == 2 * count && std::equal(params, params + count, h->checked.begin()) &&
-        std::equal(grads, grads + count, h->checked.begin() + count))
-        return ZERO1_OK;
-    h->checked.clear();
+    const uint64_t pb = bytes_of(h->opt.param_dtype), gb = bytes_of(h->opt.grad_dtype);
+    // parameters in the order of their addresses, gradients all before or all after them: nothing to sort
+    uintptr_t p_end = 0, p_begin = UINTPTR_MAX, g_begin = UINTPTR_MAX, g_end = 0;
+    bool ordered = true;
+    for (size_t i = 0; i < count; ++i) {
+        if (h->sizes[i] == 0) continue;
+        const uintptr_t p = reinterpret_cast<uintptr_t>(params[i]), g = reinterpret_cast<uintptr_t>(grads[i]);
+        ordered = ordered && p >= p_end;
+        p_begin = std::min(p_begin, p);
+        p_end = std::max<uintptr_t>(p_end, p + h->sizes[i] * pb);
+        g_begin = std::min(g_begin, g);
+        g_end = std::max<uintptr_t>(g_end, g + h->sizes[i] * gb);
+    }
+    if (ordered && (g_end <= p_begin || p_end <= g_begin)) return ZERO1_OK;
     struct Range {
         uintptr_t from, to;
         bool param;
@@ -1144,8 +1152,8 @@ int check_overlap(zero1_adamw_ctx *h, const void *const *grads, void *const *par
     for (size_t i = 0; i < count; ++i) {
         if (h->sizes[i] == 0) continue;
         const uintptr_t p = reinterpret_cast<uintptr_t>(params[i]), g = reinterpret_cast<uintptr_t>(grads[i]);
-        r.push_back({p, p + h->sizes[i] * bytes_of(h->opt.param_dtype), true, i});
-        r.push_back({g, g + h->sizes[i] * bytes_of(h->opt.grad_dtype), false, i});
+        r.push_back({p, p + h->sizes[i] * pb, true, i});
+        r.push_back({g, g + h->sizes[i] * gb, false, i});
     }
     std::sort(r.begin(), r.end(), [](const Range &a, const Range &b) { return a.from < b.from; });
     // the furthest end so far, of parameters and of anything
@@ -1157,8 +1165,6 @@ int check_overlap(zero1_adamw_ctx *h, const void *const *grads, void *const *par
         if (k == 0 || r[k].to > r[any].to) any = k;
         if (r[k].param && (param == SIZE_MAX || r[k].to > r[param].to)) param = k;
     }
-    h->checked.assign(params, params + count);
-    h->checked.insert(h->checked.end(), grads, grads + count);
     return ZERO1_OK;
 }
 

@@ -26,7 +26,7 @@ HEADERS = [os.path.join(CSRC, "zero1_internal.h"), os.path.join(CSRC, "zero1_ptx
            os.path.join(CSRC, "zero1_muon.h"), os.path.join(CSRC, "zero1_muon_tiles.h"),
            os.path.join(CSRC, "zero1_muon_device.cuh"), os.path.join(CSRC, "zero1_tc.cuh"),
            os.path.join(CSRC, "zero1_launch.h"), os.path.join(CSRC, "zero1_ffn.h"),
-           os.path.join(CSRC, "zero1_ffn_device.cuh"),
+           os.path.join(CSRC, "zero1_ffn_device.cuh"), os.path.join(CSRC, "zero1_adamw_plan.h"),
            os.path.join(INCLUDE, "zero1.h")]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")

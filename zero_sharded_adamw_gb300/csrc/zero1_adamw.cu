@@ -49,6 +49,7 @@
 #include <vector>
 
 #include "zero1.h"
+#include "zero1_adamw_plan.h"
 #include "zero1_internal.h"
 #include "zero1_launch.h"
 #include "zero1_ptx.cuh"
@@ -56,12 +57,8 @@
 namespace zero1 {
 namespace {
 
-constexpr uint32_t kListBlock = 256;      // entries of one block: 8 a lane of one warp
-constexpr int kListThreads = 256;
-constexpr uint32_t kWarps = kListThreads / 32;
 constexpr uint32_t kUpdateBlocks = 4;     // blocks of a warp of the update, fp32 moments (they are unrolled)
 constexpr uint32_t kStagedBlocks = 8;     // ... with 8 bits (16: 374 us in place of 366, 32: 392, all at once: 417)
-constexpr uint32_t kNormBlocks = 8;       // ... of the norm, at a time (4: 68 us in place of 63, 2: 68 to 80)
 constexpr float kMTop = 61439.f, kRTop = 63487.f;       // f(127, 3) - 1, f(255, 4) - 1
 constexpr uint32_t kHeldLow = 27u << 23;                // 2^-100: a block whose largest value is smaller is all zeros
 constexpr uint32_t kInf = 0x7F800000u;
@@ -931,11 +928,13 @@ struct zero1_adamw_ctx {
     int device = 0, num_sms = 0;
     void *block = nullptr;                    // one cudaMalloc: tables, status, partial sums
     uint64_t block_bytes = 0;
+    uint64_t partials = 0;                    // partial sums of the norm that the tables have room for
     zero1::ListTables d{};
 };
 
 namespace {
 
+using zero1::kCaps;
 using zero1::kListBlock;
 
 std::mutex g_adamw_mu;
@@ -988,17 +987,6 @@ struct FreeAdamw {
         delete h;
     }
 };
-
-// Blocks of a norm launch: the four an SM that run at once, or one for each 64 blocks of the list.
-uint32_t norm_grid(uint64_t nblocks, int sms)
-{
-    const uint64_t need = (nblocks + zero1::kWarps * zero1::kNormBlocks - 1) / (zero1::kWarps * zero1::kNormBlocks);
-    return (uint32_t)std::min<uint64_t>(need, 4ull * (uint64_t)sms);
-}
-
-// Tensors whose pointers one launch holds: kernel arguments are 32,764 bytes
-// at most, and longer ones take longer to launch.
-constexpr int kCaps[3] = {32, 256, 1600};
 
 int create(const uint64_t *sizes, const uint8_t *decays, uint64_t count, const zero1_hparams *hp,
            const zero1_adamw_options *opts, zero1_adamw_handle *out)
@@ -1073,10 +1061,8 @@ int create(const uint64_t *sizes, const uint8_t *decays, uint64_t count, const z
     if (major != 10 || minor != 3)
         return afail(ZERO1_ENODEV, "device %d is sm_%d%d; this library is built for sm_103a", dev, major, minor);
 
-    // partial sums of the norm, over the launches a step takes
-    uint64_t partials = 0;
-    for (uint64_t i = 0; i < count; i += kCaps[2])
-        partials += norm_grid(first[std::min<uint64_t>(i + kCaps[2], count)] - first[i], sms);
+    // of the norm, over the launches a step takes (a list that takes launches of fewer tensors takes one)
+    const uint64_t partials = zero1::norm_partials(first.data(), count, kCaps[2], sms);
     uint64_t at = 0;
     const auto take = [&](uint64_t bytes) {
         const uint64_t here = at;
@@ -1092,6 +1078,7 @@ int create(const uint64_t *sizes, const uint8_t *decays, uint64_t count, const z
     h->first = first;
     h->device = dev;
     h->num_sms = sms;
+    h->partials = partials;
     h->block_bytes = at;
     if ((e = cudaMalloc(&h->block, at)) != cudaSuccess) {
         h->block = nullptr;
@@ -1189,12 +1176,10 @@ cudaError_t norm_t(const zero1_adamw_ctx *h, const StepCall &c, uint64_t i0, uin
     p.before = before;
     p.one = 1.f;
     p.last = i1 == h->sizes.size();
-    uint32_t grid = norm_grid(p.nblocks, h->num_sms);
-    if (grid == 0) {
-        if (!p.last) return cudaSuccess;
-        grid = 1;   // the last tensors are empty: only the sum is formed
-    }
+    const uint32_t grid = zero1::norm_grid(p.nblocks, p.last, h->num_sms);
+    if (grid == 0) return cudaSuccess;
     before += grid;
+    if (before > h->partials) return cudaErrorInvalidConfiguration;
     return zero1::launch(zero1::zero1_adamw_norm_kernel<G, CAP>, dim3(grid), zero1::kListThreads, 0, c.stream, p);
 }
 

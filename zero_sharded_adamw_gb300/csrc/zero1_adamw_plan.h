@@ -1,0 +1,43 @@
+// zero1_adamw_plan.h -- host-only rules of AdamW over a list of tensors
+// (zero1_adamw.cu): the norm's launches and the partial sums they write.
+// Plain C++, so that the rules are tested without a GPU.
+#pragma once
+
+#include <algorithm>
+#include <cstdint>
+
+namespace zero1 {
+
+constexpr uint32_t kListBlock = 256;      // entries of one block: 8 a lane of one warp
+constexpr int kListThreads = 256;
+constexpr uint32_t kWarps = kListThreads / 32;
+constexpr uint32_t kNormBlocks = 8;       // blocks of a warp of the norm, at a time (4: 68 us in place of 63, 2: 68 to 80)
+
+// Tensors whose pointers one launch holds: kernel arguments are 32,764 bytes
+// at most, and longer ones take longer to launch.
+constexpr int kCaps[3] = {32, 256, 1600};
+
+// Thread blocks of the norm's launch over `nblocks` blocks of the list, each
+// of which writes one partial sum: the four an SM that run at once, or one for
+// each 64 blocks.  The step's last launch forms the norm, and so has one even
+// where its tensors are all empty; another launch without blocks is left out (0).
+inline uint32_t norm_grid(uint64_t nblocks, bool last, int sms)
+{
+    const uint64_t need = (nblocks + kWarps * kNormBlocks - 1) / (kWarps * kNormBlocks);
+    const uint32_t grid = (uint32_t)std::min<uint64_t>(need, 4ull * (uint64_t)sms);
+    return grid == 0 && last ? 1 : grid;
+}
+
+// Partial sums of a step whose launches take `cap` tensors each; tensor i has
+// the blocks first[i] to first[i + 1].
+inline uint64_t norm_partials(const uint64_t *first, uint64_t count, uint64_t cap, int sms)
+{
+    uint64_t n = 0;
+    for (uint64_t i = 0; i < count; i += cap) {
+        const uint64_t end = std::min(i + cap, count);
+        n += norm_grid(first[end] - first[i], end == count, sms);
+    }
+    return n;
+}
+
+}  // namespace zero1

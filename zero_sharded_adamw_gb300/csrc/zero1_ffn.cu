@@ -74,8 +74,9 @@ int check_shape(const zero1_ffn_shape *in, zero1_ffn_shape &s)
     return ZERO1_OK;
 }
 
-// Whether two matrices share an entry.  With rows equally far apart it is
-// exact (column slices of one matrix share none); else their extents decide.
+// Whether two matrices share an entry.  With rows equally far apart, or a
+// single row in one of them, it is exact (column slices of one matrix share
+// none); else their extents decide.
 bool share(Mat a, Mat b)
 {
     if (reinterpret_cast<uintptr_t>(a.p) > reinterpret_cast<uintptr_t>(b.p)) {
@@ -85,8 +86,8 @@ bool share(Mat a, Mat b)
     }
     const uint64_t bytes = reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p);
     if (bytes >= 2 * a.extent()) return false;
-    if (a.rows == 1) a.ld = b.ld;
-    if (b.rows == 1) b.ld = a.ld;
+    if (a.rows == 1) return true;    // no gaps: b's first entry is one of a's, over however many of b's rows a goes on
+    if (b.rows == 1) b.ld = a.ld;    // as long as it may be: what counts is where it begins in a's rows
     if (a.ld != b.ld || bytes % 2) return true;
     const uint64_t d = bytes / 2, q = d / a.ld, c = d % a.ld;
     return (q < a.rows && c < a.cols) || (q + 1 < a.rows && c + b.cols > a.ld);

@@ -15,7 +15,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
-from dataclasses import dataclass
+from dataclasses import dataclass, replace
 
 __all__ = [
     "Zero1Error", "Zero1ArgumentError", "Hparams", "Options", "Zero1", "PtrTable",
@@ -895,14 +895,15 @@ class AdamWOptions:
                               int(self.decay_before_update), 0, self.seed)
 
 
-# (sizes, options, entries of the state) of every list handle this binding created.
+# (sizes, a copy of the options, entries of the state) of every list handle this binding created.
 _ADAMW_HANDLES: dict[int, tuple[tuple[int, ...], AdamWOptions, int]] = {}
 
 
 def zero1_adamw_create(sizes, hp: Hparams | None = None, opts: AdamWOptions | None = None, decays=None) -> int:
     """Create a handle for tensors of these many entries; `decays` holds a
     truth value a tensor (None: all decay)."""
-    sizes, opts = tuple(int(n) for n in sizes), opts or AdamWOptions()
+    # a copy: what the handle was created with, whatever becomes of the caller's object
+    sizes, opts = tuple(int(n) for n in sizes), replace(opts or AdamWOptions())
     if any(not 0 <= n < 1 << 63 for n in sizes):
         raise Zero1ArgumentError("sizes: a size is out of range")
     if decays is not None:
@@ -1004,7 +1005,7 @@ class AdamW:
 
     def __init__(self, sizes, hp: Hparams | None = None, opts: AdamWOptions | None = None, decays=None):
         self.handle = None
-        self.hp, self.opts = hp or Hparams(), opts or AdamWOptions()
+        self.hp, self.opts = replace(hp or Hparams()), replace(opts or AdamWOptions())
         self.handle = zero1_adamw_create(sizes, self.hp, self.opts, decays)
         self.entries, self.starts, _ = zero1_adamw_layout(self.handle)
         self.scale_entries = self.entries // 128 if self.opts.state_bits == 8 else 0

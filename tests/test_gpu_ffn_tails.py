@@ -62,3 +62,12 @@ def test_tails_keep_their_relative_accuracy(rows, name):
     less than 0.27 of their sum of magnitudes (SiLU at -2): 2.5e-5 / 0.27 = 9.3e-5, and products: 1e-4."""
     gates = torch.arange(0x4000, 0x4101, dtype=torch.int32, device="cuda").to(torch.int16).view(BF)
     check(rows, torch.cat([gates, -gates])[:512], name, 1e-4)
+
+
+@pytest.mark.parametrize("rows", [1, 40, 200])
+@pytest.mark.parametrize("name", fp.ACTS)
+def test_gates_up_to_the_largest(rows, name):
+    """Where g^2 and g^3 leave fp32's range the activation is g or 0 and its slope 1 or 0."""
+    big = [1e2, 1e5, 1e10, 1e13, 1e15, 1e18, 2e19, 1e20, 1e30, 3e38]
+    gates = torch.tensor([s * v for v in big for s in (1, -1)], device="cuda").to(BF)
+    check(rows, torch.cat([gates, gates.new_ones(4)]), name, 1e-4)

@@ -48,7 +48,8 @@ __device__ __forceinline__ void activate(float g, float &a, float &slope)
     } else if (ACT == 2) {       // (1 + tanh(z)) / 2 = sigmoid(2 z)
         const float s = sigmoid(2.f * kRoot2Pi * (g + kCube * g * g * g));
         a = g * s;
-        if (SLOPE) slope = s + 2.f * a * (1.f - s) * kRoot2Pi * (1.f + 3.f * kCube * g * g);
+        // past |g| = 1e15 1 - s or a is 0, and no factor beside it may leave fp32's range
+        if (SLOPE) slope = s + a * (1.f - s) * (2.f * kRoot2Pi * (1.f + 3.f * kCube * fminf(g * g, 1e30f)));
     } else {                     // NaN stays NaN
         a = g <= 0.f ? 0.f : g;
         if (SLOPE) slope = g <= 0.f ? 0.f : 1.f;

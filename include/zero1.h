@@ -861,7 +861,8 @@ int zero1_adamw_destroy(zero1_adamw_handle h);
  *   grad_ptrs, param_ptrs: host arrays of one device pointer a tensor (NULL
  *     for empty ones), aligned to their elements (16-byte aligned tensors
  *     are faster); the pointers are copied into the launches.  No parameter
- *     tensor may overlap another or a gradient (ZERO1_EINVAL).
+ *     tensor may overlap another or a gradient, and no tensor the state
+ *     (ZERO1_EINVAL).
  *   master, m, v, scales: the state, 16-byte aligned; m and v fp32 or bytes;
  *     master NULL with fp32 parameters, scales NULL with fp32 moments.
  * Errors: ZERO1_EINVAL, ZERO1_EALIGN, ZERO1_ENOMEM, ZERO1_ECUDA. */

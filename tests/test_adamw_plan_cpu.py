@@ -74,3 +74,61 @@ def test_every_partial_sum_of_the_norm_has_its_place(partials, sizes, launches, 
     held, written, n = partials(sizes, sms)
     assert written <= held and n == launches
     assert held == written    # and none is waste
+
+
+STATE = r"""
+#include <cstdio>
+#include <vector>
+#include "zero1_adamw_plan.h"
+int main() {
+    unsigned long long count, pb, gb, buffers, a, b, c;
+    while (std::scanf("%llu %llu %llu %llu", &count, &pb, &gb, &buffers) == 4) {
+        std::vector<uint64_t> sizes;
+        std::vector<const void *> grads;
+        std::vector<void *> params;
+        std::vector<zero1::StateBuffer> state;
+        for (unsigned long long i = 0; i < count; ++i) {
+            if (std::scanf("%llu %llu %llu", &a, &b, &c) != 3) return 1;
+            sizes.push_back(a), params.push_back((void *)b), grads.push_back((const void *)c);
+        }
+        for (unsigned long long i = 0; i < buffers; ++i) {
+            if (std::scanf("%llu %llu", &a, &b) != 2) return 1;
+            state.push_back({(const void *)a, b});
+        }
+        int which = -1;
+        bool param = false;
+        const size_t i = zero1::tensor_in_state({sizes.data(), sizes.size(), grads.data(), params.data(), gb, pb}, state.data(),
+                                                (int)buffers, &which, &param);
+        if (i == count) std::printf("none\n");
+        else std::printf("%zu %d %d\n", i, which, (int)param);
+    }
+    return 0;
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def state(tmp_path_factory):
+    exe = compiled(tmp_path_factory, "state", STATE)
+
+    def run(tensors, buffers, pb=2, gb=2):
+        words = [len(tensors), pb, gb, len(buffers)] + [v for t in tensors for v in t] + [v for b in buffers for v in b]
+        r = subprocess.run([exe], input=" ".join(map(str, words)), capture_output=True, text=True, check=True)
+        return r.stdout.strip()
+    return run
+
+
+@pytest.mark.parametrize("tensors,buffers,answer", [
+    # (entries, parameter, gradient); (address, bytes): master, m, v, scales
+    ([(100, 4096, 8192)], [(16384, 1024), (32768, 1024)], "none"),
+    ([(100, 4096, 8192)], [(4296, 1024), (8192 - 1024, 1024)], "none"),        # ends where the other begins
+    ([(100, 4096, 8192)], [(4295, 1024), (32768, 1024)], "0 0 1"),
+    ([(100, 4096, 8192)], [(16384, 1024), (4096 - 1023, 1024)], "0 1 1"),
+    ([(100, 4096, 8192)], [(16384, 1024), (8391, 1)], "0 1 0"),
+    ([(100, 4096, 8192)], [(0, 1 << 40), (8000, 4096)], "0 1 0"),              # a buffer that is not there
+    ([(0, 0, 0), (0, 16384, 16384), (7, 4096, 16390)], [(16384, 1024)], "2 0 0"),
+    ([(0, 16384, 16384)], [(16384, 1024)], "none"),                            # empty tensors share nothing
+    ([(1 << 33, 1 << 40, 1 << 45)], [((1 << 40) + (1 << 34) - 1, 16)], "0 0 1"),
+])
+def test_tensors_that_share_memory_with_the_state(state, tensors, buffers, answer):
+    assert state(tensors, buffers) == answer

@@ -1298,6 +1298,21 @@ int check_state(const zero1_adamw_ctx *h, const void *master, const void *m, con
     return afail(ZERO1_EINVAL, "two of master, m, v and scales share memory");
 }
 
+// No tensor may share memory with the state, which other blocks write.
+int check_tensors_and_state(const zero1_adamw_ctx *h, const void *const *grads, void *const *params, const void *master,
+                            const void *m, const void *v, const void *scales)
+{
+    const uint64_t n = h->first.back() * kListBlock, each = h->opt.state_bits == 8 ? n : 4 * n;
+    const zero1::StateBuffer state[4] = {{master, 4 * n}, {m, each}, {v, each}, {scales, n / 32}};
+    const zero1::ListTensors t{h->sizes.data(), h->sizes.size(), grads, params, bytes_of(h->opt.grad_dtype), bytes_of(h->opt.param_dtype)};
+    int which = 0;
+    bool param = false;
+    const size_t i = zero1::tensor_in_state(t, state, 4, &which, &param);
+    if (i == t.count) return ZERO1_OK;
+    const char *const names[4] = {"master", "m", "v", "scales"};
+    return afail(ZERO1_EINVAL, "the %s of tensor %zu shares memory with %s", param ? "parameter" : "gradient", i, names[which]);
+}
+
 }  // namespace
 
 extern "C" {
@@ -1342,6 +1357,7 @@ int zero1_adamw_step(zero1_adamw_handle h, const void *const *grad_ptrs, void *c
         if (reinterpret_cast<uintptr_t>(grad_ptrs[i]) % gb || reinterpret_cast<uintptr_t>(param_ptrs[i]) % pb)
             return afail(ZERO1_EALIGN, "tensor %zu is not aligned to its elements", i);
     }
+    if (const int rc = check_tensors_and_state(h, grad_ptrs, param_ptrs, master, m, v, scales)) return rc;
     cudaError_t e;
     try {
         if (const int rc = check_overlap(h, grad_ptrs, param_ptrs)) return rc;

@@ -1,9 +1,11 @@
 // zero1_adamw_plan.h -- host-only rules of AdamW over a list of tensors
-// (zero1_adamw.cu): the norm's launches and the partial sums they write.
+// (zero1_adamw.cu): the norm's launches and the partial sums they write, and
+// which buffers of a step share memory.
 // Plain C++, so that the rules are tested without a GPU.
 #pragma once
 
 #include <algorithm>
+#include <cstddef>
 #include <cstdint>
 
 namespace zero1 {
@@ -38,6 +40,41 @@ inline uint64_t norm_partials(const uint64_t *first, uint64_t count, uint64_t ca
         n += norm_grid(first[end] - first[i], end == count, sms);
     }
     return n;
+}
+
+// A buffer of the state: where it begins, its bytes.
+struct StateBuffer {
+    const void *p;
+    uint64_t bytes;
+};
+
+// A step's tensors (sizes[i] entries each) and the bytes of an entry.
+struct ListTensors {
+    const uint64_t *sizes;
+    size_t count;
+    const void *const *grads;
+    void *const *params;
+    uint64_t grad_bytes, param_bytes;
+};
+
+// The first tensor of which the parameter or the gradient shares memory with
+// a buffer of the state (count: none does), and that buffer's number.
+inline size_t tensor_in_state(const ListTensors &t, const StateBuffer *state, int buffers, int *which, bool *param)
+{
+    for (size_t i = 0; i < t.count; ++i) {
+        if (t.sizes[i] == 0) continue;
+        const uintptr_t p = reinterpret_cast<uintptr_t>(t.params[i]), p_end = p + t.sizes[i] * t.param_bytes;
+        const uintptr_t g = reinterpret_cast<uintptr_t>(t.grads[i]), g_end = g + t.sizes[i] * t.grad_bytes;
+        for (int k = 0; k < buffers; ++k) {
+            if (!state[k].p) continue;
+            const uintptr_t from = reinterpret_cast<uintptr_t>(state[k].p), to = from + state[k].bytes;
+            *param = p < to && from < p_end;
+            if (!*param && !(g < to && from < g_end)) continue;
+            *which = k;
+            return i;
+        }
+    }
+    return t.count;
 }
 
 }  // namespace zero1

@@ -865,7 +865,7 @@ int zero1_adamw_destroy(zero1_adamw_handle h);
  *     (ZERO1_EINVAL).
  *   master, m, v, scales: the state, 16-byte aligned; m and v fp32 or bytes;
  *     master NULL with fp32 parameters, scales NULL with fp32 moments.
- * Errors: ZERO1_EINVAL, ZERO1_EALIGN, ZERO1_ENOMEM, ZERO1_ECUDA. */
+ * Errors: ZERO1_EINVAL, ZERO1_EALIGN, ZERO1_ECUDA. */
 int zero1_adamw_step(zero1_adamw_handle h, const void *const *grad_ptrs, void *const *param_ptrs, float *master, void *m,
                      void *v, float *scales, void *stream);
 

@@ -2,6 +2,7 @@
 from __future__ import annotations
 
 import os
+import random
 import shutil
 import subprocess
 
@@ -132,3 +133,72 @@ def state(tmp_path_factory):
 ])
 def test_tensors_that_share_memory_with_the_state(state, tensors, buffers, answer):
     assert state(tensors, buffers) == answer
+
+
+SHARED = r"""
+#include <cstdio>
+#include <cstdlib>
+#include <new>
+#include <vector>
+#include "zero1_adamw_plan.h"
+static unsigned long long allocations = 0;
+void *operator new(std::size_t n) { ++allocations; if (void *p = std::malloc(n)) return p; throw std::bad_alloc(); }
+void operator delete(void *p) noexcept { std::free(p); }
+void operator delete(void *p, std::size_t) noexcept { std::free(p); }
+int main() {
+    unsigned long long count, pb, gb, a, b, c;
+    while (std::scanf("%llu %llu %llu", &count, &pb, &gb) == 3) {
+        std::vector<uint64_t> sizes;
+        std::vector<const void *> grads;
+        std::vector<void *> params;
+        for (unsigned long long i = 0; i < count; ++i) {
+            if (std::scanf("%llu %llu %llu", &a, &b, &c) != 3) return 1;
+            sizes.push_back(a), params.push_back((void *)b), grads.push_back((const void *)c);
+        }
+        std::vector<zero1::TensorRange> ranges(2 * count);
+        const unsigned long long before = allocations;
+        const size_t i = zero1::shared_param({sizes.data(), sizes.size(), grads.data(), params.data(), gb, pb}, ranges.data());
+        std::printf("%zu %llu\n", i, allocations - before);
+    }
+    return 0;
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def shared(tmp_path_factory):
+    exe = compiled(tmp_path_factory, "shared", SHARED)
+
+    def run(lists, pb, gb):
+        words = [v for tensors in lists for v in [len(tensors), pb, gb] + [w for t in tensors for w in t]]
+        r = subprocess.run([exe], input=" ".join(map(str, words)), capture_output=True, text=True, check=True)
+        return [tuple(int(v) for v in line.split()) for line in r.stdout.splitlines()]
+    return run
+
+
+@pytest.mark.parametrize("pb,gb", [(2, 2), (4, 2), (2, 4)])
+def test_parameters_that_share_memory_are_found_without_allocating(shared, pb, gb):
+    """3,000 lists of up to 40 tensors in any order of addresses, empty ones among them, against every pair."""
+    rng = random.Random(pb * 10 + gb)
+    lists, expected = [], []
+    for _ in range(3000):
+        count = rng.choice((1, 2, 3, 8, 40))
+        room = rng.choice((60, 600, 6000)) * count
+        tensors = [(rng.choice((0, 1, 5, 30)), 4 * rng.randrange(room // 4), 4 * rng.randrange(room // 4)) for _ in range(count)]
+        if rng.random() < 0.3:    # each in a place of its own, in a random order
+            places = rng.sample(range(2 * count), 2 * count)
+            tensors = [(n, 128 * places[2 * i], 128 * places[2 * i + 1]) for i, (n, _, _) in enumerate(tensors)]
+        every = [(p, p + n * pb, i, True) for i, (n, p, _) in enumerate(tensors) if n]
+        every += [(g, g + n * gb, i, False) for i, (n, _, g) in enumerate(tensors) if n]
+        guilty = set()
+        for x, a in enumerate(every):
+            for b in every[x + 1:]:
+                if (a[3] or b[3]) and a[0] < b[1] and b[0] < a[1]:
+                    guilty |= {r[2] for r in (a, b) if r[3]}
+        lists.append(tensors)
+        expected.append((count, guilty))
+    answers = shared(lists, pb, gb)
+    assert len(answers) == len(lists) and {bool(g) for _, g in expected} == {True, False}
+    for (i, allocated), (count, guilty) in zip(answers, expected):
+        assert allocated == 0
+        assert i in guilty if guilty else i == count

@@ -925,6 +925,7 @@ struct zero1_adamw_ctx {
     zero1_adamw_options opt{};
     std::vector<uint64_t> sizes;
     std::vector<uint64_t> first;              // block each tensor starts at; one more at the end
+    std::vector<zero1::TensorRange> ranges;   // of a step's tensors, filled anew in every step
     int device = 0, num_sms = 0;
     void *block = nullptr;                    // one cudaMalloc: tables, status, partial sums
     uint64_t block_bytes = 0;
@@ -1076,6 +1077,7 @@ int create(const uint64_t *sizes, const uint8_t *decays, uint64_t count, const z
     h->opt = o;
     h->sizes.assign(sizes, sizes + count);
     h->first = first;
+    h->ranges.resize(2 * count);
     h->device = dev;
     h->num_sms = sms;
     h->partials = partials;
@@ -1107,51 +1109,6 @@ int create(const uint64_t *sizes, const uint8_t *decays, uint64_t count, const z
         g_adamw_live.insert(h.get());
     }
     *out = h.release();
-    return ZERO1_OK;
-}
-
-// No parameter tensor may share memory with another, or with a gradient: each
-// is written by blocks that run in any order.
-int check_overlap(const zero1_adamw_ctx *h, const void *const *grads, void *const *params)
-{
-    const size_t count = h->sizes.size();
-    const uint64_t pb = bytes_of(h->opt.param_dtype), gb = bytes_of(h->opt.grad_dtype);
-    // parameters in the order of their addresses, gradients all before or all after them: nothing to sort
-    uintptr_t p_end = 0, p_begin = UINTPTR_MAX, g_begin = UINTPTR_MAX, g_end = 0;
-    bool ordered = true;
-    for (size_t i = 0; i < count; ++i) {
-        if (h->sizes[i] == 0) continue;
-        const uintptr_t p = reinterpret_cast<uintptr_t>(params[i]), g = reinterpret_cast<uintptr_t>(grads[i]);
-        ordered = ordered && p >= p_end;
-        p_begin = std::min(p_begin, p);
-        p_end = std::max<uintptr_t>(p_end, p + h->sizes[i] * pb);
-        g_begin = std::min(g_begin, g);
-        g_end = std::max<uintptr_t>(g_end, g + h->sizes[i] * gb);
-    }
-    if (ordered && (g_end <= p_begin || p_end <= g_begin)) return ZERO1_OK;
-    struct Range {
-        uintptr_t from, to;
-        bool param;
-        size_t i;
-    };
-    std::vector<Range> r;
-    r.reserve(2 * count);
-    for (size_t i = 0; i < count; ++i) {
-        if (h->sizes[i] == 0) continue;
-        const uintptr_t p = reinterpret_cast<uintptr_t>(params[i]), g = reinterpret_cast<uintptr_t>(grads[i]);
-        r.push_back({p, p + h->sizes[i] * pb, true, i});
-        r.push_back({g, g + h->sizes[i] * gb, false, i});
-    }
-    std::sort(r.begin(), r.end(), [](const Range &a, const Range &b) { return a.from < b.from; });
-    // the furthest end so far, of parameters and of anything
-    size_t any = 0, param = SIZE_MAX;
-    for (size_t k = 0; k < r.size(); ++k) {
-        if (k > 0 && ((r[k].param && r[any].to > r[k].from) || (param != SIZE_MAX && r[param].to > r[k].from)))
-            return afail(ZERO1_EINVAL, "parameter tensor %zu shares memory with another tensor of the call",
-                         r[k].param ? r[k].i : r[param].i);
-        if (k == 0 || r[k].to > r[any].to) any = k;
-        if (r[k].param && (param == SIZE_MAX || r[k].to > r[param].to)) param = k;
-    }
     return ZERO1_OK;
 }
 
@@ -1298,19 +1255,23 @@ int check_state(const zero1_adamw_ctx *h, const void *master, const void *m, con
     return afail(ZERO1_EINVAL, "two of master, m, v and scales share memory");
 }
 
-// No tensor may share memory with the state, which other blocks write.
-int check_tensors_and_state(const zero1_adamw_ctx *h, const void *const *grads, void *const *params, const void *master,
-                            const void *m, const void *v, const void *scales)
+// No tensor may share memory with the state, and no parameter with another
+// tensor: other blocks write them.
+int check_tensors(zero1_adamw_ctx *h, const void *const *grads, void *const *params, const void *master, const void *m,
+                  const void *v, const void *scales)
 {
     const uint64_t n = h->first.back() * kListBlock, each = h->opt.state_bits == 8 ? n : 4 * n;
     const zero1::StateBuffer state[4] = {{master, 4 * n}, {m, each}, {v, each}, {scales, n / 32}};
     const zero1::ListTensors t{h->sizes.data(), h->sizes.size(), grads, params, bytes_of(h->opt.grad_dtype), bytes_of(h->opt.param_dtype)};
     int which = 0;
     bool param = false;
-    const size_t i = zero1::tensor_in_state(t, state, 4, &which, &param);
-    if (i == t.count) return ZERO1_OK;
+    size_t i = zero1::tensor_in_state(t, state, 4, &which, &param);
     const char *const names[4] = {"master", "m", "v", "scales"};
-    return afail(ZERO1_EINVAL, "the %s of tensor %zu shares memory with %s", param ? "parameter" : "gradient", i, names[which]);
+    if (i < t.count)
+        return afail(ZERO1_EINVAL, "the %s of tensor %zu shares memory with %s", param ? "parameter" : "gradient", i, names[which]);
+    i = zero1::shared_param(t, h->ranges.data());
+    if (i < t.count) return afail(ZERO1_EINVAL, "parameter tensor %zu shares memory with another tensor of the call", i);
+    return ZERO1_OK;
 }
 
 }  // namespace
@@ -1357,13 +1318,8 @@ int zero1_adamw_step(zero1_adamw_handle h, const void *const *grad_ptrs, void *c
         if (reinterpret_cast<uintptr_t>(grad_ptrs[i]) % gb || reinterpret_cast<uintptr_t>(param_ptrs[i]) % pb)
             return afail(ZERO1_EALIGN, "tensor %zu is not aligned to its elements", i);
     }
-    if (const int rc = check_tensors_and_state(h, grad_ptrs, param_ptrs, master, m, v, scales)) return rc;
+    if (const int rc = check_tensors(h, grad_ptrs, param_ptrs, master, m, v, scales)) return rc;
     cudaError_t e;
-    try {
-        if (const int rc = check_overlap(h, grad_ptrs, param_ptrs)) return rc;
-    } catch (const std::bad_alloc &) {
-        return afail(ZERO1_ENOMEM, "host allocation failed");
-    }
     AdamwDeviceGuard g(h->device);
     const StepCall c{grad_ptrs, param_ptrs, master, m, v, scales, static_cast<cudaStream_t>(stream)};
     if (h->opt.param_dtype == ZERO1_DTYPE_BF16)

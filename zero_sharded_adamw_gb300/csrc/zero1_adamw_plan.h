@@ -77,4 +77,44 @@ inline size_t tensor_in_state(const ListTensors &t, const StateBuffer *state, in
     return t.count;
 }
 
+// A tensor's bytes, for shared_param.
+struct TensorRange {
+    uintptr_t from, to;
+    size_t tensor;
+    bool param;
+};
+
+// A parameter tensor that shares memory with another tensor of the call
+// (count: there is none): each is written by blocks that run in any order.
+// `ranges` is room for 2 count of them; nothing is allocated.
+inline size_t shared_param(const ListTensors &t, TensorRange *ranges)
+{
+    // parameters in the order of their addresses, gradients all before or all after them: nothing to sort
+    uintptr_t p_end = 0, p_begin = UINTPTR_MAX, g_begin = UINTPTR_MAX, g_end = 0;
+    bool ordered = true;
+    size_t n = 0;
+    for (size_t i = 0; i < t.count; ++i) {
+        if (t.sizes[i] == 0) continue;
+        const uintptr_t p = reinterpret_cast<uintptr_t>(t.params[i]), g = reinterpret_cast<uintptr_t>(t.grads[i]);
+        const uintptr_t p_to = p + t.sizes[i] * t.param_bytes, g_to = g + t.sizes[i] * t.grad_bytes;
+        ordered = ordered && p >= p_end;
+        p_begin = std::min(p_begin, p);
+        p_end = std::max(p_end, p_to);
+        g_begin = std::min(g_begin, g);
+        g_end = std::max(g_end, g_to);
+        ranges[n++] = {p, p_to, i, true};
+        ranges[n++] = {g, g_to, i, false};
+    }
+    if (ordered && (g_end <= p_begin || p_end <= g_begin)) return t.count;
+    std::sort(ranges, ranges + n, [](const TensorRange &a, const TensorRange &b) { return a.from < b.from; });
+    // the furthest end so far, of parameters and of anything
+    const TensorRange *any = nullptr, *param = nullptr;
+    for (const TensorRange *r = ranges; r != ranges + n; ++r) {
+        if ((r->param && any && any->to > r->from) || (param && param->to > r->from)) return r->param ? r->tensor : param->tensor;
+        if (!any || r->to > any->to) any = r;
+        if (r->param && (!param || r->to > param->to)) param = r;
+    }
+    return t.count;
+}
+
 }  // namespace zero1

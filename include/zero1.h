@@ -768,8 +768,8 @@ int zero1_ffn_workspace(const zero1_ffn_shape *shape, int backward, uint64_t *by
  *     be kept;
  *   errors: optional device word (NULL = none); bit 0 is set if a kernel
  *     wait gave up (1 s limit), in which case the outputs are not valid.
- * No output may share an entry with another buffer of the call, and no buffer
- * may lie in the workspace.  rows = 0 does nothing.  Asynchronous on `stream`;
+ * No output (the error word is one) may share an entry with another buffer of
+ * the call, and no buffer may lie in the workspace.  rows = 0 does nothing.  Asynchronous on `stream`;
  * allocates nothing; may be captured.
  * Errors: ZERO1_EINVAL, ZERO1_EALIGN, ZERO1_ECUDA. */
 int zero1_ffn_forward(const zero1_ffn_shape *shape, const void *x, const void *w_gate, const void *w_up,

@@ -835,6 +835,16 @@ def _ffn_workspace(workspace) -> tuple[int | None, int]:
     return workspace.data_ptr() or None, workspace.numel() * workspace.element_size()
 
 
+def _error_word(errors) -> int | None:
+    """Address of the optional 32-bit word a kernel sets, which a tensor has to hold in device memory."""
+    if errors is not None and hasattr(errors, "is_cuda"):
+        if not errors.is_cuda:
+            raise Zero1ArgumentError(f"errors: expected a CUDA tensor, got {errors.device}")
+        if errors.nbytes < 4:
+            raise Zero1ArgumentError(f"errors: {errors.nbytes} bytes, the call writes 4")
+    return _addr(errors)
+
+
 def zero1_ffn_workspace(shape: FfnShape, backward: bool = False) -> int:
     """Bytes of workspace a forward or backward call needs (host only, no device)."""
     b = C.c_uint64()
@@ -852,7 +862,7 @@ def zero1_ffn_forward(shape: FfnShape, x, w_gate, w_up, w_down, gate, up, h, y, 
         shape._ref, _take_matrix(x, mx, "x"), _take_matrix(w_gate, mg, "w_gate"), _take_matrix(w_up, mu, "w_up"),
         _take_matrix(w_down, md, "w_down"), None if gate is None else _take_matrix(gate, mh, "gate"),
         None if up is None else _take_matrix(up, mh, "up"), _take_matrix(h, mh, "h"), _take_matrix(y, my, "y"),
-        *_ffn_workspace(workspace), _addr(errors), _stream(stream))
+        *_ffn_workspace(workspace), _error_word(errors), _stream(stream))
     if rc:
         _check(rc)
 
@@ -866,7 +876,7 @@ def zero1_ffn_backward(shape: FfnShape, dy, x, w_gate, w_up, w_down, gate, up, h
         _take_matrix(w_up, mu, "w_up"), _take_matrix(w_down, md, "w_down"), _take_matrix(gate, mh, "gate"),
         _take_matrix(up, mh, "up"), _take_matrix(h, mh, "h"), None if dx is None else _take_matrix(dx, mx, "dx"),
         _take_matrix(dw_gate, mg, "dw_gate"), _take_matrix(dw_up, mu, "dw_up"), _take_matrix(dw_down, md, "dw_down"),
-        *_ffn_workspace(workspace), _addr(errors), _stream(stream))
+        *_ffn_workspace(workspace), _error_word(errors), _stream(stream))
     if rc:
         _check(rc)
 

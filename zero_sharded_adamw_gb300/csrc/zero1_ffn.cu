@@ -109,6 +109,17 @@ int check_mats(const zero1_ffn_shape &s, const Mat *m, int count)
     return ZERO1_OK;
 }
 
+// The error word shares no entry with a matrix.
+int check_errors(const unsigned *errors, const Mat *m, int count)
+{
+    if (!errors) return ZERO1_OK;
+    if (reinterpret_cast<uintptr_t>(errors) % 4) return ffail(ZERO1_EALIGN, "errors is not 4-byte aligned");
+    const Mat word{errors, 1, 2, 2, "errors", true};
+    for (int i = 0; i < count; ++i)
+        if (m[i].p && share(word, m[i])) return ffail(ZERO1_EINVAL, "errors and %s share memory", m[i].name);
+    return ZERO1_OK;
+}
+
 // ------------------------------------------------------------- workspace
 
 uint64_t round_up(uint64_t x, uint64_t a) { return (x + a - 1) / a * a; }
@@ -324,7 +335,8 @@ void run(Call &c, FfnParams &p, F f)
     c.launched = true;
 }
 
-int check_workspace(const zero1_ffn_shape &s, bool backward, const void *workspace, uint64_t bytes, const Mat *m, int count)
+int check_workspace(const zero1_ffn_shape &s, bool backward, const void *workspace, uint64_t bytes, const Mat *m, int count,
+                    const unsigned *errors)
 {
     const uint64_t need = workspace_of(s, backward);
     if (bytes < need) return ffail(ZERO1_EINVAL, "the workspace holds %llu bytes, the call needs %llu", (unsigned long long)bytes, (unsigned long long)need);
@@ -336,6 +348,8 @@ int check_workspace(const zero1_ffn_shape &s, bool backward, const void *workspa
         if (need && m[i].p && at < from + need && from < at + 2 * m[i].extent())
             return ffail(ZERO1_EINVAL, "%s lies in the workspace", m[i].name);
     }
+    const uintptr_t word = reinterpret_cast<uintptr_t>(errors);
+    if (word && word < from + need && from < word + 4) return ffail(ZERO1_EINVAL, "errors lies in the workspace");
     return ZERO1_OK;
 }
 
@@ -364,7 +378,6 @@ int zero1_ffn_forward(const zero1_ffn_shape *shape, const void *x, const void *w
     if (s.rows == 0) return ZERO1_OK;
     if (!x || !w_gate || !w_up || !w_down || !h || !y) return ffail(ZERO1_EINVAL, "NULL pointer argument");
     if ((gate == nullptr) != (up == nullptr)) return ffail(ZERO1_EINVAL, "gate and up are kept together, or neither");
-    if (reinterpret_cast<uintptr_t>(errors) % 4) return ffail(ZERO1_EALIGN, "errors is not 4-byte aligned");
     const Mat mats[8] = {{x, s.rows, s.width, s.ldx, "x", false},
                          {w_gate, s.width, s.hidden, s.ld_gate, "w_gate", false},
                          {w_up, s.width, s.hidden, s.ld_up, "w_up", false},
@@ -374,7 +387,8 @@ int zero1_ffn_forward(const zero1_ffn_shape *shape, const void *x, const void *w
                          {gate, s.rows, s.hidden, s.ldh, "gate", true},
                          {up, s.rows, s.hidden, s.ldh, "up", true}};
     if (const int rc = check_mats(s, mats, 8)) return rc;
-    if (const int rc = check_workspace(s, false, workspace, workspace_bytes, mats, 8)) return rc;
+    if (const int rc = check_errors(errors, mats, 8)) return rc;
+    if (const int rc = check_workspace(s, false, workspace, workspace_bytes, mats, 8, errors)) return rc;
     Call c(s, workspace, errors, stream);
     if (c.rc) return c.rc;
 
@@ -469,9 +483,9 @@ int zero1_ffn_backward(const zero1_ffn_shape *shape, const void *dy, const void 
         return ZERO1_OK;
     }
     if (!dy || !x || !w_gate || !w_up || !w_down || !gate || !up || !h) return ffail(ZERO1_EINVAL, "NULL pointer argument");
-    if (reinterpret_cast<uintptr_t>(errors) % 4) return ffail(ZERO1_EALIGN, "errors is not 4-byte aligned");
     if (const int rc = check_mats(s, mats, 12)) return rc;
-    if (const int rc = check_workspace(s, true, workspace, workspace_bytes, mats, 12)) return rc;
+    if (const int rc = check_errors(errors, mats, 12)) return rc;
+    if (const int rc = check_workspace(s, true, workspace, workspace_bytes, mats, 12, errors)) return rc;
     Call c(s, workspace, errors, stream);
     if (c.rc) return c.rc;
 

@@ -769,6 +769,13 @@ def zero1_layernorm_backward(rows: int, cols: int, dtype: int, dy, lddy: int, x,
 ACT_SILU, ACT_GELU, ACT_GELU_TANH, ACT_RELU = 0, 1, 2, 3
 
 
+def _int32(v: int, what: str) -> int:
+    """`v`, which C fields of 32 bits would otherwise cut off."""
+    if not -(1 << 31) <= v < 1 << 31:
+        raise Zero1ArgumentError(f"{what}: {v} is out of range")
+    return v
+
+
 class _CFfnShape(C.Structure):
     _fields_ = [("size", C.c_uint32), ("activation", C.c_int32)] + \
                [(k, C.c_uint64) for k in ("rows", "width", "hidden", "ldx", "ldy", "ldh", "ld_gate", "ld_up", "ld_down")] + \
@@ -797,8 +804,8 @@ class FfnShape:
         for k in ("rows", "width", "hidden", "ldx", "ldy", "ldh", "ld_gate", "ld_up", "ld_down"):
             if not 0 <= getattr(self, k) < 1 << 63:
                 raise Zero1ArgumentError(f"{k}: {getattr(self, k)} is out of range")
-        c = _CFfnShape(C.sizeof(_CFfnShape), self.activation, self.rows, self.width, self.hidden, self.ldx, self.ldy,
-                       self.ldh, self.ld_gate, self.ld_up, self.ld_down, int(self.unaligned),
+        c = _CFfnShape(C.sizeof(_CFfnShape), _int32(self.activation, "activation"), self.rows, self.width, self.hidden,
+                       self.ldx, self.ldy, self.ldh, self.ld_gate, self.ld_up, self.ld_down, int(self.unaligned),
                        int(self.inject_wait_timeout))
         r, w, h = self.rows, self.width, self.hidden
         # (rows, columns, stride, shape, strides) of x, y, h, w_gate, w_up and w_down, for the checks of every call
@@ -901,8 +908,8 @@ class AdamWOptions:
     def _c(self) -> _CAdamWOptions:
         if not 0 <= self.seed < 1 << 64:
             raise Zero1ArgumentError(f"seed: {self.seed} is not an unsigned 64-bit number")
-        return _CAdamWOptions(C.sizeof(_CAdamWOptions), self.state_bits, self.param_dtype, self.grad_dtype,
-                              int(self.decay_before_update), 0, self.seed)
+        ints = [_int32(getattr(self, k), k) for k in ("state_bits", "param_dtype", "grad_dtype")]
+        return _CAdamWOptions(C.sizeof(_CAdamWOptions), *ints, int(self.decay_before_update), 0, self.seed)
 
 
 # (sizes, a copy of the options, entries of the state) of every list handle this binding created.
@@ -980,6 +987,8 @@ def zero1_adamw_moments(h: int, m, v, scales, m_out=None, v_out=None, stream=Non
 
 
 def zero1_adamw_set_steps(h: int, t: int, stream=None) -> None:
+    if not 0 <= t < 1 << 64:
+        raise Zero1ArgumentError(f"steps: {t} is not an unsigned 64-bit number")
     _check(_load().zero1_adamw_set_steps(h, t, _stream(stream)))
 
 

@@ -812,10 +812,14 @@ int zero1_ffn_backward(const zero1_ffn_shape *shape, const void *dy, const void 
  * and its block's scales are M/61439 and R/63487 (0 for a block whose largest
  * value is below 2^-100: it is held as zeros).  Codes are rounded up or down
  * at random with the exact value as their mean, by a hash of `seed`, the step
- * and the entry's place: the same inputs give the same bits.  A block with an
- * infinity or a NaN among its new m (or v) has a NaN scale, and its m (or v)
- * stand for NaN; other blocks are not touched by it (clipping, whose norm is then infinite
- * or NaN, turns the whole list NaN or holds it, as zero1_step does).
+ * and the entry's place: the same inputs give the same bits.  That holds for m
+ * and for sqrt(v) (which gets no zero code unless it is zero); v itself gains
+ * the variance of its root's rounding and comes out high, by 0.6% at beta2 =
+ * 0.95 and by 2 to 3% at 0.999 (gradients drawn anew in every step), so updates
+ * are smaller by half of that.  A block with an infinity or a NaN among its new
+ * m (or v) has a NaN scale, and its m (or v) stand for NaN; other blocks are
+ * not touched by it (clipping, whose norm is then infinite or NaN, turns the
+ * whole list NaN or holds it, as zero1_step does).
  *   state_bits: 8 or 32;
  *   param_dtype, grad_dtype: ZERO1_DTYPE_BF16 or ZERO1_DTYPE_F32;
  *   decay_before_update: as zero1_options;

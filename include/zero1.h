@@ -714,7 +714,8 @@ int zero1_layernorm_backward(uint64_t rows, uint64_t cols, int dtype, const void
  * Wg and Wu may be column slices of one matrix.  Both projections, the
  * activation and the product are one kernel.  Sums are fp32; h (of more than
  * 16 rows), and in the backward pass dgate and dup, are rounded to bf16 once,
- * as they are the next products' operands.  The sums' order of a forward pass
+ * as they are the next products' operands.  Of at most 16 rows h goes on as two
+ * bf16 parts; an infinity in Wd then gives NaN, as it meets a part that is 0.  The sums' order of a forward pass
  * of at most 128 rows goes by the SMs that the stream may use
  * (zero1_sm_partition), all others' by the shape alone.
  *   activation: g sigmoid(g) (SILU), g Phi(g) (GELU, Phi the normal

@@ -8,7 +8,7 @@ namespace zero1 {
 
 // act(g), and its derivative, in fp32.  The sigmoid from the approximate
 // exponential and quotient: 2e-6 of itself at |g| = 20, a thousandth of a
-// bf16 rounding.
+// bf16 rounding; 0 where it is below fp32's normal range (g < -87.3).
 __device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
 
 constexpr float kDensity = 0.39894228040143268f;                                     // 1/sqrt(2 pi)

@@ -715,9 +715,9 @@ int zero1_layernorm_backward(uint64_t rows, uint64_t cols, int dtype, const void
  * activation and the product are one kernel.  Sums are fp32; h (of more than
  * 16 rows), and in the backward pass dgate and dup, are rounded to bf16 once,
  * as they are the next products' operands.  Of at most 16 rows h goes on as two
- * bf16 parts; an infinity in Wd then gives NaN, as it meets a part that is 0.  The sums' order of a forward pass
- * of at most 128 rows goes by the SMs that the stream may use
- * (zero1_sm_partition), all others' by the shape alone.
+ * bf16 parts; an infinity in Wd then gives NaN, as it meets a part that is 0.
+ * The sums' order of a forward pass of at most 128 rows goes by the SMs that
+ * the stream may use (zero1_sm_partition), all others' by the shape alone.
  *   activation: g sigmoid(g) (SILU), g Phi(g) (GELU, Phi the normal
  *     distribution function), the latter's tanh form (GELU_TANH), or
  *     max(g, 0) (RELU, NaN stays NaN);
@@ -770,8 +770,8 @@ int zero1_ffn_workspace(const zero1_ffn_shape *shape, int backward, uint64_t *by
  *   errors: optional device word (NULL = none); bit 0 is set if a kernel
  *     wait gave up (1 s limit), in which case the outputs are not valid.
  * No output (the error word is one) may share an entry with another buffer of
- * the call, and no buffer may lie in the workspace.  rows = 0 does nothing.  Asynchronous on `stream`;
- * allocates nothing; may be captured.
+ * the call, and no buffer may lie in the workspace.  rows = 0 does nothing.
+ * Asynchronous on `stream`; allocates nothing; may be captured.
  * Errors: ZERO1_EINVAL, ZERO1_EALIGN, ZERO1_ECUDA. */
 int zero1_ffn_forward(const zero1_ffn_shape *shape, const void *x, const void *w_gate, const void *w_up,
                       const void *w_down, void *gate, void *up, void *h, void *y, void *workspace,

@@ -24,17 +24,17 @@
 //
 // Every fp32 operation is rounded by itself (no fma), so master, parameters
 // and codes are those of the written formulas bit for bit (but for the sign of
-// a zero: a lane whose m and v are all zero moves by +0 where m is -0).  The norm's sum
-// of squares is compensated in fp32 (each square and each addition with its
-// error) and then fp64, so that the fp32 clip coefficient is its correct
-// rounding but for values within 1e-12 of a tie.
+// a zero: a lane whose m and v are all zero moves by +0 where m is -0).  The
+// norm's sum of squares is compensated in fp32 (each square and each addition
+// with its error) and then fp64, so that the fp32 clip coefficient is its
+// correct rounding but for values within 1e-12 of a tie.
 //
 // Measured on the GPT-2-small list (98 tensors, 124 million entries, bf16):
 // norm 62 us (4.0 TB/s; half the issue slots, its loads and its arithmetic
 // take turns), update with fp32 moments 505 us (28 bytes an entry at 6.9 TB/s,
-// bound by HBM: a plain copy moves 6.7), with 8 bits 360 us (16 bytes at 5.5 TB/s; 81% of the issue
-// slots busy, 90 instructions an entry), reading 8-bit moments out 190 us (6.5
-// TB/s).  4,096 entries in one launch: 9.5 us, all latency.
+// bound by HBM: a plain copy moves 6.7), with 8 bits 360 us (16 bytes at 5.5
+// TB/s; 81% of the issue slots busy, 90 instructions an entry), reading 8-bit
+// moments out 190 us (6.5 TB/s).  4,096 entries in one launch: 9.5 us, all latency.
 #include <cuda_runtime.h>
 
 #include <algorithm>

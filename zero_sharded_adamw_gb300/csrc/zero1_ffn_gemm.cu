@@ -30,7 +30,7 @@ constexpr uint32_t kWarpTurn = 4096;                // 32 rows x 32 fp32 of an e
 // Eight epilogue warps have registers for what is in flight (16,384 x 768 x
 // 2048: dh's product in 67 us, 76 with sixteen; 8,192 x 4096 x 11008 backward
 // 2.77 ms, 2.86).  Sixteen finish one tile sooner, where no pair has another
-// to go on with (2,000 x 256 x 688 backward in 37 us, 41 with eight).
+// to go on with (2,000 x 256 x 688 backward in 35 us, 37 with eight).
 template <int WARPS>
 struct Gemm {
     static constexpr int kThreads = 64 + 32 * WARPS;

@@ -26,7 +26,7 @@ def test_steps(bad):
         z.zero1_adamw_set_steps(12345, bad)
 
 
-def test_numbers_that_fit_are_the_librarys_to_judge():
+def test_numbers_that_fit_reach_the_library():
     for bad in (4, -1, (1 << 31) - 1, -(1 << 31)):
         with pytest.raises(z.Zero1Error, match="unknown activation"):
             z.zero1_ffn_workspace(z.FfnShape(4, 16, 32, bad))
